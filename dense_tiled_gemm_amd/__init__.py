@@ -20,7 +20,10 @@ Entry points (same names as the C-ABI in ``include/gemm_bt.h``):
   gemm_bt_workspace_size(M, N, K, in_dtype, out_dtype), gemm_bt_plan_ws(M, N, K, in_dtype, out_dtype, ...)
   gemm_bt_noalloc(A, B, C, M, N, K, in_dtype, out_dtype, stream)   gemm_bt_ws with the library's scratch
 and torch convenience wrappers ``mm_bt(a, b, out_dtype)`` (2-D or batched 3-D operands),
-``mm_layout(a, b, a_layout, b_layout, out_dtype)`` and ``mm(a, b, out_dtype)`` (= a @ b).
+``mm_layout(a, b, a_layout, b_layout, out_dtype)`` and ``mm(a, b, out_dtype)`` (= a @ b).  The operators around the
+product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_backward, gemm_bt_act_backward) are
+called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
+``add_rms_norm_backward`` and ``quantize_rows``, which need torch and are imported when first used.
 """
 from __future__ import annotations
 
@@ -38,7 +41,9 @@ LIB_PATH = os.environ.get("GEMM_BT_LIB") or os.path.join(_HERE, "libgemm_bt.so")
 EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layout", "gemm_bt_status_string",
            "gemm_bt_version", "gemm_bt_plan", "gemm_bt_plan_batched", "gemm_bt_plan_layout",
            "gemm_bt_plan_batched_layout", "gemm_bt_tile_coord", "gemm_bt_ws", "gemm_bt_workspace_size",
-           "gemm_bt_plan_ws", "gemm_bt_noalloc")
+           "gemm_bt_plan_ws", "gemm_bt_noalloc", "gemm_bt_epi", "gemm_bt_rms_norm", "gemm_bt_rms_norm_backward",
+           "gemm_bt_rms_norm_backward_workspace", "gemm_bt_quantize_rows", "gemm_bt_act_backward",
+           "gemm_bt_act_backward_workspace")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -107,6 +112,18 @@ def load():
             lib.gemm_bt_plan_ws.restype = ci
             lib.gemm_bt_noalloc.argtypes = [vp, vp, vp, i64, i64, i64, ci, ci, vp]
             lib.gemm_bt_noalloc.restype = ci
+            sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+            lib.gemm_bt_epi.argtypes = [vp, vp, vp, i64, i64, i64, ci, ci, vp, vp, sz, vp]
+            lib.gemm_bt_rms_norm.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ci, ci, ci, vp]
+            lib.gemm_bt_quantize_rows.argtypes = [vp, i64, vp, vp, i64, i64, ci, ci, vp]
+            lib.gemm_bt_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, ci, ci, vp, sz, vp]
+            lib.gemm_bt_rms_norm_backward_workspace.argtypes = [i64, i64, szp]
+            lib.gemm_bt_act_backward.argtypes = [vp, vp, vp, vp, i64, i64, ci, ci, ci, ci, vp, sz, vp]
+            lib.gemm_bt_act_backward_workspace.argtypes = [i64, i64, szp]
+            for f in (lib.gemm_bt_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
+                      lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
+                      lib.gemm_bt_act_backward_workspace):
+                f.restype = ci
             _lib = lib
     return _lib
 
@@ -386,3 +403,17 @@ def mm(a, b, out_dtype=None, out=None, stream=None):
     """C = a @ b for 16-bit tensors a (M,K) and b (K,N), or batches of them (Z,M,K) and (Z,K,N): B is read
     K-outer, as it lies in memory."""
     return mm_layout(a, b, K_INNER, K_OUTER, out_dtype, out, stream)
+
+
+_LAYERS = ("linear", "linear_backward", "add_rms_norm", "add_rms_norm_backward", "quantize_rows")
+
+
+def __getattr__(name):
+    # the wrappers of `layers` import torch, which this module otherwise does only when a wrapper is called
+    if name in _LAYERS:
+        from . import layers
+
+        for n in _LAYERS:
+            globals()[n] = getattr(layers, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,7 +18,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # keep the compiler from forming packed-fp32 VALU ops (v_pk_*_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # MFMAs read and write their accumulators in VGPRs.  For a 256-thread
@@ -31,16 +32,25 @@ FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, "gemm_bt.hip")]
+    return [os.path.join(CSRC, name) for name in ("gemm_bt.hip", "gemm_epi.hip", "norm.hip")]
 
 
 def build(extra=None, out=SO, verbose=False) -> str:
+    """Compile every source (side by side) into an object file in a folder of its own, then link them into `out`."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC] + list(extra or []) \
-        + sources() + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory(prefix="gemm_bt_build") as folder:
+        def compile_one(src):
+            obj = os.path.join(folder, os.path.basename(src) + ".o")
+            cmd = [HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC] + list(extra or []) \
+                + ["-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            subprocess.run(cmd, check=True)
+            return obj
+
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            objects = list(pool.map(compile_one, sources()))
+        subprocess.run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared"] + objects + ["-o", tmp], check=True)
     os.replace(tmp, out)
     return out
 

@@ -32,6 +32,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace gbt {
 
@@ -172,14 +173,20 @@ struct SkArgs {
     unsigned* counters;  // one arrival counter per tile, zero between calls
     float* partials;     // one slot of BM * BN floats per workgroup
 };
+// EPI = 1: the same kernel with an epilogue (epilogue.hpp) between the sums
+// and C; its arguments travel with the split's.
+struct SkEpiArgs : SkArgs {
+    EpiArgs epi;
+};
 
 template <int IN, int OUT, int BM, int BN, int BK, int STAGES, int WM, int WN, int SWZ, int SCHED = 0, int PF = 0,
-          int MF = 32, int LDW = 0, int RING5 = 0, int SK = 0, int PH = 0>
+          int MF = 32, int LDW = 0, int RING5 = 0, int SK = 0, int PH = 0, int EPI = 0>
 __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
                                                           void* __restrict__ C, int M, int N, int K,
                                                           int tiles_m, int tiles_n, int group_m,
                                                           int vec_store, int item_tiles_m, long long sa, long long sb,
-                                                          long long sc, const SkArgs sk) {
+                                                          long long sc,
+                                                          const std::conditional_t<EPI, SkEpiArgs, SkArgs> sk) {
     constexpr int W = WM * WN;
     constexpr int ESZ = in_size(IN);     // bytes per input element (2, or 1 for 8-bit floats)
     constexpr int EPC = 16 / ESZ;        // elements per 16-byte chunk
@@ -781,7 +788,12 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     auto store_c = [&](void* Cp, int m0, int n0, Acc& acc) {
         int tid_r = threadIdx.x;
         asm volatile("" : "+v"(tid_r));
-        if constexpr (!WHOLE_ROWS) {
+        if constexpr (EPI) {
+            // every wave is past its last LDS read and its loads have landed
+            barrier_no_fence();
+            store_tile_epi<IN == GEMM_BT_INT8, FN, FM, BM, BN, WM, 64 * W, STAGES * STAGE_BYTES, MF>(
+                acc, lds, Cp, M, N, m0, n0, wm * TM, wn * TN, wm, tid_r, sk.epi);
+        } else if constexpr (!WHOLE_ROWS) {
             store_tile<store_type(OUT), FN, FM, MF>(acc, Cp, M, N, m0, n0, wm * TM, wn * TN, tid_r & 63, vec_store);
         } else {
             // every wave is past its last LDS read and its loads have landed

@@ -8,7 +8,9 @@
 #include <cstring>
 
 #include "common.hpp"
+#include "device.hpp"
 #include "dma_kernel.hpp"
+#include "epi_kernels.hpp"
 #include "skinny_dma.hpp"
 #ifdef GEMM_BT_TUNING
 // measured alternatives: register streaming for M <= 16, register-staged
@@ -895,7 +897,7 @@ constexpr int kMaxDev = 64;
 static std::atomic<int> g_dev_state[kMaxDev];  // 0 unknown, 1 gfx950, 2 other
 static std::atomic<int> g_dev_cus[kMaxDev];
 
-static int check_device(int* num_cu) {
+int check_device(int* num_cu) {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
         (void)hipGetLastError();
@@ -974,7 +976,7 @@ static int check_items(const void* A, const void* B, const void* C, int kind, in
 // CU count the plans are made for: the current device's when it is a
 // gfx950, else 256 (an MI355X), so that a plan taken on the host describes the
 // launch on the device that is present.
-static int plan_cus() {
+int plan_cus() {
     int n = 256;
     return check_device(&n) == GEMM_BT_OK ? n : 256;
 }
@@ -998,12 +1000,12 @@ static SkArgs sk_args(const gemm_bt_plan_t& p, int64_t K, void* ws) {
 // the data-parallel grid as gemm_bt does.
 static int launch_inner(const void* A, const void* B, void* C, int64_t batch, int64_t M, int64_t N, int64_t K,
                         int64_t stride_a, int64_t stride_b, int64_t stride_c, int in_dtype, int out_dtype, void* ws,
-                        size_t ws_bytes, void* stream) {
+                        size_t ws_bytes, void* stream, const EpiArgs* epi = nullptr) {
     gemm_bt_plan_t p;
     if (stride_a < 0 || stride_b < 0 || stride_c < 0) return GEMM_BT_ERR_INVALID_VALUE;
     const bool multi = batch > 1;
     const int isz = is_8bit(in_dtype) ? 1 : 2;
-    const int osz = out_size(out_dtype);
+    const int osz = epi ? elem_size(epi_type(epi->mode, EPI_OUT_TYPE)) : out_size(out_dtype);  // bytes per element of C
     const int a_al = item_align(A, batch, stride_a, isz), b_al = item_align(B, batch, stride_b, isz),
               c_al = item_align(C, batch, stride_c, osz);
     const bool allow_sk = ws != nullptr;
@@ -1029,10 +1031,12 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         // two launches in stream order: rows [0, m1), then the rest (each
         // with its own plan; the second may use the workspace)
         const int64_t m1 = p.split_rows;
-        st = launch_inner(A, B, C, 1, m1, N, K, 0, 0, 0, in_dtype, out_dtype, ws, ws_bytes, stream);
+        st = launch_inner(A, B, C, 1, m1, N, K, 0, 0, 0, in_dtype, out_dtype, ws, ws_bytes, stream, epi);
         if (st != GEMM_BT_OK) return st;
+        EpiArgs rest;
+        if (epi) rest = epi_rows(*epi, m1, N);
         return launch_inner((const char*)A + m1 * K * isz, B, (char*)C + m1 * N * osz, 1, M - m1, N, K, 0, 0, 0,
-                            in_dtype, out_dtype, ws, ws_bytes, stream);
+                            in_dtype, out_dtype, ws, ws_bytes, stream, epi ? &rest : nullptr);
     }
     if (p.split_items > 0) {
         // items [0, z1), then the rest, in stream order (a stride of 0
@@ -1056,7 +1060,12 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         u16* c16 = (u16*)C;
         size_t n16 = (size_t)M * (size_t)N * osz / 2;
         void* args[] = {&c16, &n16, &sc};
-        e = hipLaunchKernel((const void*)&zero_fill_kernel, dim3((unsigned)p.grid, gy), dim3(p.threads), args, 0, s);
+        if (epi) {
+            EpiArgs ea = *epi;
+            void* eargs[] = {&C, &Mi, &Ni, &ea};
+            e = hipLaunchKernel(epi_fill_fn(), dim3((unsigned)p.grid), dim3(p.threads), eargs, 0, s);
+        } else
+            e = hipLaunchKernel((const void*)&zero_fill_kernel, dim3((unsigned)p.grid, gy), dim3(p.threads), args, 0, s);
     } else {
         const u16* a = (const u16*)A;
         const u16* b = (const u16*)B;
@@ -1067,10 +1076,13 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         if (vec_store && (N * osz) % 16 == 0 && c_al >= 16) vec_store = 2;
         if (p.kernel == KIND_DMA) {
             int n = 0;
-            const void* fn = p.split_tiles > 0 ? sk_fn(p.variant, in_dtype, out_dtype)
-                                               : dma_variants(&n)[p.variant].fn[in_index(in_dtype)][out_index(out_dtype)];
+            const void* fn = epi ? epi_dma_fn(p.variant, in_dtype, p.split_tiles > 0)
+                             : p.split_tiles > 0 ? sk_fn(p.variant, in_dtype, out_dtype)
+                                                 : dma_variants(&n)[p.variant].fn[in_index(in_dtype)][out_index(out_dtype)];
             if (!fn) return GEMM_BT_ERR_UNSUPPORTED;  // no kernel of this plan in this build
-            SkArgs ska = sk_args(p, K, ws);
+            SkEpiArgs ska;  // a kernel without an epilogue takes its first part
+            (SkArgs&)ska = sk_args(p, K, ws);
+            if (epi) ska.epi = *epi;
             // one grid row: the items stacked along the tile rows (stream-K: the persistent grid)
             int tm = (int)(p.tiles_m * batch), tn = (int)p.tiles_n, gm = p.group_m, itm = (int)p.tiles_m;
             const unsigned gx = (unsigned)(p.split_tiles > 0 ? p.grid : p.grid * batch);
@@ -1086,7 +1098,9 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
 #endif
         } else {
             const void* fn = nullptr;
-            if (p.variant >= 1) {
+            if (epi) {
+                fn = epi_skinny_fn(in_dtype);
+            } else if (p.variant >= 1) {
                 int n = 0;
                 fn = skinny_variants(&n)[p.variant - 1].fn[in_index(in_dtype)][out_index(out_dtype)];
             } else {
@@ -1096,7 +1110,10 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
 #endif
             }
             if (!fn) return GEMM_BT_ERR_UNSUPPORTED;  // no kernel of this plan in this build
+            EpiArgs ea;
+            if (epi) ea = *epi;
             void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &vec_store, &sa, &sb, &sc};
+            if (epi) args[6] = &ea;
             e = hipLaunchKernel(fn, dim3((unsigned)p.grid, gy), dim3(p.threads), args, 0, s);
         }
     }
@@ -1240,6 +1257,40 @@ int gemm_bt_batched(const void* A, const void* B, void* C, int64_t batch, int64_
 int gemm_bt_ws(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype,
                void* workspace, size_t workspace_bytes, void* stream) {
     return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, out_dtype, workspace, workspace_bytes, stream);
+}
+
+int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype,
+                const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream) {
+    auto float_type = [](int t) { return t == GEMM_BT_F32 || t == GEMM_BT_F16 || t == GEMM_BT_BF16; };
+    if (!float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    EpiArgs e = {nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype << EPI_OUT_TYPE};
+    if (epilogue) {
+        const gemm_bt_epilogue_t& g = *epilogue;
+        if (g.activation < GEMM_BT_ACT_NONE || g.activation > GEMM_BT_ACT_SILU) return GEMM_BT_ERR_INVALID_VALUE;
+        e.row_scale = g.row_scale;
+        e.col_scale = g.col_scale;
+        e.bias = g.bias;
+        e.residual = g.residual;
+        e.preact = g.preact;
+        e.mode |= g.activation << EPI_ACT;
+        // a term that is there: its bit and its type
+        auto term = [&](const void* ptr, int bit, int type, int shift) {
+            if (!ptr) return true;
+            if (!float_type(type) || (uintptr_t)ptr % elem_size(type)) return false;
+            e.mode |= bit | type << shift;
+            return true;
+        };
+        if (!term(g.row_scale, EPI_ROW_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) ||
+            !term(g.col_scale, EPI_COL_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) ||
+            !term(g.bias, EPI_BIAS, g.bias_dtype, EPI_BIAS_TYPE) ||
+            !term(g.residual, EPI_RESIDUAL, g.residual_dtype, EPI_RESIDUAL_TYPE) ||
+            !term(g.preact, EPI_PREACT, g.preact_dtype, EPI_PREACT_TYPE))
+            return GEMM_BT_ERR_INVALID_VALUE;
+    }
+    static_assert(GEMM_BT_F32 == 0, "the scales' type adds no bits");
+    // an int8 product is planned as the one with int32 sums (4 bytes per output, what any float type fits in)
+    const int plan_out = in_dtype == GEMM_BT_INT8 ? GEMM_BT_INT32 : out_dtype;
+    return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, plan_out, workspace, workspace_bytes, stream, &e);
 }
 
 int gemm_bt_noalloc(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,

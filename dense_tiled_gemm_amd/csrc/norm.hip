@@ -1,0 +1,819 @@
+// norm.hip -- the row operators next to the product: root-mean-square norm
+// with the residual's addition, out in 16 or 32 bits or in 8 bits with one
+// scale per row; 8-bit rows with scales of a matrix as it is; the norm's
+// backward pass; and the backward pass of an epilogue's activation and bias.
+//
+// All of them are bound by HBM: each reads its inputs once and writes its
+// outputs once.  A row is read into registers (8 elements per thread and
+// chunk), every statistic is taken from there, and the row leaves from there.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "epilogue.hpp"
+
+namespace gbt {
+
+// ---- reductions ----------------------------------------------------------------
+
+struct SumOp {
+    __device__ static float zero() { return 0.0f; }
+    __device__ static float join(float a, float b) { return a + b; }
+};
+// largest of the bits of |v|: for finite values the largest magnitude, and
+// above every finite value once one of them is infinite or NaN
+struct MaxBitsOp {
+    __device__ static float zero() { return 0.0f; }
+    __device__ static float join(float a, float b) { return as_f32(max(as_u32(a), as_u32(b))); }
+};
+
+// The value joined over the T threads of a row (T = 64: one wave; else the
+// whole workgroup, through `part`), the same for all of them and in an order
+// that depends on T only.
+template <class Op, int T>
+__device__ __forceinline__ float row_join(float v, float* part) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v = Op::join(v, __shfl_xor(v, m));
+    if constexpr (T > 64) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) part[wave] = v;
+        __syncthreads();
+        v = Op::zero();
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w) v = Op::join(v, part[w]);
+    }
+    return v;
+}
+
+// ---- 8-bit codes ---------------------------------------------------------------
+
+typedef u32x2 u32x2_byte __attribute__((aligned(1)));
+
+// Four values (|v| <= 448 or 127 up to rounding, or NaN) in 8 bits, to nearest even.
+template <int QT>
+__device__ __forceinline__ u32 quant4(float a, float b, float c, float d) {
+    if constexpr (QT == GEMM_BT_FP8_E4M3) {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    } else {
+        // NaN becomes 0 in the conversion to an integer
+        auto code = [](float v) { return (u32)(int)__builtin_fminf(__builtin_fmaxf(__builtin_rintf(v), -127.0f), 127.0f) & 255u; };
+        return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
+    }
+}
+__device__ __forceinline__ void store_codes(void* p, int qt, size_t i, int n, const float (&v)[8]) {
+    u32x2 w;
+    if (qt == GEMM_BT_FP8_E4M3)
+        w = u32x2{quant4<GEMM_BT_FP8_E4M3>(v[0], v[1], v[2], v[3]), quant4<GEMM_BT_FP8_E4M3>(v[4], v[5], v[6], v[7])};
+    else
+        w = u32x2{quant4<GEMM_BT_INT8>(v[0], v[1], v[2], v[3]), quant4<GEMM_BT_INT8>(v[4], v[5], v[6], v[7])};
+    unsigned char* s = (unsigned char*)p + i;
+    if (n >= 8) {
+        __builtin_nontemporal_store(w, (u32x2_byte*)s);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n) s[e] = (unsigned char)(w[e >> 2] >> (8 * (e & 3)));
+    }
+}
+
+// A row's scale, from the bits of its largest magnitude: amax / 448 (E4M3) or
+// amax / 127 (int8), kept above 2^-100 so that its reciprocal is finite; NaN
+// for a row that holds an infinity or a NaN.
+__device__ __forceinline__ float row_scale_of(float amax, int qt) {
+    if (as_u32(amax) >= 0x7F800000u) return as_f32(0x7FC00000u);
+    return __builtin_fmaxf(amax / (qt == GEMM_BT_FP8_E4M3 ? 448.0f : 127.0f), 0x1p-100f);
+}
+
+// ---- norm and quantisation, forward ----------------------------------------------
+
+// 1 / sqrt(ss / d + eps) of a row whose squares sum to ss in fp32.  Where that
+// sum left fp32's range (|h| above 2^64 / sqrt d, or below 2^-45 with next to
+// no eps) the squares are summed once more, of the row scaled by a power of
+// two that brings its largest magnitude near 1.  each(f) calls f on every
+// value of h that the thread holds; `part` has two more rows for the joins.
+// An infinity gives 0, a NaN NaN.
+template <int T, class Each>
+__device__ __forceinline__ float rstd_of(float ss, int d, float eps, float (*part)[16], int flip, Each&& each) {
+    const float mean = ss / (float)d + eps;
+    if (__builtin_expect(!(mean > 0x1p-90f && mean < __builtin_inff()), 0)) {
+        float amax = 0.0f;
+        each([&](float v) __attribute__((always_inline)) { amax = MaxBitsOp::join(amax, __builtin_fabsf(v)); });
+        amax = row_join<MaxBitsOp, T>(amax, part[flip]);
+        if (amax > 0.0f && amax < __builtin_inff()) {
+            const float s = as_f32((254u - min(as_u32(amax) >> 23, 253u)) << 23);
+            float sq = 0.0f;
+            each([&](float v) __attribute__((always_inline)) { sq = __builtin_fmaf(v * s, v * s, sq); });
+            sq = row_join<SumOp, T>(sq, part[2 + flip]);
+            const float e = eps * s * s;
+            return e < __builtin_inff() ? s / __builtin_sqrtf(sq / (float)d + e) : 1.0f / __builtin_sqrtf(eps);
+        }
+    }
+    return 1.0f / __builtin_sqrtf(mean);
+}
+
+struct NormArgs {
+    const void* x;
+    const void* residual;  // nullptr: none
+    const void* weight;    // nullptr: the rows as they are (quantisation alone)
+    void* y;
+    void* h;               // x + residual rounded, nullptr: not kept
+    float* scale;          // 8-bit y
+    float* rstd;           // nullptr: not kept
+    long long rows, ldx, ldr;
+    int d;
+    float eps;
+    int y_type;
+};
+
+__device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
+
+// T threads hold one row, U chunks of 8 elements each (T * U * 8 >= d); a
+// workgroup of NT threads works on NT / T rows at a time.
+template <int XT, int WT, int T, int U, int NT>
+__global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
+    static_assert(T == NT || T == 64, "a row belongs to a wave or to the workgroup");
+    constexpr int RB = NT / T;
+    __shared__ float part[8][16];
+    const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int d = a.d;
+    int flip = 0;
+    for (long long row = (long long)blockIdx.x * RB + threadIdx.x / T; row < a.rows; row += (long long)gridDim.x * RB) {
+        Raw8 xr[U], rr[U], wr[U];
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                const int n = min(8, d - i);
+                xr[u] = load_raw8(a.x, XT, (size_t)(row * a.ldx) + i, n);
+                if (a.residual) rr[u] = load_raw8(a.residual, XT, (size_t)(row * a.ldr) + i, n);
+                if (a.weight) wr[u] = load_raw8(a.weight, WT, (size_t)i, n);
+            }
+        });
+        float h[U][8], ss = 0.0f;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                decode8(xr[u], XT, h[u]);
+                if (a.residual) {
+                    float v[8];
+                    decode8(rr[u], XT, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[u][e] += v[e];
+                }
+                if (a.h) store8(a.h, XT, (size_t)(row * d) + i, min(8, d - i), h[u]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[u][e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[u][e], h[u][e], ss);
+        });
+        float rstd = 1.0f;
+        if (a.weight) {
+            ss = row_join<SumOp, T>(ss, part[flip]);
+            rstd = rstd_of<T>(ss, d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f(h[u][e]);
+            });
+            if (a.rstd && t == 0) a.rstd[row] = rstd;
+        }
+        float amax = 0.0f;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                if (a.weight) {
+                    float w[8];
+                    decode8(wr[u], WT, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * rstd * w[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[u][e]));
+                if (!is_code_type(a.y_type)) store8(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
+            }
+        });
+        if (is_code_type(a.y_type)) {
+            amax = row_join<MaxBitsOp, T>(amax, part[2 + flip]);
+            const float s = row_scale_of(amax, a.y_type), inv = 1.0f / s;
+            if (t == 0) a.scale[row] = s;
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int i = (u * T + renew(t)) * 8;
+                if (i < d) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[u][e] *= inv;
+                    store_codes(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
+                }
+            });
+        }
+        flip ^= 1;  // the next row's joins use other words: no thread may still read these
+    }
+}
+
+// Rows too long for a workgroup's registers: read once per statistic.  h is
+// written in the last pass, so that it may replace x or the residual.
+template <int XT, int WT>
+__global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
+    constexpr int T = 1024;
+    __shared__ float part[8][16];
+    const int t = threadIdx.x;
+    int flip = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        auto load_h = [&](int i, int n, float (&h)[8]) __attribute__((always_inline)) {
+            decode8(load_raw8(a.x, XT, (size_t)(row * a.ldx) + i, n), XT, h);
+            if (a.residual) {
+                float v[8];
+                decode8(load_raw8(a.residual, XT, (size_t)(row * a.ldr) + i, n), XT, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] += v[e];
+            }
+        };
+        auto load_y = [&](int i, int n, float rstd, float (&h)[8]) __attribute__((always_inline)) {
+            load_h(i, n, h);
+            if (a.weight) {
+                float w[8];
+                decode8(load_raw8(a.weight, WT, (size_t)i, n), WT, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = h[e] * rstd * w[e];
+            }
+        };
+        float rstd = 1.0f, inv = 1.0f, h[8];
+        if (a.weight) {
+            float ss = 0.0f;
+            for (long long i = t * 8; i < a.d; i += T * 8) {
+                load_h((int)i, min(8, a.d - (int)i), h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
+            }
+            ss = row_join<SumOp, T>(ss, part[flip]);
+            rstd = rstd_of<T>(ss, a.d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
+                for (long long i = t * 8; i < a.d; i += T * 8) {
+                    load_h((int)i, min(8, a.d - (int)i), h);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f(h[e]);
+                }
+            });
+            if (a.rstd && t == 0) a.rstd[row] = rstd;
+        }
+        if (is_code_type(a.y_type)) {
+            float amax = 0.0f;
+            for (long long i = t * 8; i < a.d; i += T * 8) {
+                load_y((int)i, min(8, a.d - (int)i), rstd, h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[e]));
+            }
+            amax = row_join<MaxBitsOp, T>(amax, part[2 + flip]);
+            const float s = row_scale_of(amax, a.y_type);
+            inv = 1.0f / s;
+            if (t == 0) a.scale[row] = s;
+        }
+        for (long long i = t * 8; i < a.d; i += T * 8) {
+            const int n = min(8, a.d - (int)i);
+            const size_t at = (size_t)(row * a.d) + i;
+            if (a.h) {
+                load_h((int)i, n, h);
+                float y[8];
+                load_y((int)i, n, rstd, y);
+                store8(a.h, XT, at, n, h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = y[e];
+            } else {
+                load_y((int)i, n, rstd, h);
+            }
+            if (is_code_type(a.y_type)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] *= inv;
+                store_codes(a.y, a.y_type, at, n, h);
+            } else {
+                store8(a.y, a.y_type, at, n, h);
+            }
+        }
+        flip ^= 1;
+    }
+}
+
+// ---- norm, backward --------------------------------------------------------------
+
+struct NormBackArgs {
+    const void* dy;
+    const void* h;
+    const void* weight;
+    const float* rstd;
+    const void* dh;   // nullptr: none
+    void* dx;
+    float* partials;  // gridDim.x rows of d sums of dy * xhat
+    long long rows, ld_dy, ldh, ld_dh;
+    int d;
+};
+
+// With xhat = h rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + dh, and
+// dw = sum over rows of dy xhat.  Layout as in norm_kernel; each thread sums
+// dw of its own columns over the workgroup's rows in registers, and the
+// workgroup leaves one row of partial sums.  AHEAD: the next row is fetched
+// while this one is worked on, and the weight stays in registers; without it
+// (rows that fill the registers) both are read when they are needed.
+template <int XT, int WT, int T, int U, int NT, bool AHEAD>
+__global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
+    static_assert(T == NT || T == 64, "a row belongs to a wave or to the workgroup");
+    constexpr int RB = NT / T;
+    __shared__ float part[2][16];
+    __shared__ float joined[RB > 1 ? RB * T * U * 8 : 1];
+    const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int d = a.d;
+    float dw[U][8];
+    Raw8 wr[U];
+    if constexpr (AHEAD)
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) wr[u] = load_raw8(a.weight, WT, (size_t)i, min(8, d - i));
+        });
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[u][e] = 0.0f;
+    const long long step = (long long)gridDim.x * RB;
+    struct Row {
+        Raw8 dy[U], h[U], dh[U];
+        float rstd;
+    };
+    auto fetch = [&](long long row, Row& r) __attribute__((always_inline)) {
+        if (row >= a.rows) return;
+        r.rstd = a.rstd[row];
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                const int n = min(8, d - i);
+                r.dy[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
+                r.h[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n);
+                if (AHEAD && a.dh) r.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
+            }
+        });
+    };
+    int flip = 0;
+    long long row = (long long)blockIdx.x * RB + threadIdx.x / T;
+    Row now;
+    if constexpr (AHEAD) fetch(row, now);
+    for (; row < a.rows; row += step) {
+        Row next;
+        if constexpr (AHEAD) {
+            fetch(row + step, next);
+        } else {
+            fetch(row, now);
+        }
+        float xhat[U][8], g[U][8], c = 0.0f;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                float w[8];
+                if constexpr (!AHEAD) wr[u] = load_raw8(a.weight, WT, (size_t)i, min(8, d - i));
+                decode8(now.h[u], XT, xhat[u]);
+                decode8(now.dy[u], XT, g[u]);
+                decode8(wr[u], WT, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    xhat[u][e] *= now.rstd;
+                    dw[u][e] = __builtin_fmaf(g[u][e], xhat[u][e], dw[u][e]);
+                    g[u][e] *= w[e];
+                    c = __builtin_fmaf(g[u][e], xhat[u][e], c);
+                }
+            }
+        });
+        c = row_join<SumOp, T>(c, part[flip]) / (float)d;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = now.rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
+                if (a.dh) {
+                    float v[8];
+                    if constexpr (!AHEAD) now.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, min(8, d - i));
+                    decode8(now.dh[u], XT, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += v[e];
+                }
+                store8(a.dx, XT, (size_t)(row * d) + i, min(8, d - i), o);
+            }
+        });
+        if constexpr (AHEAD) now = next;
+        flip ^= 1;
+    }
+    if constexpr (RB > 1) {
+        // join the waves' sums, in wave order
+        const int wave = threadIdx.x >> 6;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) joined[(wave * U * 8 + u * 8 + e) * 64 + t] = dw[u][e];
+        });
+        __syncthreads();
+        if (wave != 0) return;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int w = 1; w < RB; ++w) dw[u][e] += joined[(w * U * 8 + u * 8 + e) * 64 + t];
+        });
+    }
+    static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        const int i = (u * T + t) * 8;
+        if (i < d) {
+            float* p = a.partials + (size_t)blockIdx.x * d + i;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < d) p[e] = dw[u][e];
+        }
+    });
+}
+
+// Rows too long for a workgroup's registers: dw is summed in the workgroup's
+// row of partial sums itself, each word by one thread.
+template <int XT, int WT>
+__global__ __launch_bounds__(1024) void norm_back_long_kernel(const NormBackArgs a) {
+    constexpr int T = 1024;
+    __shared__ float part[2][16];
+    const int t = threadIdx.x;
+    float* sums = a.partials + (size_t)blockIdx.x * a.d;
+    for (long long i = t; i < a.d; i += T) sums[i] = 0.0f;
+    int flip = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float rstd = a.rstd[row];
+        auto load1x = [&](const void* p, long long ld, long long i) { return load1(p, XT, (size_t)(row * ld + i)); };
+        float c = 0.0f;
+        for (long long i = t; i < a.d; i += T)
+            c = __builtin_fmaf(load1x(a.dy, a.ld_dy, i) * load1(a.weight, WT, i), load1x(a.h, a.ldh, i) * rstd, c);
+        c = row_join<SumOp, T>(c, part[flip]) / (float)a.d;
+        for (long long i = t; i < a.d; i += T) {
+            const float dy = load1x(a.dy, a.ld_dy, i), xhat = load1x(a.h, a.ldh, i) * rstd;
+            float o = rstd * __builtin_fmaf(-xhat, c, dy * load1(a.weight, WT, i));
+            if (a.dh) o += load1x(a.dh, a.ld_dh, i);
+            store1(a.dx, XT, (size_t)(row * a.d + i), o);
+            sums[i] = __builtin_fmaf(dy, xhat, sums[i]);
+        }
+        flip ^= 1;
+    }
+}
+
+// ---- column sums: the last step ---------------------------------------------------
+
+// out[j] = sum of the `parts` rows of partial sums, in an order that depends
+// on `parts` only: 16 threads per column take every 16th row, then a tree.
+__global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ partials, void* out, int out_type, int parts,
+                                                   long long d) {
+    __shared__ float sums[16][17];
+    const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
+    const long long j = (long long)blockIdx.x * 16 + c;
+    float s = 0.0f;
+    if (j < d) {
+        int r = k;
+        for (; r + 7 * 16 < parts; r += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = partials[(size_t)(r + 16 * e) * d + j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[e];
+        }
+        for (; r < parts; r += 16) s += partials[(size_t)r * d + j];
+    }
+    sums[k][c] = s;
+    __syncthreads();
+    if (k == 0 && j < d) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = sums[i][c];
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+            for (int i = 0; i < w; ++i) v[i] += v[i + w];
+        store1(out, out_type, (size_t)j, v[0]);
+    }
+}
+
+// ---- activation and bias, backward -------------------------------------------------
+
+struct ActBackArgs {
+    const void* dy;
+    const void* preact;  // nullptr: no activation
+    void* dz;            // nullptr: not wanted
+    float* partials;     // nullptr: no column sums; else gridDim.y rows of n sums of dz
+    long long rows;
+    int n, rows_per_block;
+    int type, preact_type, act;
+};
+
+// dz = dy act'(z), and the sums of dz over a block of rows.  L lanes hold 8
+// columns each; a workgroup's 256 / L groups of lanes take its rows in turn.
+template <int L>
+__global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
+    constexpr int G = 256 / L;
+    __shared__ float joined[G][L * 8];
+    const int l = threadIdx.x % L, g = threadIdx.x / L;
+    const int j = (blockIdx.x * L + l) * 8;
+    const int n = min(8, a.n - j);
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    const long long first = (long long)blockIdx.y * a.rows_per_block;
+    const long long last = min(a.rows, first + a.rows_per_block);
+    if (n > 0)
+        with_act(a.preact ? a.act : GEMM_BT_ACT_NONE, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+            auto one = [&](const Raw8& dyr, const Raw8& zr, long long row) __attribute__((always_inline)) {
+                float v[8];
+                decode8(dyr, a.type, v);
+                if constexpr (ACT != GEMM_BT_ACT_NONE) {
+                    float z[8];
+                    decode8(zr, a.preact_type, z);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= act_slope<ACT>(z[e]);
+                }
+                if (a.dz) store8(a.dz, a.type, (size_t)(row * a.n) + j, n, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += v[e];
+            };
+            auto load = [&](long long row, Raw8& dyr, Raw8& zr) __attribute__((always_inline)) {
+                dyr = load_raw8(a.dy, a.type, (size_t)(row * a.n) + j, n);
+                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8(a.preact, a.preact_type, (size_t)(row * a.n) + j, n);
+            };
+            long long row = first + g;
+            for (; row + 3 * G < last; row += 4 * G) {  // four rows in flight
+                Raw8 dyr[4], zr[4];
+                static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
+                    constexpr int u = decltype(uc)::value;
+                    load(row + u * G, dyr[u], zr[u]);
+                });
+                static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
+                    constexpr int u = decltype(uc)::value;
+                    one(dyr[u], zr[u], row + u * G);
+                });
+            }
+            for (; row < last; row += G) {
+                Raw8 dyr, zr;
+                load(row, dyr, zr);
+                one(dyr, zr, row);
+            }
+        });
+    if (!a.partials) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) joined[g][l * 8 + e] = sum[e];
+    __syncthreads();
+    float* p = a.partials + (size_t)blockIdx.y * a.n;
+    for (int c = threadIdx.x; c < L * 8; c += 256) {
+        const long long col = (long long)blockIdx.x * L * 8 + c;
+        if (col >= a.n) continue;
+        float s = joined[0][c];
+#pragma unroll
+        for (int i = 1; i < G; ++i) s += joined[i][c];
+        p[col] = s;
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+static int launch(const void* fn, dim3 grid, int threads, void** args, void* stream) {
+    if (hipLaunchKernel(fn, grid, dim3(threads), args, 0, (hipStream_t)stream) != hipSuccess) {
+        (void)hipGetLastError();
+        return GEMM_BT_ERR_LAUNCH;
+    }
+    return GEMM_BT_OK;
+}
+
+static bool float_type(int t) { return t == GEMM_BT_F32 || t == GEMM_BT_F16 || t == GEMM_BT_BF16; }
+static bool aligned(const void* p, int t) { return (uintptr_t)p % elem_size(t) == 0; }
+static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld < (1LL << 40); }
+
+struct RowPlan {
+    const void* fn;
+    int threads, rows_per_block;
+};
+
+template <int XT, int WT>
+static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
+    const int64_t chunks = (d + 7) / 8;
+    // Few rows: the whole row at once, as many threads as it has chunks, so
+    // that one load's latency is all that is waited for.
+    if (rows <= 2 * num_cu) {
+        if (chunks <= 64) return {(const void*)&norm_kernel<XT, WT, 64, 1, 64>, 64, 1};
+        if (chunks <= 256) return {(const void*)&norm_kernel<XT, WT, 256, 1, 256>, 256, 1};
+        if (chunks <= 512) return {(const void*)&norm_kernel<XT, WT, 512, 1, 512>, 512, 1};
+        if (chunks <= 1024) return {(const void*)&norm_kernel<XT, WT, 1024, 1, 1024>, 1024, 1};
+    }
+    if (chunks <= 64) return {(const void*)&norm_kernel<XT, WT, 64, 1, 256>, 256, 4};
+    if (chunks <= 128) return {(const void*)&norm_kernel<XT, WT, 64, 2, 256>, 256, 4};
+    if (chunks <= 256) return {(const void*)&norm_kernel<XT, WT, 256, 1, 256>, 256, 1};
+    if (chunks <= 512) return {(const void*)&norm_kernel<XT, WT, 256, 2, 256>, 256, 1};
+    if (chunks <= 1024) return {(const void*)&norm_kernel<XT, WT, 512, 2, 512>, 512, 1};
+    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 1024, 2, 1024>, 1024, 1};
+    return {(const void*)&norm_long_kernel<XT, WT>, 1024, 1};
+}
+
+template <int XT, int WT>
+static RowPlan norm_back_plan(int64_t d) {
+    const int64_t chunks = (d + 7) / 8;
+    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 64, 1, 256, true>, 256, 4};
+    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 64, 2, 256, true>, 256, 4};
+    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 256, 1, 256, true>, 256, 1};
+    if (chunks <= 512) return {(const void*)&norm_back_kernel<XT, WT, 256, 2, 256, true>, 256, 1};
+    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 512, 2, 512, true>, 512, 1};
+    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 1024, 2, 1024, false>, 1024, 1};
+    return {(const void*)&norm_back_long_kernel<XT, WT>, 1024, 1};
+}
+
+// f<x_type, w_type>() for the weight types there are kernels for: x's own and fp32.
+static bool weight_type_ok(int x_type, int w_type) { return w_type == x_type || w_type == GEMM_BT_F32; }
+template <class F>
+static RowPlan with_types(int x_type, int w_type, F&& f) {
+    typedef std::integral_constant<int, GEMM_BT_F32> F32;
+    typedef std::integral_constant<int, GEMM_BT_F16> F16;
+    typedef std::integral_constant<int, GEMM_BT_BF16> BF16;
+    if (x_type == GEMM_BT_F32) return f(F32{}, F32{});
+    if (x_type == GEMM_BT_F16) return w_type == GEMM_BT_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
+    return w_type == GEMM_BT_F32 ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
+}
+
+static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
+    int num_cu = 0;
+    const int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    const RowPlan p = with_types(x_type, w_type, [&](auto x, auto w) { return norm_plan<x(), w()>(a.rows, a.d, num_cu); });
+    const int64_t grid = std::min<int64_t>((a.rows + p.rows_per_block - 1) / p.rows_per_block, 1 << 20);
+    void* args[] = {&a};
+    return launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
+}
+
+static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
+    return with_types(x_type, w_type, [&](auto x, auto w) { return norm_back_plan<x(), w()>(d); });
+}
+// Workgroups of the backward pass, each of which leaves one row of partial sums.
+static int64_t norm_back_grid(const RowPlan& p, int64_t rows, int num_cu) {
+    const int64_t most = (int64_t)num_cu * std::max(1, 512 / p.threads);
+    return std::min<int64_t>((rows + p.rows_per_block - 1) / p.rows_per_block, most);
+}
+
+// Row blocks of the activation's backward pass (the grid's second axis).
+struct ActBackPlan {
+    const void* fn;
+    int64_t strips, blocks;
+    int rows_per_block;
+};
+static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu) {
+    ActBackPlan p;
+    int lanes = 64;
+    if (n <= 64) { lanes = 8; p.fn = (const void*)&act_back_kernel<8>; }
+    else if (n <= 128) { lanes = 16; p.fn = (const void*)&act_back_kernel<16>; }
+    else if (n <= 256) { lanes = 32; p.fn = (const void*)&act_back_kernel<32>; }
+    else p.fn = (const void*)&act_back_kernel<64>;
+    const int groups = 256 / lanes;  // rows a workgroup takes at a time
+    p.strips = (n + lanes * 8 - 1) / (lanes * 8);
+    // about four workgroups per CU, each with whole rounds of its groups
+    const int64_t want = std::max<int64_t>(1, 4 * num_cu / p.strips);
+    int64_t per = (rows + want - 1) / want;
+    per = std::max<int64_t>(groups, (per + groups - 1) / groups * groups);
+    p.blocks = (rows + per - 1) / per;
+    while (p.blocks > 32768) {  // the grid's second axis ends at 65535
+        per *= 2;
+        p.blocks = (rows + per - 1) / per;
+    }
+    p.rows_per_block = (int)per;
+    return p;
+}
+
+static int fold(const float* partials, void* out, int out_type, int64_t parts, int64_t d, void* stream) {
+    int np = (int)parts;
+    long long dd = d;
+    void* args[] = {&partials, &out, &out_type, &np, &dd};
+    return launch((const void*)&fold_kernel, dim3((unsigned)((d + 15) / 16)), 256, args, stream);
+}
+
+}  // namespace gbt
+
+using namespace gbt;
+
+extern "C" {
+
+int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* y, void* h,
+                     float* scale, float* rstd, int64_t rows, int64_t d, float eps, int x_dtype, int w_dtype, int y_dtype,
+                     void* stream) {
+    if (rows < 0 || d < 0 || !(eps >= 0.0f)) return GEMM_BT_ERR_INVALID_VALUE;
+    const bool codes = y_dtype == GEMM_BT_FP8_E4M3 || y_dtype == GEMM_BT_INT8;
+    if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype) || !(codes || float_type(y_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (rows == 0 || d == 0) return GEMM_BT_OK;
+    if (!x || !weight || !y || (codes && !scale)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!stride_ok(ldx, d) || (residual && !stride_ok(ldr, d))) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!aligned(x, x_dtype) || !aligned(residual, x_dtype) || !aligned(h, x_dtype) || !aligned(weight, w_dtype) ||
+        (!codes && !aligned(y, y_dtype)) || !aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32))
+        return GEMM_BT_ERR_INVALID_VALUE;
+    NormArgs a = {x, residual, weight, y, h, scale, rstd, rows, ldx, ldr, (int)d, eps, y_dtype};
+    return launch_norm(a, x_dtype, w_dtype, stream);
+}
+
+int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int64_t rows, int64_t d, int x_dtype,
+                          int q_dtype, void* stream) {
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!float_type(x_dtype) || (q_dtype != GEMM_BT_FP8_E4M3 && q_dtype != GEMM_BT_INT8)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (rows == 0 || d == 0) return GEMM_BT_OK;
+    if (!x || !q || !scale || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
+    NormArgs a = {x, nullptr, nullptr, q, nullptr, scale, nullptr, rows, ldx, 0, (int)d, 0.0f, q_dtype};
+    return launch_norm(a, x_dtype, x_dtype, stream);
+}
+
+int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    *bytes = (size_t)(norm_back_grid(norm_back_plan_of(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * 4);
+    return GEMM_BT_OK;
+}
+
+int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight,
+                              const float* rstd, const void* dh, int64_t ld_dh, void* dx, void* dweight, int64_t rows,
+                              int64_t d, int x_dtype, int w_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d == 0) return GEMM_BT_OK;
+    if (!dweight || !aligned(dweight, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (rows > 0) {
+        if (!dy || !h || !weight || !rstd || !dx || !workspace) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!stride_ok(ld_dy, d) || !stride_ok(ldh, d) || (dh && !stride_ok(ld_dh, d))) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!aligned(dy, x_dtype) || !aligned(h, x_dtype) || !aligned(dh, x_dtype) || !aligned(dx, x_dtype) ||
+            !aligned(weight, w_dtype) || !aligned(rstd, GEMM_BT_F32) || !aligned(workspace, GEMM_BT_F32))
+            return GEMM_BT_ERR_INVALID_VALUE;
+    }
+    int num_cu = 0;
+    int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    int64_t grid = 0;
+    if (rows > 0) {
+        const RowPlan p = norm_back_plan_of(x_dtype, w_dtype, d);
+        grid = norm_back_grid(p, rows, num_cu);
+        if (workspace_bytes < (size_t)(grid * d * 4)) return GEMM_BT_ERR_INVALID_VALUE;
+        NormBackArgs a = {dy, h, weight, rstd, dh, dx, (float*)workspace, rows, ld_dy, ldh, ld_dh, (int)d};
+        void* args[] = {&a};
+        st = launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
+        if (st != GEMM_BT_OK) return st;
+    }
+    return fold((const float*)workspace, dweight, w_dtype, grid, d, stream);
+}
+
+int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    if (rows < 0 || n < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (n > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (rows > 0 && n > 0) *bytes = (size_t)(act_back_plan(rows, n, plan_cus()).blocks * n * 4);
+    return GEMM_BT_OK;
+}
+
+int gemm_bt_act_backward(const void* dy, const void* preact, void* dz, void* dbias, int64_t rows, int64_t n,
+                         int activation, int dtype, int preact_dtype, int bias_dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (rows < 0 || n < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (activation < GEMM_BT_ACT_NONE || activation > GEMM_BT_ACT_SILU) return GEMM_BT_ERR_INVALID_VALUE;
+    const bool act = activation != GEMM_BT_ACT_NONE;
+    if (!float_type(dtype) || (act && !float_type(preact_dtype)) || (dbias && !float_type(bias_dtype)))
+        return GEMM_BT_ERR_UNSUPPORTED;
+    if (n > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (n == 0) return GEMM_BT_OK;
+    if (dbias && !aligned(dbias, bias_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (rows > 0) {
+        if (!dy || (act && !preact) || (dbias && !workspace)) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!aligned(dy, dtype) || !aligned(dz, dtype) || (act && !aligned(preact, preact_dtype)) ||
+            !aligned(workspace, GEMM_BT_F32))
+            return GEMM_BT_ERR_INVALID_VALUE;
+    }
+    if (!dbias && (!dz || rows == 0)) return GEMM_BT_OK;
+    int num_cu = 0;
+    int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    int64_t parts = 0;
+    if (rows > 0) {
+        const ActBackPlan p = act_back_plan(rows, n, num_cu);
+        parts = p.blocks;
+        if (dbias && workspace_bytes < (size_t)(parts * n * 4)) return GEMM_BT_ERR_INVALID_VALUE;
+        ActBackArgs a = {dy,      act ? preact : nullptr, dz,    dbias ? (float*)workspace : nullptr, rows, (int)n, p.rows_per_block,
+                         dtype, preact_dtype,           activation};
+        void* args[] = {&a};
+        st = launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
+        if (st != GEMM_BT_OK) return st;
+    }
+    return dbias ? fold((const float*)workspace, dbias, bias_dtype, parts, n, stream) : GEMM_BT_OK;
+}
+
+}  // extern "C"

@@ -37,14 +37,16 @@
 
 #include "common.hpp"
 #include "dma_kernel.hpp"
+#include "epilogue.hpp"
 
 namespace gbt {
 
-template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT = 0>
-__global__ __launch_bounds__(64 * W) void skinny_dma_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
-                                                           void* __restrict__ C, int M, int N, int K,
-                                                           int vec_store, long long sa, long long sb, long long sc) {
-    batch_item(blockIdx.y, A, B, C, sa, sb, sc);  // one grid row per batch item
+// The kernel's body.  `epi` is the epilogue's arguments (EpiArgs), or nothing
+// (SkinnyPlain): then the sums are rounded into C as they are.
+struct SkinnyPlain {};
+template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT, class Epi>
+__device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
+                                            int M, int N, int K, int vec_store, const Epi& epi) {
     constexpr int AR = 16;                 // rows of A held (M <= 16)
     constexpr int CPR = KB / 8;            // 16-byte chunks per row per stage
     constexpr int ROWB = KB * 2;           // bytes per row per stage
@@ -202,6 +204,13 @@ __global__ __launch_bounds__(64 * W) void skinny_dma_kernel(const u16* __restric
         const u32 o = ((u32)m * (u32)N + (u32)n) * OSZ;
         const float v0 = sum[0], v1 = sum[1], v2 = sum[2], v3 = sum[3];
         if (nl >= BN) continue;
+        if constexpr (!std::is_same_v<Epi, SkinnyPlain>) {
+            const float vv[4] = {v0, v1, v2, v3};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < N) store_one_epi(vv[e], C, N, m, n + e, epi);
+            continue;
+        }
         if (vec_store) {
             if (n < N) {
                 if constexpr (OUT == GEMM_BT_F32) {
@@ -227,6 +236,21 @@ __global__ __launch_bounds__(64 * W) void skinny_dma_kernel(const u16* __restric
             }
         }
     }
+}
+
+template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT = 0>
+__global__ __launch_bounds__(64 * W) void skinny_dma_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
+                                                           void* __restrict__ C, int M, int N, int K,
+                                                           int vec_store, long long sa, long long sb, long long sc) {
+    batch_item(blockIdx.y, A, B, C, sa, sb, sc);  // one grid row per batch item
+    skinny_body<IN, OUT, BN, KB, STAGES, W, ROT>(A, B, C, M, N, K, vec_store, SkinnyPlain{});
+}
+
+template <int IN, int BN, int KB, int STAGES, int W>
+__global__ __launch_bounds__(64 * W) void skinny_epi_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
+                                                           void* __restrict__ C, int M, int N, int K,
+                                                           const EpiArgs epi) {
+    skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, epi);
 }
 
 }  // namespace gbt

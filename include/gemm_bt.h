@@ -204,6 +204,123 @@ int gemm_bt_ws(const void* A, const void* B, void* C, int64_t M, int64_t N, int6
 int gemm_bt_noalloc(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,
                     int out_dtype, void* stream);
 
+/* Activations of an epilogue; Phi is the normal distribution's function. */
+typedef enum {
+    GEMM_BT_ACT_NONE = 0,      /* z */
+    GEMM_BT_ACT_RELU = 1,      /* max(z, 0) */
+    GEMM_BT_ACT_GELU = 2,      /* z Phi(z) */
+    GEMM_BT_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    GEMM_BT_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} gemm_bt_activation;
+
+/* What gemm_bt_epi does to the sums before they are stored; a NULL pointer
+   leaves its term out. */
+typedef struct {
+    const float* row_scale; /* M fp32 factors, one per row of A (8-bit rows with scales) */
+    const float* col_scale; /* N fp32 factors, one per row of B */
+    const void* bias;       /* N elements of bias_dtype */
+    const void* residual;   /* M x N elements of residual_dtype, row-major; may be C itself if its type is C's */
+    void* preact;           /* M x N elements of preact_dtype, row-major: receives Z (for a backward pass) */
+    int bias_dtype, residual_dtype, preact_dtype; /* GEMM_BT_F32, _F16 or _BF16, read where the pointer is not NULL */
+    int activation;                               /* gemm_bt_activation */
+} gemm_bt_epilogue_t;
+
+/*
+ * The product with its epilogue in the same kernel:
+ *   Z[i][j] = row_scale[i] * col_scale[j] * sum_k A[i][k] B[j][k] + bias[j]
+ *   C[i][j] = act(Z[i][j]) + residual[i][j]
+ * The sum, Z, the activation and the residual's addition are held in fp32 and
+ * rounded once into C (and once into preact).  Inputs are those of gemm_bt;
+ * out_dtype is GEMM_BT_F32, _BF16 or _F16 for every input type: an int8
+ * product's exact int32 sum is converted to fp32 (rounded above 2^24) before
+ * its scales.  The activations use the hardware's exponential and reciprocal:
+ * they are accurate to a few units of fp32's last place.
+ *   epilogue   NULL, or every pointer in it NULL and the activation none: C is
+ *              the plain product (in floating point for int8 inputs too)
+ *   workspace  as for gemm_bt_ws (NULL: no split along K); the plan and the
+ *              sizes are those of gemm_bt_plan_ws and gemm_bt_workspace_size
+ *              (for int8 inputs with out_dtype GEMM_BT_INT32)
+ * K == 0 is the empty sum: C = act(bias) + residual, A and B are not read.
+ * bias, residual and preact need the alignment of their elements only.
+ * preact must not overlap C or an input.  Types that are none of the above,
+ * an unknown activation: INVALID_VALUE.  Everything else is as for gemm_bt_ws.
+ */
+int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,
+                int out_dtype, const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * Row operators around the product.  Matrices are row-major with `d` (or `n`)
+ * contiguous elements per row; an input's rows start `ld` elements apart (ld
+ * >= d), outputs are dense.  x, residual and h share x_dtype; a weight is of
+ * x_dtype or GEMM_BT_F32 (else UNSUPPORTED).  Pointers need the alignment of
+ * their elements only; every size from 0 up is served (no rows: nothing is
+ * written but a gradient's zeros; up to 2^31 - 8193 columns and 2^31 rows,
+ * else UNSUPPORTED).  Statistics are held in fp32 and every output is rounded
+ * once.  Results are the same bits on every run on the same device.  Calls
+ * are asynchronous on `stream`, allocate nothing and report argument errors
+ * before anything is enqueued, as the products do.
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual        (h = x where residual is NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)
+ *   y = h * rstd * weight
+ * y_dtype GEMM_BT_F32, _F16 or _BF16, or 8 bits with one scale per row, for
+ * an 8-bit product: with amax the row's largest |y| and Q = 448 (_FP8_E4M3)
+ * or 127 (_INT8), scale = max(amax / Q, 2^-100) and y holds y / scale rounded
+ * to nearest even.  A row with an infinity or a NaN among its y gets the
+ * scale NaN (its codes then hold no value).
+ *   y      rows x d of y_dtype
+ *   h      rows x d of x_dtype, or NULL: receives h rounded.  It may be x or
+ *          residual itself where that one's rows are dense; y may not
+ *   scale  rows fp32 (8-bit y; else not used)
+ *   rstd   rows fp32, or NULL: receives 1 / sqrt(...) for the backward pass
+ *   eps    >= 0 (else INVALID_VALUE)
+ */
+int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* y,
+                     void* h, float* scale, float* rstd, int64_t rows, int64_t d, float eps, int x_dtype,
+                     int w_dtype, int y_dtype, void* stream);
+
+/* The rows of x in 8 bits (q_dtype GEMM_BT_FP8_E4M3 or GEMM_BT_INT8) and their
+   scales, as gemm_bt_rms_norm leaves its y. */
+int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int64_t rows, int64_t d, int x_dtype,
+                          int q_dtype, void* stream);
+
+/*
+ * The norm's backward pass.  With xhat = h * rstd, g = dy * weight and dy the
+ * gradient of y (of the values before rounding, for 8-bit y):
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dh,   dweight = sum over rows of dy * xhat
+ * dx is the gradient of x and of residual alike.
+ *   h, rstd    as gemm_bt_rms_norm left them (x itself where there was no residual)
+ *   dh         the gradient that reaches h from elsewhere, or NULL
+ *   dx         rows x d of x_dtype; may be dy or dh itself where its rows are dense
+ *   dweight    d elements of w_dtype
+ *   workspace  at least gemm_bt_rms_norm_backward_workspace bytes, 4-byte
+ *              aligned, any contents (not used for rows == 0)
+ */
+int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight,
+                              const float* rstd, const void* dh, int64_t ld_dh, void* dx, void* dweight,
+                              int64_t rows, int64_t d, int x_dtype, int w_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
+
+/*
+ * The backward pass of gemm_bt_epi's activation and bias:
+ *   dz = dy * act'(preact),   dbias = sum over rows of dz
+ * (the gradients of A and B are then products of dz, gemm_bt_batched_layout's
+ * operands stored K-outer; that of the residual is dy itself).
+ *   preact  rows x n of preact_dtype as gemm_bt_epi left it (not read for GEMM_BT_ACT_NONE)
+ *   dz      rows x n of dtype, or NULL; may be dy itself
+ *   dbias   n elements of bias_dtype, or NULL (then no workspace is needed)
+ *   workspace  at least gemm_bt_act_backward_workspace bytes, 4-byte aligned, any contents
+ */
+int gemm_bt_act_backward(const void* dy, const void* preact, void* dz, void* dbias, int64_t rows, int64_t n,
+                         int activation, int dtype, int preact_dtype, int bias_dtype, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes);
+
 /* Workspace gemm_bt_ws needs for these sizes and types (0 when it runs the
    plain grid), for the current device (256 compute units without one).  At
    most 16 KiB + 256 * 64 KiB (16.02 MiB) on an MI355X, whatever the
