@@ -21,8 +21,8 @@ Entry points (same names as the C-ABI in ``include/gemm_bt.h``):
   gemm_bt_noalloc(A, B, C, M, N, K, in_dtype, out_dtype, stream)   gemm_bt_ws with the library's scratch
 and torch convenience wrappers ``mm_bt(a, b, out_dtype)`` (2-D or batched 3-D operands),
 ``mm_layout(a, b, a_layout, b_layout, out_dtype)`` and ``mm(a, b, out_dtype)`` (= a @ b).  The operators around the
-product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_backward, gemm_bt_act_backward) are
-called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
+product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_backward, gemm_bt_act_backward,
+gemm_bt_linear_backward) are called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
 ``add_rms_norm_backward`` and ``quantize_rows``, which need torch and are imported when first used.
 """
 from __future__ import annotations
@@ -43,7 +43,7 @@ EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layo
            "gemm_bt_plan_batched_layout", "gemm_bt_tile_coord", "gemm_bt_ws", "gemm_bt_workspace_size",
            "gemm_bt_plan_ws", "gemm_bt_noalloc", "gemm_bt_epi", "gemm_bt_rms_norm", "gemm_bt_rms_norm_backward",
            "gemm_bt_rms_norm_backward_workspace", "gemm_bt_quantize_rows", "gemm_bt_act_backward",
-           "gemm_bt_act_backward_workspace")
+           "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -120,9 +120,12 @@ def load():
             lib.gemm_bt_rms_norm_backward_workspace.argtypes = [i64, i64, szp]
             lib.gemm_bt_act_backward.argtypes = [vp, vp, vp, vp, i64, i64, ci, ci, ci, ci, vp, sz, vp]
             lib.gemm_bt_act_backward_workspace.argtypes = [i64, i64, szp]
+            lib.gemm_bt_linear_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp, sz, vp]
+            lib.gemm_bt_linear_backward_workspace.argtypes = [i64, i64, i64, ci, szp]
             for f in (lib.gemm_bt_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
                       lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
-                      lib.gemm_bt_act_backward_workspace):
+                      lib.gemm_bt_act_backward_workspace, lib.gemm_bt_linear_backward,
+                      lib.gemm_bt_linear_backward_workspace):
                 f.restype = ci
             _lib = lib
     return _lib

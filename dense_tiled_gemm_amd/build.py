@@ -32,7 +32,7 @@ FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, name) for name in ("gemm_bt.hip", "gemm_epi.hip", "norm.hip")]
+    return [os.path.join(CSRC, name) for name in ("gemm_bt.hip", "gemm_epi.hip", "norm.hip", "linear_back.hip")]
 
 
 def build(extra=None, out=SO, verbose=False) -> str:

@@ -1,0 +1,337 @@
+// linear_back.hip -- the backward pass of the product with bias and
+// activation: with dz = dy act'(z),
+//   dX = dz W        (M x K, summed over N)
+//   dW = dz^T X      (N x K, summed over M)
+//   db = sum over rows of dz.
+// dz is made once, in the inputs' 16-bit type, by one pass over dy and z that
+// also leaves partial sums of db (act_back_kernel).  Both products then run in
+// ONE launch on the transpose-read tiles of trans_kernel.hpp, operands as they
+// lie in memory: the tiles of one fill the compute units that the other leaves
+// idle, the last block of each column of db is folded by a few more
+// workgroups, and a backward pass costs two launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "rows.hpp"
+#include "trans_kernel.hpp"
+
+namespace gbt {
+
+// One of the two products, in tiles of BT x BT, each tile's K steps of 64 in
+// `pieces` runs of `per` steps.  A single piece is rounded into `out`; of
+// several, piece j leaves fp32 sums in `parts` + j * rows * cols.
+struct BackProduct {
+    const u16* a;
+    const u16* b;
+    void* out;
+    float* parts;
+    int rows, cols, depth;  // of the result, and of the sum
+    int lda, ldb;
+    int tiles_m, tiles_n, pieces, per;
+    int blocks;   // workgroups: tiles_m * tiles_n * pieces, padded to whole rounds of the 8 dies
+    int shifted;  // rows of `out` are not whole 16-byte chunks (of `parts`: shifted_parts)
+    int shifted_parts;
+};
+struct BackArgs {
+    BackProduct dw, dx;
+    FoldArgs fold;  // out == nullptr: none
+};
+
+template <int IN, bool TA, int BT, int WN>
+__device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigned char* lds) {
+    const int total = p.tiles_m * p.tiles_n * p.pieces;
+    if (pid >= total) return;
+    // die by die, the pieces of a tile next to each other
+    const int v = (int)xcd_seq(pid, total);
+    const int tile = v / p.pieces, j = v - tile * p.pieces;
+    int64_t tm, tn;
+    band_coord(tile, p.tiles_m, p.tiles_n, 4, &tm, &tn);
+    const int k0 = j * p.per * 64;
+    const int depth = min(p.depth - k0, p.per * 64);
+    const u16* a = TA ? p.a + (size_t)k0 * p.lda : p.a + k0;
+    const u16* b = p.b + (size_t)k0 * p.ldb;
+    if (p.pieces == 1)
+        trans_body<IN, IN, TA, true, BT, BT, 2, WN>(a, b, p.out, p.rows, p.cols, depth, p.lda, p.ldb, (int)tm * BT,
+                                                    (int)tn * BT, p.shifted, lds);
+    else
+        trans_body<IN, GEMM_BT_F32, TA, true, BT, BT, 2, WN>(a, b, p.parts + (size_t)j * p.rows * p.cols, p.rows, p.cols,
+                                                             depth, p.lda, p.ldb, (int)tm * BT, (int)tn * BT,
+                                                             p.shifted_parts, lds);
+}
+
+template <int IN, int BT, int WN>
+__global__ __launch_bounds__(128 * WN) void linear_back_kernel(const BackArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * 2 * BT * 64 * 2];
+    int blk = blockIdx.x;
+    if (blk < a.dw.blocks) return back_tile<IN, true, BT, WN>(a.dw, blk, lds);
+    blk -= a.dw.blocks;
+    if (blk < a.dx.blocks) return back_tile<IN, false, BT, WN>(a.dx, blk, lds);
+    fold_columns<128 * WN>(a.fold, blk - a.dx.blocks, (float(*)[17])lds);
+}
+
+// out = sum of `pieces` slices of n fp32 sums, in order, rounded once.
+struct SliceArgs {
+    const float* parts[2];
+    void* out[2];
+    long long n[2];
+    int pieces[2];
+    int type;
+};
+__global__ __launch_bounds__(256) void slices_kernel(const SliceArgs a) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const long long step = (long long)gridDim.x * 256 * 8;
+        for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < a.n[s]; i += step) {
+            const int n = (int)min(8LL, a.n[s] - i);
+            float v[8];
+            decode8(load_raw8(a.parts[s], GEMM_BT_F32, (size_t)i, n), GEMM_BT_F32, v);
+            for (int j = 1; j < a.pieces[s]; ++j) {
+                float w[8];
+                decode8(load_raw8(a.parts[s], GEMM_BT_F32, (size_t)(j * a.n[s] + i), n), GEMM_BT_F32, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += w[e];
+            }
+            store8(a.out[s], a.type, (size_t)i, n, v);
+        }
+    }
+}
+
+// Rows of x and then of w, k elements each, into rows of `pitch` elements (the
+// rest zeros): for k % 8 != 0, whose rows are not whole 16-byte chunks.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const u16* x, const u16* w, u16* out, long long m, long long n, int k,
+                                                       int pitch) {
+    const int groups = pitch / 8;
+    const long long total = (m + n) * groups;
+    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < total; q += (long long)gridDim.x * 256) {
+        const long long row = q / groups;
+        const int j = (int)(q - row * groups) * 8;
+        const u16* src = row < m ? x + row * k : w + (row - m) * k;
+        const Raw8 r = load_raw8(src, GEMM_BT_BF16, (size_t)j, min(8, k - j));
+        *(u32x4*)(out + row * pitch + j) = r.a;
+    }
+}
+
+__global__ void fill_zero16_kernel(u16* p, long long n) {
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) p[i] = 0;
+}
+
+// ---- host ------------------------------------------------------------------------
+
+static int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+static int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Everything a backward pass of these sizes needs: its tiles, and where its
+// parts lie in the workspace (byte offsets; the sizes do not depend on which
+// gradients are asked for).
+struct BackPlan {
+    int bt;
+    bool make_dz, pad;
+    int64_t ldz, ldk;  // row pitches of dz, and of X and W (elements)
+    int pieces_w, per_w, pieces_x, per_x;
+    int64_t sums_parts;
+    int64_t off_dz, off_sums, off_parts_w, off_parts_x, off_pad, bytes;
+};
+
+// Runs of K steps for a product of `tiles` tiles of `steps` steps each, where
+// all tiles of both products would take `fair` steps on every CU: a tile much
+// longer than that is cut into runs of about that length, each of which leaves
+// fp32 sums; the cut costs a launch that adds them, so only a gain of `least`
+// steps is taken.  `most` steps is what a run may hold (2 GiB of an operand).
+static void cut(int64_t steps, int64_t fair, int64_t least, int64_t most, int* pieces, int* per) {
+    int64_t run = steps;
+    if (steps - fair >= least) run = std::max<int64_t>(fair, 8);
+    run = std::max<int64_t>(1, std::min(run, most));
+    *pieces = (int)std::max<int64_t>(1, (steps + run - 1) / run);
+    *per = (int)((steps + *pieces - 1) / std::max(1, *pieces));
+    *per = std::max(1, *per);
+    *pieces = (int)std::max<int64_t>(1, (steps + *per - 1) / *per);
+}
+
+static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu) {
+    BackPlan p = {};
+    p.make_dz = act || N % 8 != 0;
+    p.pad = K % 8 != 0;
+    p.ldz = up8(N);
+    p.ldk = up8(K);
+    auto tiles = [](int64_t r, int64_t c, int64_t bt) { return ((r + bt - 1) / bt) * ((c + bt - 1) / bt); };
+    // the tile rule of the products with operands stored K-outer, for the tiles
+    // of both products together
+    const int64_t big = tiles(M, K, 256) + tiles(N, K, 256), small = tiles(M, K, 128) + tiles(N, K, 128);
+    const bool use_big = big == num_cu || big * 8 > (int64_t)num_cu * 11 || (big < num_cu && big * 2 >= num_cu && small > num_cu);
+    p.bt = use_big ? 256 : 128;
+    const int64_t steps_w = (M + 63) / 64, steps_x = (N + 63) / 64;
+    const int64_t work = tiles(N, K, p.bt) * steps_w + tiles(M, K, p.bt) * steps_x;
+    const int64_t fair = (work + num_cu - 1) / num_cu;
+    const int64_t least = use_big ? 12 : 24;
+    const int64_t most = 0x7FFFFFFFLL / (128 * std::max(p.ldz, p.ldk));  // steps of 64 rows below 2 GiB
+    cut(steps_w, fair, least, std::max<int64_t>(1, most), &p.pieces_w, &p.per_w);
+    cut(steps_x, fair, least, std::max<int64_t>(1, most), &p.pieces_x, &p.per_x);
+    p.sums_parts = M > 0 && N > 0 ? act_back_parts(M, N, num_cu) : 0;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up256(bytes);
+        return here;
+    };
+    p.off_dz = take(p.make_dz ? M * p.ldz * 2 : 0);
+    p.off_sums = take(p.sums_parts * N * 4);
+    p.off_parts_w = take(p.pieces_w > 1 ? p.pieces_w * N * K * 4 : 0);
+    p.off_parts_x = take(p.pieces_x > 1 ? p.pieces_x * M * K * 4 : 0);
+    p.off_pad = take(p.pad ? (M + N) * p.ldk * 2 : 0);
+    p.bytes = at;
+    return p;
+}
+
+static bool sizes_ok(int64_t M, int64_t N, int64_t K) {
+    // 32-bit buffer offsets inside one panel of 256 rows, and of 64 steps of K
+    const int64_t most = 0x7FFFFFFFLL / 1024;
+    return M <= 0x7FFFFFFF - 256 && N <= most && K <= most;
+}
+
+static int fill_zero(void* out, int64_t n, void* stream) {
+    if (n == 0) return GEMM_BT_OK;
+    u16* p = (u16*)out;
+    long long nn = n;
+    void* args[] = {&p, &nn};
+    return launch((const void*)&fill_zero16_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4096)), 256, args, stream);
+}
+
+static int linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
+                           int64_t M, int64_t N, int64_t K, int act, int type, int preact_type, char* ws, const BackPlan& p,
+                           int num_cu, void* stream) {
+    int st;
+    // dz, and the partial sums of its columns
+    const void* dz = dy;
+    if (p.make_dz || dbias) {
+        if (p.make_dz) dz = ws + p.off_dz;
+        st = launch_act_back({dy, act != GEMM_BT_ACT_NONE ? preact : nullptr, p.make_dz && (dx || dw) ? (void*)dz : nullptr,
+                              dbias ? (float*)(ws + p.off_sums) : nullptr, M, (int)N, (int)p.ldz, 0, type, preact_type, act},
+                             num_cu, stream);
+        if (st != GEMM_BT_OK) return st;
+    }
+    if (p.pad && (dx || dw)) {
+        // X for dW, W for dX: only what is read
+        const u16 *sx = (const u16*)x, *sw = (const u16*)w;
+        long long m = dw ? M : 0, n = dx ? N : 0;
+        u16 *at = (u16*)(ws + p.off_pad), *out = dw ? at : at + M * p.ldk;
+        int k = (int)K, pitch = (int)p.ldk;
+        void* args[] = {&sx, &sw, &out, &m, &n, &k, &pitch};
+        st = launch((const void*)&pad_rows_kernel, dim3((unsigned)std::min<int64_t>(((m + n) * p.ldk / 8 + 255) / 256, 1 << 16)),
+                    256, args, stream);
+        if (st != GEMM_BT_OK) return st;
+        x = at;
+        w = at + M * p.ldk;
+    }
+    auto product = [&](const void* a, const void* b, void* out, float* parts, int64_t rows, int64_t cols, int64_t depth,
+                       int64_t lda, int64_t ldb, int pieces, int per) {
+        BackProduct q = {};
+        if (!out || rows == 0 || cols == 0) return q;
+        q.a = (const u16*)a;
+        q.b = (const u16*)b;
+        q.out = out;
+        q.parts = parts;
+        q.rows = (int)rows;
+        q.cols = (int)cols;
+        q.depth = (int)depth;
+        q.lda = (int)lda;
+        q.ldb = (int)ldb;
+        q.tiles_m = (int)((rows + p.bt - 1) / p.bt);
+        q.tiles_n = (int)((cols + p.bt - 1) / p.bt);
+        q.pieces = pieces;
+        q.per = per;
+        q.blocks = (q.tiles_m * q.tiles_n * pieces + 7) / 8 * 8;
+        q.shifted = cols % 8 != 0 || (uintptr_t)out % 16 != 0;
+        q.shifted_parts = cols % 4 != 0;
+        return q;
+    };
+    BackArgs a = {};
+    a.dw = product(dz, x, dw, (float*)(ws + p.off_parts_w), N, K, M, p.ldz, p.ldk, p.pieces_w, p.per_w);
+    a.dx = product(dz, w, dx, (float*)(ws + p.off_parts_x), M, K, N, p.ldz, p.ldk, p.pieces_x, p.per_x);
+    unsigned grid = (unsigned)(a.dw.blocks + a.dx.blocks);
+    if (dbias) {
+        a.fold = {(const float*)(ws + p.off_sums), dbias, N, (int)p.sums_parts, type};
+        grid += fold_blocks(N);
+    }
+    if (grid == 0) return GEMM_BT_OK;
+    const bool bf = type == GEMM_BT_BF16;
+    const void* fn = p.bt == 256 ? (bf ? (const void*)&linear_back_kernel<GEMM_BT_BF16, 256, 4> : (const void*)&linear_back_kernel<GEMM_BT_F16, 256, 4>)
+                                 : (bf ? (const void*)&linear_back_kernel<GEMM_BT_BF16, 128, 2> : (const void*)&linear_back_kernel<GEMM_BT_F16, 128, 2>);
+    void* args[] = {&a};
+    st = launch(fn, dim3(grid), p.bt == 256 ? 512 : 256, args, stream);
+    if (st != GEMM_BT_OK) return st;
+    SliceArgs s = {};
+    s.type = type;
+    int64_t most = 0;
+    const BackProduct* q[2] = {&a.dw, &a.dx};
+    for (int i = 0; i < 2; ++i)
+        if (q[i]->pieces > 1) {
+            s.parts[i] = q[i]->parts;
+            s.out[i] = q[i]->out;
+            s.n[i] = (long long)q[i]->rows * q[i]->cols;
+            s.pieces[i] = q[i]->pieces;
+            most = std::max<int64_t>(most, s.n[i]);
+        }
+    if (most == 0) return GEMM_BT_OK;
+    void* sargs[] = {&s};
+    return launch((const void*)&slices_kernel, dim3((unsigned)std::min<int64_t>((most + 2047) / 2048, 8 * num_cu)), 256, sargs,
+                  stream);
+}
+
+}  // namespace gbt
+
+using namespace gbt;
+
+extern "C" {
+
+int gemm_bt_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    if (M < 0 || N < 0 || K < 0 || activation < GEMM_BT_ACT_NONE || activation > GEMM_BT_ACT_SILU)
+        return GEMM_BT_ERR_INVALID_VALUE;
+    if (!sizes_ok(M, N, K)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (M > 0 && N > 0) *bytes = (size_t)back_plan(M, N, K, activation != GEMM_BT_ACT_NONE, plan_cus()).bytes;
+    return GEMM_BT_OK;
+}
+
+int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
+                            int64_t M, int64_t N, int64_t K, int activation, int dtype, int preact_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    if (M < 0 || N < 0 || K < 0 || activation < GEMM_BT_ACT_NONE || activation > GEMM_BT_ACT_SILU)
+        return GEMM_BT_ERR_INVALID_VALUE;
+    const bool act = activation != GEMM_BT_ACT_NONE;
+    if ((dtype != GEMM_BT_F16 && dtype != GEMM_BT_BF16) || (act && !float_type(preact_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
+    if (!sizes_ok(M, N, K)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (K == 0) dx = dw = nullptr;  // nothing to write
+    if (M == 0) dx = nullptr;
+    if (N == 0) dw = dbias = nullptr;
+    if (!dx && !dw && !dbias) return GEMM_BT_OK;
+    if (!aligned(dx, dtype) || !aligned(dw, dtype) || !aligned(dbias, dtype)) return GEMM_BT_ERR_INVALID_VALUE;
+    const bool empty = M == 0 || N == 0;  // the sums have no terms
+    if (!empty) {
+        if (!dy || (dx && !w) || (dw && !x) || (act && !preact)) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!aligned(dy, dtype) || (act && !aligned(preact, preact_dtype)) || !aligned(x, dtype) || !aligned(w, dtype))
+            return GEMM_BT_ERR_INVALID_VALUE;
+    }
+    int num_cu = 0;
+    int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    if (empty) {
+        if (dx) st = fill_zero(dx, M * K, stream);
+        if (st == GEMM_BT_OK && dw) st = fill_zero(dw, N * K, stream);
+        if (st == GEMM_BT_OK && dbias) st = fill_zero(dbias, N, stream);
+        return st;
+    }
+    const BackPlan p = back_plan(M, N, K, act, num_cu);
+    if (p.bytes > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < (size_t)p.bytes))
+        return GEMM_BT_ERR_INVALID_VALUE;
+    // the products read whole 16-byte chunks of their operands where they lie
+    auto chunks = [](const void* q) { return (uintptr_t)q % 16 == 0; };
+    if ((dx || dw) && ((!p.make_dz && !chunks(dy)) || (!p.pad && ((dw && !chunks(x)) || (dx && !chunks(w))))))
+        return GEMM_BT_ERR_UNSUPPORTED;
+    return linear_backward(dy, x, w, preact, dx, dw, dbias, M, N, K, activation, dtype, preact_dtype,
+                           (char*)workspace, p, num_cu, stream);
+}
+
+}  // extern "C"

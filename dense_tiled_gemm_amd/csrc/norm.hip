@@ -12,6 +12,7 @@
 
 #include "device.hpp"
 #include "epilogue.hpp"
+#include "rows.hpp"
 
 namespace gbt {
 
@@ -28,20 +29,18 @@ struct MaxBitsOp {
     __device__ static float join(float a, float b) { return as_f32(max(as_u32(a), as_u32(b))); }
 };
 
-// The value joined over the T threads of a row (T = 64: one wave; else the
-// whole workgroup, through `part`), the same for all of them and in an order
-// that depends on T only.
-template <class Op, int T>
+// The value joined over the threads of a row (WAVE: one wave; else the whole
+// workgroup, through `part`), the same for all of them and in an order that
+// depends on their number only.
+template <class Op, bool WAVE>
 __device__ __forceinline__ float row_join(float v, float* part) {
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) v = Op::join(v, __shfl_xor(v, m));
-    if constexpr (T > 64) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) part[wave] = v;
+    if constexpr (!WAVE) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
         v = Op::zero();
-#pragma unroll
-        for (int w = 0; w < T / 64; ++w) v = Op::join(v, part[w]);
+        for (int w = 0; w < (int)blockDim.x >> 6; ++w) v = Op::join(v, part[w]);
     }
     return v;
 }
@@ -94,18 +93,18 @@ __device__ __forceinline__ float row_scale_of(float amax, int qt) {
 // two that brings its largest magnitude near 1.  each(f) calls f on every
 // value of h that the thread holds; `part` has two more rows for the joins.
 // An infinity gives 0, a NaN NaN.
-template <int T, class Each>
+template <bool WAVE, class Each>
 __device__ __forceinline__ float rstd_of(float ss, int d, float eps, float (*part)[16], int flip, Each&& each) {
     const float mean = ss / (float)d + eps;
     if (__builtin_expect(!(mean > 0x1p-90f && mean < __builtin_inff()), 0)) {
         float amax = 0.0f;
         each([&](float v) __attribute__((always_inline)) { amax = MaxBitsOp::join(amax, __builtin_fabsf(v)); });
-        amax = row_join<MaxBitsOp, T>(amax, part[flip]);
+        amax = row_join<MaxBitsOp, WAVE>(amax, part[flip]);
         if (amax > 0.0f && amax < __builtin_inff()) {
             const float s = as_f32((254u - min(as_u32(amax) >> 23, 253u)) << 23);
             float sq = 0.0f;
             each([&](float v) __attribute__((always_inline)) { sq = __builtin_fmaf(v * s, v * s, sq); });
-            sq = row_join<SumOp, T>(sq, part[2 + flip]);
+            sq = row_join<SumOp, WAVE>(sq, part[2 + flip]);
             const float e = eps * s * s;
             return e < __builtin_inff() ? s / __builtin_sqrtf(sq / (float)d + e) : 1.0f / __builtin_sqrtf(eps);
         }
@@ -129,17 +128,18 @@ struct NormArgs {
 
 __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
 
-// T threads hold one row, U chunks of 8 elements each (T * U * 8 >= d); a
-// workgroup of NT threads works on NT / T rows at a time.
-template <int XT, int WT, int T, int U, int NT>
-__global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
-    static_assert(T == NT || T == 64, "a row belongs to a wave or to the workgroup");
-    constexpr int RB = NT / T;
+// The T threads that hold a row, U chunks of 8 elements each (T * U * 8 >= d),
+// are a wave (WAVE; a workgroup is up to 4 of them, each with rows of its own) or
+// the whole workgroup, of as many waves as the row fills.
+template <int XT, int WT, int U, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs a) {
     __shared__ float part[8][16];
-    const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int T = WAVE ? 64 : blockDim.x, RB = WAVE ? blockDim.x >> 6 : 1;
+    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int d = a.d;
     int flip = 0;
-    for (long long row = (long long)blockIdx.x * RB + threadIdx.x / T; row < a.rows; row += (long long)gridDim.x * RB) {
+    for (long long row = (long long)blockIdx.x * RB + (WAVE ? threadIdx.x >> 6 : 0); row < a.rows;
+         row += (long long)gridDim.x * RB) {
         Raw8 xr[U], rr[U], wr[U];
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
@@ -173,8 +173,8 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
         });
         float rstd = 1.0f;
         if (a.weight) {
-            ss = row_join<SumOp, T>(ss, part[flip]);
-            rstd = rstd_of<T>(ss, d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
+            ss = row_join<SumOp, WAVE>(ss, part[flip]);
+            rstd = rstd_of<WAVE>(ss, d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
             }
         });
         if (is_code_type(a.y_type)) {
-            amax = row_join<MaxBitsOp, T>(amax, part[2 + flip]);
+            amax = row_join<MaxBitsOp, WAVE>(amax, part[2 + flip]);
             const float s = row_scale_of(amax, a.y_type), inv = 1.0f / s;
             if (t == 0) a.scale[row] = s;
             static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
@@ -251,8 +251,8 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
             }
-            ss = row_join<SumOp, T>(ss, part[flip]);
-            rstd = rstd_of<T>(ss, a.d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
+            ss = row_join<SumOp, false>(ss, part[flip]);
+            rstd = rstd_of<false>(ss, a.d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
                 for (long long i = t * 8; i < a.d; i += T * 8) {
                     load_h((int)i, min(8, a.d - (int)i), h);
 #pragma unroll
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[e]));
             }
-            amax = row_join<MaxBitsOp, T>(amax, part[2 + flip]);
+            amax = row_join<MaxBitsOp, false>(amax, part[2 + flip]);
             const float s = row_scale_of(amax, a.y_type);
             inv = 1.0f / s;
             if (t == 0) a.scale[row] = s;
@@ -318,13 +318,13 @@ struct NormBackArgs {
 // workgroup leaves one row of partial sums.  AHEAD: the next row is fetched
 // while this one is worked on, and the weight stays in registers; without it
 // (rows that fill the registers) both are read when they are needed.
-template <int XT, int WT, int T, int U, int NT, bool AHEAD>
-__global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
-    static_assert(T == NT || T == 64, "a row belongs to a wave or to the workgroup");
-    constexpr int RB = NT / T;
+template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST>
+__global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
+    constexpr int RB = WAVE ? MOST / 64 : 1;
     __shared__ float part[2][16];
-    __shared__ float joined[RB > 1 ? RB * T * U * 8 : 1];
-    const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+    __shared__ float joined[WAVE ? MOST * U * 8 : 1];
+    const int T = WAVE ? 64 : blockDim.x;
+    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int d = a.d;
     float dw[U][8];
     Raw8 wr[U];
@@ -351,14 +351,14 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 const int n = min(8, d - i);
-                r.dy[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
-                r.h[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n);
-                if (AHEAD && a.dh) r.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
+                r.dy[u] = load_raw8<true>(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
+                r.h[u] = load_raw8<true>(a.h, XT, (size_t)(row * a.ldh) + i, n);
+                if (AHEAD && a.dh) r.dh[u] = load_raw8<true>(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
             }
         });
     };
     int flip = 0;
-    long long row = (long long)blockIdx.x * RB + threadIdx.x / T;
+    long long row = (long long)blockIdx.x * RB + (WAVE ? threadIdx.x >> 6 : 0);
     Row now;
     if constexpr (AHEAD) fetch(row, now);
     for (; row < a.rows; row += step) {
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
                 }
             }
         });
-        c = row_join<SumOp, T>(c, part[flip]) / (float)d;
+        c = row_join<SumOp, WAVE>(c, part[flip]) / (float)d;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(1024) void norm_back_long_kernel(const NormBackArgs
         float c = 0.0f;
         for (long long i = t; i < a.d; i += T)
             c = __builtin_fmaf(load1x(a.dy, a.ld_dy, i) * load1(a.weight, WT, i), load1x(a.h, a.ldh, i) * rstd, c);
-        c = row_join<SumOp, T>(c, part[flip]) / (float)a.d;
+        c = row_join<SumOp, false>(c, part[flip]) / (float)a.d;
         for (long long i = t; i < a.d; i += T) {
             const float dy = load1x(a.dy, a.ld_dy, i), xhat = load1x(a.h, a.ldh, i) * rstd;
             float o = rstd * __builtin_fmaf(-xhat, c, dy * load1(a.weight, WT, i));
@@ -468,50 +468,12 @@ __global__ __launch_bounds__(1024) void norm_back_long_kernel(const NormBackArgs
 
 // ---- column sums: the last step ---------------------------------------------------
 
-// out[j] = sum of the `parts` rows of partial sums, in an order that depends
-// on `parts` only: 16 threads per column take every 16th row, then a tree.
-__global__ __launch_bounds__(256) void fold_kernel(const float* __restrict__ partials, void* out, int out_type, int parts,
-                                                   long long d) {
-    __shared__ float sums[16][17];
-    const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const long long j = (long long)blockIdx.x * 16 + c;
-    float s = 0.0f;
-    if (j < d) {
-        int r = k;
-        for (; r + 7 * 16 < parts; r += 8 * 16) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = partials[(size_t)(r + 16 * e) * d + j];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += v[e];
-        }
-        for (; r < parts; r += 16) s += partials[(size_t)r * d + j];
-    }
-    sums[k][c] = s;
-    __syncthreads();
-    if (k == 0 && j < d) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = sums[i][c];
-#pragma unroll
-        for (int w = 8; w > 0; w >>= 1)
-#pragma unroll
-            for (int i = 0; i < w; ++i) v[i] += v[i + w];
-        store1(out, out_type, (size_t)j, v[0]);
-    }
+__global__ __launch_bounds__(512) void fold_kernel(const FoldArgs a) {
+    __shared__ float sums[512 / 16][17];
+    fold_columns<512>(a, blockIdx.x, sums);
 }
 
 // ---- activation and bias, backward -------------------------------------------------
-
-struct ActBackArgs {
-    const void* dy;
-    const void* preact;  // nullptr: no activation
-    void* dz;            // nullptr: not wanted
-    float* partials;     // nullptr: no column sums; else gridDim.y rows of n sums of dz
-    long long rows;
-    int n, rows_per_block;
-    int type, preact_type, act;
-};
 
 // dz = dy act'(z), and the sums of dz over a block of rows.  L lanes hold 8
 // columns each; a workgroup's 256 / L groups of lanes take its rows in turn.
@@ -539,31 +501,29 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= act_slope<ACT>(z[e]);
                 }
-                if (a.dz) store8(a.dz, a.type, (size_t)(row * a.n) + j, n, v);
+                if (a.dz) store8(a.dz, a.type, (size_t)(row * a.ldz) + j, min(8, a.ldz - j), v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += v[e];
             };
             auto load = [&](long long row, Raw8& dyr, Raw8& zr) __attribute__((always_inline)) {
-                dyr = load_raw8(a.dy, a.type, (size_t)(row * a.n) + j, n);
-                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8(a.preact, a.preact_type, (size_t)(row * a.n) + j, n);
+                dyr = load_raw8<true>(a.dy, a.type, (size_t)(row * a.n) + j, n);
+                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8<true>(a.preact, a.preact_type, (size_t)(row * a.n) + j, n);
             };
+            // four rows in flight: each is fetched again as soon as it is used
+            Raw8 dyr[4], zr[4];
             long long row = first + g;
-            for (; row + 3 * G < last; row += 4 * G) {  // four rows in flight
-                Raw8 dyr[4], zr[4];
+            static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                if (row + u * G < last) load(row + u * G, dyr[u], zr[u]);
+            });
+            for (; row < last; row += 4 * G)
                 static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
                     constexpr int u = decltype(uc)::value;
-                    load(row + u * G, dyr[u], zr[u]);
+                    if (row + u * G < last) {
+                        one(dyr[u], zr[u], row + u * G);
+                        if (row + (u + 4) * G < last) load(row + (u + 4) * G, dyr[u], zr[u]);
+                    }
                 });
-                static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
-                    constexpr int u = decltype(uc)::value;
-                    one(dyr[u], zr[u], row + u * G);
-                });
-            }
-            for (; row < last; row += G) {
-                Raw8 dyr, zr;
-                load(row, dyr, zr);
-                one(dyr, zr, row);
-            }
         });
     if (!a.partials) return;
 #pragma unroll
@@ -582,16 +542,6 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
 
 // ---- host ------------------------------------------------------------------------
 
-static int launch(const void* fn, dim3 grid, int threads, void** args, void* stream) {
-    if (hipLaunchKernel(fn, grid, dim3(threads), args, 0, (hipStream_t)stream) != hipSuccess) {
-        (void)hipGetLastError();
-        return GEMM_BT_ERR_LAUNCH;
-    }
-    return GEMM_BT_OK;
-}
-
-static bool float_type(int t) { return t == GEMM_BT_F32 || t == GEMM_BT_F16 || t == GEMM_BT_BF16; }
-static bool aligned(const void* p, int t) { return (uintptr_t)p % elem_size(t) == 0; }
 static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld < (1LL << 40); }
 
 struct RowPlan {
@@ -599,35 +549,33 @@ struct RowPlan {
     int threads, rows_per_block;
 };
 
+// Whole waves that hold `chunks` groups of 8 elements, U of them per thread.
+static int threads_for(int64_t chunks, int U) { return (int)((chunks + 64 * U - 1) / (64 * U) * 64); }
+
 template <int XT, int WT>
 static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
     const int64_t chunks = (d + 7) / 8;
-    // Few rows: the whole row at once, as many threads as it has chunks, so
-    // that one load's latency is all that is waited for.
-    if (rows <= 2 * num_cu) {
-        if (chunks <= 64) return {(const void*)&norm_kernel<XT, WT, 64, 1, 64>, 64, 1};
-        if (chunks <= 256) return {(const void*)&norm_kernel<XT, WT, 256, 1, 256>, 256, 1};
-        if (chunks <= 512) return {(const void*)&norm_kernel<XT, WT, 512, 1, 512>, 512, 1};
-        if (chunks <= 1024) return {(const void*)&norm_kernel<XT, WT, 1024, 1, 1024>, 1024, 1};
-    }
-    if (chunks <= 64) return {(const void*)&norm_kernel<XT, WT, 64, 1, 256>, 256, 4};
-    if (chunks <= 128) return {(const void*)&norm_kernel<XT, WT, 64, 2, 256>, 256, 4};
-    if (chunks <= 256) return {(const void*)&norm_kernel<XT, WT, 256, 1, 256>, 256, 1};
-    if (chunks <= 512) return {(const void*)&norm_kernel<XT, WT, 256, 2, 256>, 256, 1};
-    if (chunks <= 1024) return {(const void*)&norm_kernel<XT, WT, 512, 2, 512>, 512, 1};
-    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 1024, 2, 1024>, 1024, 1};
+    // Few rows (at most two per CU): one chunk per thread, so that one load's
+    // latency is all that is waited for.
+    const bool few = rows <= 2 * num_cu;
+    if (chunks <= 64)
+        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true>, 64, 1}
+                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true>, 256, 4};
+    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true>, 256, 4};
+    if (chunks <= 256 || (few && chunks <= 1024))
+        return {(const void*)&norm_kernel<XT, WT, 1, false>, threads_for(chunks, 1), 1};
+    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false>, threads_for(chunks, 2), 1};
     return {(const void*)&norm_long_kernel<XT, WT>, 1024, 1};
 }
 
 template <int XT, int WT>
 static RowPlan norm_back_plan(int64_t d) {
     const int64_t chunks = (d + 7) / 8;
-    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 64, 1, 256, true>, 256, 4};
-    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 64, 2, 256, true>, 256, 4};
-    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 256, 1, 256, true>, 256, 1};
-    if (chunks <= 512) return {(const void*)&norm_back_kernel<XT, WT, 256, 2, 256, true>, 256, 1};
-    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 512, 2, 512, true>, 512, 1};
-    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 1024, 2, 1024, false>, 1024, 1};
+    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 1, true, true, 256>, 256, 4};
+    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 2, true, true, 256>, 256, 4};
+    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 1, false, true, 256>, threads_for(chunks, 1), 1};
+    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 2, false, true, 512>, threads_for(chunks, 2), 1};
+    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 2, false, false, 1024>, threads_for(chunks, 2), 1};
     return {(const void*)&norm_back_long_kernel<XT, WT>, 1024, 1};
 }
 
@@ -656,10 +604,15 @@ static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
 static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
     return with_types(x_type, w_type, [&](auto x, auto w) { return norm_back_plan<x(), w()>(d); });
 }
-// Workgroups of the backward pass, each of which leaves one row of partial sums.
+// Workgroups of the backward pass, each of which leaves one row of partial
+// sums: about 512 threads per CU, and the same number of rows for all of them
+// but the last ones.  (8192 x 4096 bf16, us: 512 threads per CU 53.6, 768 59.0,
+// 1024 63.6; 16384 x 1024 28.3, 29.6, 32.6: more workgroups do not read faster,
+// and each leaves d fp32 sums more to write and fold.)
 static int64_t norm_back_grid(const RowPlan& p, int64_t rows, int num_cu) {
-    const int64_t most = (int64_t)num_cu * std::max(1, 512 / p.threads);
-    return std::min<int64_t>((rows + p.rows_per_block - 1) / p.rows_per_block, most);
+    const int64_t most = std::max<int64_t>(num_cu, (int64_t)num_cu * 512 / p.threads) * p.rows_per_block;
+    const int64_t per = (rows + most - 1) / most * p.rows_per_block;  // rows of a workgroup
+    return per > 0 ? (rows + per - 1) / per : 0;
 }
 
 // Row blocks of the activation's backward pass (the grid's second axis).
@@ -677,7 +630,9 @@ static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu) {
     else p.fn = (const void*)&act_back_kernel<64>;
     const int groups = 256 / lanes;  // rows a workgroup takes at a time
     p.strips = (n + lanes * 8 - 1) / (lanes * 8);
-    // about four workgroups per CU, each with whole rounds of its groups
+    // about four workgroups per CU, each with whole rounds of its groups (4096 x
+    // 4096 bf16, gelu_tanh, us: two per CU 34.1, four 26.3, eight 28.5, which
+    // also leave twice the partial sums)
     const int64_t want = std::max<int64_t>(1, 4 * num_cu / p.strips);
     int64_t per = (rows + want - 1) / want;
     per = std::max<int64_t>(groups, (per + groups - 1) / groups * groups);
@@ -691,10 +646,18 @@ static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu) {
 }
 
 static int fold(const float* partials, void* out, int out_type, int64_t parts, int64_t d, void* stream) {
-    int np = (int)parts;
-    long long dd = d;
-    void* args[] = {&partials, &out, &out_type, &np, &dd};
-    return launch((const void*)&fold_kernel, dim3((unsigned)((d + 15) / 16)), 256, args, stream);
+    FoldArgs a = {partials, out, d, (int)parts, out_type};
+    void* args[] = {&a};
+    return launch((const void*)&fold_kernel, dim3(fold_blocks(d)), 512, args, stream);
+}
+
+int64_t act_back_parts(int64_t rows, int64_t n, int num_cu) { return act_back_plan(rows, n, num_cu).blocks; }
+
+int launch_act_back(ActBackArgs a, int num_cu, void* stream) {
+    const ActBackPlan p = act_back_plan(a.rows, a.n, num_cu);
+    a.rows_per_block = p.rows_per_block;
+    void* args[] = {&a};
+    return launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
 }
 
 }  // namespace gbt
@@ -804,13 +767,11 @@ int gemm_bt_act_backward(const void* dy, const void* preact, void* dz, void* dbi
     if (st != GEMM_BT_OK) return st;
     int64_t parts = 0;
     if (rows > 0) {
-        const ActBackPlan p = act_back_plan(rows, n, num_cu);
-        parts = p.blocks;
+        parts = act_back_parts(rows, n, num_cu);
         if (dbias && workspace_bytes < (size_t)(parts * n * 4)) return GEMM_BT_ERR_INVALID_VALUE;
-        ActBackArgs a = {dy,      act ? preact : nullptr, dz,    dbias ? (float*)workspace : nullptr, rows, (int)n, p.rows_per_block,
-                         dtype, preact_dtype,           activation};
-        void* args[] = {&a};
-        st = launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
+        st = launch_act_back({dy, act ? preact : nullptr, dz, dbias ? (float*)workspace : nullptr, rows, (int)n, (int)n, 0, dtype,
+                              preact_dtype, activation},
+                             num_cu, stream);
         if (st != GEMM_BT_OK) return st;
     }
     return dbias ? fold((const float*)workspace, dbias, bias_dtype, parts, n, stream) : GEMM_BT_OK;

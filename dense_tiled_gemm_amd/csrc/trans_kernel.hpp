@@ -59,42 +59,36 @@ struct OpGeom {
     static constexpr int BYTES = ROWS * ROWB;
 };
 
+// One tile of one product, or of a range of its K: the tile at rows m0,
+// columns n0 of C, summed over k in [0, K) of operands that start there.  lda
+// and ldb are the row pitches in elements (A: M or K of the whole matrix, or
+// more; likewise B).  `lds` holds 2 * (GA + GB) bytes.  A K-inner row of K
+// elements is read in whole 16-byte chunks, so with K % 8 != 0 its pitch
+// covers them and the elements past K are zeros; a K-outer row likewise past
+// M or N, with any values there.
 template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void trans_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
-                                                             void* __restrict__ C, int M, int N, int K, int tiles_m,
-                                                             int tiles_n, int group_m, int vec_store, int item_tiles_m,
-                                                             long long sa, long long sb, long long sc) {
+__device__ __forceinline__ void trans_body(const u16* A, const u16* B, void* C, int M, int N, int K, int lda, int ldb,
+                                           int m0, int n0, bool shifted, unsigned char* lds) {
     constexpr int T = 64 * WM * WN, BK = 64;
     constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
     typedef OpGeom<BM, TA> GA;
     typedef OpGeom<BN, TB> GB;
     constexpr int STAGE = GA::BYTES + GB::BYTES;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform (LDS-DMA base)
     const int wm = wave / WN, wn = wave % WN;
 
-    int64_t tm64, tn64;
-    tile_coord(blockIdx.x, tiles_m, tiles_n, group_m, &tm64, &tn64);
-    if (tiles_m != item_tiles_m) {
-        // batch items are stacked along the tile rows, as in dma_kernel
-        const int z = (int)tm64 / item_tiles_m;
-        tm64 -= (int64_t)z * item_tiles_m;
-        batch_item(z, A, B, C, sa, sb, sc);
-    }
-    const int m0 = (int)tm64 * BM, n0 = (int)tn64 * BN;
-
     // Global view of one operand as four buffer-resource words: rows past the
     // extent (K-inner) or the matrix end (K-outer) read as zero.
-    auto make_src = [&](const u16* X, int x0, int ext, bool kouter, int bx) {
+    auto make_src = [&](const u16* X, int x0, int ext, int ld, bool kouter, int bx) {
         if (kouter)
-            return rsrc_words(X + x0, (u32)min(((size_t)K * ext - x0) * 2, (size_t)0x7FFFFFFF));
-        return rsrc_words(X + (size_t)x0 * K, (u32)min(bx, ext - x0) * (u32)K * 2u);
+            return rsrc_words(X + x0, (u32)min(((size_t)K * ld - x0) * 2, (size_t)0x7FFFFFFF));
+        return rsrc_words(X + (size_t)x0 * ld, (u32)((min(bx, ext - x0) - 1) * (u32)ld + (u32)((K + 7) & ~7)) * 2u);
     };
-    const i32x4 ra = make_src(A, m0, M, TA, BM);
-    const i32x4 rb = make_src(B, n0, N, TB, BN);
+    const i32x4 ra = make_src(A, m0, M, lda, TA, BM);
+    const i32x4 rb = make_src(B, n0, N, ldb, TB, BN);
     const int lim_a = M - m0, lim_b = N - n0;
 
     // Loader: LDS-DMA, one 1 KiB block (RPI = 1024 / ROWB rows) per wave
@@ -116,12 +110,12 @@ __global__ __launch_bounds__(64 * WM * WN) void trans_kernel(const u16* __restri
             const int row = blk * RPI + lane / G::CR;
             u32 off;
             if constexpr (KO) {
-                // row = k within the step; ld_bytes = the operand's row pitch (2 * M or 2 * N)
+                // row = k within the step; ld_bytes = the operand's row pitch
                 const int c = lc ^ kouter_swz(row);
                 const int k = kt * BK + row;
                 off = (k < K && c * 8 < lim) ? (u32)k * ld_bytes + (u32)c * 16u : kOutOfRange;
             } else {
-                // row = tile row; ld_bytes = 2 * K
+                // row = tile row
                 const int c = lc ^ ((row >> 1) & 7);
                 const int kc = kt * BK + c * 8;
                 off = kc < K ? (u32)row * ld_bytes + (u32)kc * 2u : kOutOfRange;
@@ -133,8 +127,8 @@ __global__ __launch_bounds__(64 * WM * WN) void trans_kernel(const u16* __restri
     typedef std::integral_constant<bool, TB> KB;
     auto issue = [&](int stage, int kt) {
         unsigned char* base = lds + stage * STAGE;
-        issue_op(ra, base, GA(), KA(), kt, lim_a, TA ? (u32)M * 2u : (u32)K * 2u);
-        issue_op(rb, base + GA::BYTES, GB(), KB(), kt, lim_b, TB ? (u32)N * 2u : (u32)K * 2u);
+        issue_op(ra, base, GA(), KA(), kt, lim_a, (u32)lda * 2u);
+        issue_op(rb, base + GA::BYTES, GB(), KB(), kt, lim_b, (u32)ldb * 2u);
     };
 
     // Fragment reads for k-substep ks (32 k) of the 16-row/column block at x
@@ -206,7 +200,25 @@ __global__ __launch_bounds__(64 * WM * WN) void trans_kernel(const u16* __restri
     // the loop ended on a barrier: LDS is free for the whole-row epilogue
     // (shifted when rows of C are not 16-byte aligned)
     store_tile_lds<OUT, FN, FM, BM, BN, WM, T, 2 * STAGE, 16>(acc, lds, C, M, N, m0, n0, wm * TM, wn * TN, wm, tid,
-                                                             vec_store != 2);
+                                                             shifted);
+}
+
+template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void trans_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
+                                                             void* __restrict__ C, int M, int N, int K, int tiles_m,
+                                                             int tiles_n, int group_m, int vec_store, int item_tiles_m,
+                                                             long long sa, long long sb, long long sc) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * (OpGeom<BM, TA>::BYTES + OpGeom<BN, TB>::BYTES)];
+    int64_t tm64, tn64;
+    tile_coord(blockIdx.x, tiles_m, tiles_n, group_m, &tm64, &tn64);
+    if (tiles_m != item_tiles_m) {
+        // batch items are stacked along the tile rows, as in dma_kernel
+        const int z = (int)tm64 / item_tiles_m;
+        tm64 -= (int64_t)z * item_tiles_m;
+        batch_item(z, A, B, C, sa, sb, sc);
+    }
+    trans_body<IN, OUT, TA, TB, BM, BN, WM, WN>(A, B, C, M, N, K, TA ? M : K, TB ? N : K, (int)tm64 * BM, (int)tn64 * BN,
+                                                vec_store != 2, lds);
 }
 
 }  // namespace gbt

@@ -7,13 +7,13 @@ leading dimensions.  Rows may lie any number of elements apart; other layouts ar
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, INT32, K_INNER, K_OUTER, OK, GemmBtError, gemm_bt_workspace_size,
-               load, mm_layout, workspace_for)
+from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, INT32, OK, GemmBtError, gemm_bt_workspace_size, load, workspace_for
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
@@ -50,11 +50,11 @@ class LinearGrads(NamedTuple):
     dbias: Optional[torch.Tensor]
 
 
-def _on_gpu(*tensors):
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise ValueError("expected tensors on a GPU, got %s" % device)
-    for t in tensors:
+def _on_gpu(first, *others):
+    if not first.is_cuda:
+        raise ValueError("expected tensors on a GPU, got %s" % first.device)
+    device = first.device
+    for t in others:
         if t is not None and t.device != device:
             raise ValueError("all tensors must be on the same GPU")
     return device
@@ -67,13 +67,12 @@ def _check(status, what):
 
 def _rows(t, what="x"):
     """(tensor, row stride) of (..., d) seen as (rows, d) without a copy where the rows are evenly spaced."""
-    if t.dim() == 0:
-        raise ValueError("%s needs at least one dimension" % what)
-    if t.dim() == 2:
-        if t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
-            return t, t.stride(0)
-    elif t.is_contiguous():
+    if t.is_contiguous():
+        if t.dim() == 0:
+            raise ValueError("%s needs at least one dimension" % what)
         return t, t.shape[-1]
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t, t.stride(0)
     return t.contiguous(), t.shape[-1]
 
 
@@ -81,27 +80,23 @@ def _dense(t):
     return t if t.is_contiguous() else t.contiguous()
 
 
-class _on:
-    """The device and stream of a call: switches the current device only if it is another one."""
+def _chunked(t):
+    """t with dense rows from a 16-byte boundary on."""
+    t = _dense(t)
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
-    __slots__ = ("device", "guard")
 
-    def __init__(self, device):
-        self.device = device
-        self.guard = None
+_HERE = contextlib.nullcontext()
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _on(device):
+    """The context of a call on `device`: one that switches to it only if it is not the current device."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _stream(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+    # the handle alone: torch.cuda.current_stream would build a Stream object around it on every call (1.9 us)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
 
 
 def _ptr(t):
@@ -119,9 +114,9 @@ def _same_shape(t, x, what):
         raise ValueError("%s must be a %s tensor of shape %s" % (what, x.dtype, tuple(x.shape)))
 
 
-def _output(out, shape, dtype, device, what="out"):
+def _output(out, like, shape, dtype, device, what="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or not out.is_contiguous() or out.device != device:
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
     return out
@@ -153,10 +148,10 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, save_rstd=F
     xr, ldx = _rows(x)
     rr, ldr = (None, 0) if residual is None else _rows(residual, "residual")
     rows = x.numel() // d if d else 0
-    y = _output(out, x.shape, y_dtype, device)
-    h = None if residual is None else _output(h_out, x.shape, x.dtype, device, "h_out")
-    scale = torch.empty(lead, dtype=torch.float32, device=device) if y_dtype in _EIGHT else None
-    rstd = torch.empty(lead, dtype=torch.float32, device=device) if save_rstd else None
+    y = _output(out, x, x.shape, y_dtype, device)
+    h = None if residual is None else _output(h_out, x, x.shape, x.dtype, device, "h_out")
+    scale = x.new_empty(lead, dtype=torch.float32) if y_dtype in _EIGHT else None
+    rstd = x.new_empty(lead, dtype=torch.float32) if save_rstd else None
     with _on(device):
         _check(load().gemm_bt_rms_norm(xr.data_ptr(), ldx, _ptr(rr), ldr, _dense(weight).data_ptr(), y.data_ptr(), _ptr(h),
                                        _ptr(scale), _ptr(rstd), rows, d, eps, x_code, _CODES[weight.dtype],
@@ -172,8 +167,8 @@ def quantize_rows(x, dtype=torch.float8_e4m3fn, stream=None):
         raise TypeError("dtype must be float8_e4m3fn or int8, got %s" % dtype)
     xr, ldx = _rows(x)
     d = x.shape[-1]
-    q = torch.empty(x.shape, dtype=dtype, device=device)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    q = x.new_empty(x.shape, dtype=dtype)
+    scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     with _on(device):
         _check(load().gemm_bt_quantize_rows(xr.data_ptr(), ldx, q.data_ptr(), scale.data_ptr(), x.numel() // d if d else 0,
                                             d, x_code, _CODES[dtype], _stream(device, stream)), "gemm_bt_quantize_rows")
@@ -198,14 +193,14 @@ def add_rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     dyr, ld_dy = _rows(dy, "dy")
     hr, ldh = _rows(h, "h")
     dhr, ld_dh = (None, 0) if dh is None else _rows(dh, "dh")
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=device)
-    dw = torch.empty(d, dtype=weight.dtype, device=device)
+    dx = dy.new_empty(dy.shape)
+    dw = weight.new_empty(d)
     lib = load()
     with _on(device):
         s = _stream(device, stream)
         need = ctypes.c_size_t()
         _check(lib.gemm_bt_rms_norm_backward_workspace(rows, d, ctypes.byref(need)), "gemm_bt_rms_norm_backward_workspace")
-        ws = _scratch(device, s, need.value)
+        ws = _scratch(dy, s, need.value)
         _check(lib.gemm_bt_rms_norm_backward(dyr.data_ptr(), ld_dy, hr.data_ptr(), ldh, _dense(weight).data_ptr(),
                                              _dense(rstd).data_ptr(), _ptr(dhr), ld_dh, dx.data_ptr(), dw.data_ptr(), rows,
                                              d, code, _CODES[weight.dtype], _ptr(ws), need.value, s),
@@ -213,13 +208,13 @@ def add_rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     return dx, dw
 
 
-def _scratch(device, stream, nbytes):
+def _scratch(like, stream, nbytes):
     """Working memory of one call, on its stream: torch may hand it out again after that stream has passed the call."""
     if nbytes == 0:
         return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream != torch.cuda.current_stream(device).cuda_stream:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    if stream != torch._C._cuda_getCurrentRawStream(like.device.index):
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
     return ws
 
 
@@ -276,10 +271,10 @@ def linear(x, weight, bias=None, activation="none", residual=None, x_scale=None,
             t = _dense(t)
             keep.append(t)
             setattr(e, name, t.data_ptr())
-    y = _output(out, shape, y_dtype, device)
+    y = _output(out, x, shape, y_dtype, device)
     z = None
     if save_preact:
-        z = torch.empty(shape, dtype=wide, device=device)
+        z = x.new_empty(shape, dtype=wide)
         e.preact = z.data_ptr()
         e.preact_dtype = _CODES[wide]
     out_code = _CODES[y_dtype]
@@ -300,7 +295,7 @@ def linear_backward(dy, x, weight, preact=None, activation="none", bias_grad=Tru
     """The gradients of linear's x, weight and bias for 16-bit x and weight: LinearGrads(dx, dweight, dbias).
 
     dy (..., N): the gradient of the result, of x's type; preact: what linear returned with save_preact (not needed
-    for the activation "none").  N and K must be multiples of 8.  The gradient of the residual is dy itself.
+    for the activation "none").  The gradient of the residual is dy itself.
     """
     device = _on_gpu(dy, x, weight, preact)
     if not (x.dtype == weight.dtype == dy.dtype) or x.dtype not in (torch.float16, torch.bfloat16):
@@ -308,34 +303,28 @@ def linear_backward(dy, x, weight, preact=None, activation="none", bias_grad=Tru
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1] or dy.shape != x.shape[:-1] + (weight.shape[0],):
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1] or dy.shape != x.shape[:-1] + weight.shape[:1]:
         raise ValueError("expected dy (..., N), x (..., K) and weight (N, K), got %s, %s and %s"
                          % (tuple(dy.shape), tuple(x.shape), tuple(weight.shape)))
-    if act and (preact is None or preact.shape != dy.shape):
-        raise ValueError("preact must be the pre-activation that linear returned, of shape %s" % (tuple(dy.shape),))
+    code = z_code = _CODES[dy.dtype]
+    if act:
+        if preact is None or preact.shape != dy.shape:
+            raise ValueError("preact must be the pre-activation that linear returned, of shape %s" % (tuple(dy.shape),))
+        z_code = _float_code(preact, "preact")
+        preact = _dense(preact)
     N, K = weight.shape
     M = dy.shape[:-1].numel()
-    code = _CODES[dy.dtype]
-    dy, x, weight = _dense(dy), _dense(x), _dense(weight)
-    dz, dbias = dy, None
-    if act or bias_grad:
-        lib = load()
-        if act:
-            preact = _dense(preact)
-            z_code = _float_code(preact, "preact")
-            dz = torch.empty_like(dy)
-        if bias_grad:
-            dbias = torch.empty(N, dtype=weight.dtype, device=device)
-        with _on(device):
-            s = _stream(device, stream)
-            need = ctypes.c_size_t()
-            if bias_grad:
-                _check(lib.gemm_bt_act_backward_workspace(M, N, ctypes.byref(need)), "gemm_bt_act_backward_workspace")
-            ws = _scratch(device, s, need.value)
-            _check(lib.gemm_bt_act_backward(dy.data_ptr(), preact.data_ptr() if act else None,
-                                            dz.data_ptr() if act else None, _ptr(dbias), M, N, act, code,
-                                            z_code if act else code, code, _ptr(ws), need.value, s), "gemm_bt_act_backward")
-    dz2, x2 = dz.reshape(M, N), x.reshape(M, K)
-    dx = mm_layout(dz2, weight, K_INNER, K_OUTER, stream=stream).reshape(x.shape) if need_dx else None
-    dw = mm_layout(dz2, x2, K_OUTER, K_OUTER, stream=stream) if need_dweight else None
-    return LinearGrads(dx, dw, dbias)
+    dy, x, weight = _chunked(dy), _chunked(x), _chunked(weight)
+    dx = x.new_empty(x.shape) if need_dx else None
+    dw = weight.new_empty((N, K)) if need_dweight else None
+    db = weight.new_empty(N) if bias_grad else None
+    lib = load()
+    with _on(device):
+        s = _stream(device, stream)
+        need = ctypes.c_size_t()
+        _check(lib.gemm_bt_linear_backward_workspace(M, N, K, act, ctypes.byref(need)), "gemm_bt_linear_backward_workspace")
+        ws = _scratch(dy, s, need.value)
+        _check(lib.gemm_bt_linear_backward(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), preact.data_ptr() if act else None,
+                                           _ptr(dx), _ptr(dw), _ptr(db), M, N, K, act, code, z_code, _ptr(ws), need.value, s),
+               "gemm_bt_linear_backward")
+    return LinearGrads(dx, dw, db)

@@ -309,8 +309,7 @@ int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
 /*
  * The backward pass of gemm_bt_epi's activation and bias:
  *   dz = dy * act'(preact),   dbias = sum over rows of dz
- * (the gradients of A and B are then products of dz, gemm_bt_batched_layout's
- * operands stored K-outer; that of the residual is dy itself).
+ * (gemm_bt_linear_backward is this with the gradients of A and B).
  *   preact  rows x n of preact_dtype as gemm_bt_epi left it (not read for GEMM_BT_ACT_NONE)
  *   dz      rows x n of dtype, or NULL; may be dy itself
  *   dbias   n elements of bias_dtype, or NULL (then no workspace is needed)
@@ -320,6 +319,31 @@ int gemm_bt_act_backward(const void* dy, const void* preact, void* dz, void* dbi
                          int activation, int dtype, int preact_dtype, int bias_dtype, void* workspace,
                          size_t workspace_bytes, void* stream);
 int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes);
+
+/*
+ * The whole backward pass of C = act(X W^T + bias) for 16-bit X (M x K) and W
+ * (N x K), dy the gradient of C (M x N), all of dtype GEMM_BT_F16 or _BF16:
+ *   dz = dy * act'(preact), rounded into dtype (dy itself for GEMM_BT_ACT_NONE)
+ *   dx = dz W,   dw = dz^T X,   dbias = sum over rows of dz before its rounding
+ * Sums are held in fp32 and rounded once.  X, W and dy are read as they lie in
+ * memory: nothing is transposed or copied but rows that are not whole 16-byte
+ * chunks (N or K not a multiple of 8), which are padded in the workspace.  A
+ * product whose sum is long and whose result is small is cut along the sum
+ * into fp32 slices that are added in order, so results are the same bits on
+ * every run on the same device.
+ *   preact     M x N of preact_dtype, as gemm_bt_epi left it (activation NONE: not read)
+ *   dx, dw, dbias  M x K, N x K and N elements of dtype; NULL: not wanted
+ *   workspace  at least gemm_bt_linear_backward_workspace bytes, 16-byte
+ *              aligned, any contents
+ * N and K up to 2^21 - 1.  x, w and (for GEMM_BT_ACT_NONE with N % 8 == 0) dy
+ * need 16-byte alignment where K % 8 == 0 (else UNSUPPORTED); the rest needs
+ * the alignment of its elements.  A gradient whose sum has no terms is zeros.
+ * The gradient of an epilogue's residual is dy itself.
+ */
+int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw,
+                            void* dbias, int64_t M, int64_t N, int64_t K, int activation, int dtype,
+                            int preact_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int gemm_bt_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes);
 
 /* Workspace gemm_bt_ws needs for these sizes and types (0 when it runs the
    plain grid), for the current device (256 compute units without one).  At

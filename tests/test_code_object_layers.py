@@ -21,7 +21,7 @@ def test_no_kernel_of_any_source_uses_scratch(tmp_path):
     subprocess.run([TOOLS[0], "--dump-section=.hip_fatbin=" + fat, gb.LIB_PATH, os.devnull], check=True)
     data = open(fat, "rb").read()
     starts = [m.start() for m in re.finditer(MAGIC, data)]
-    assert len(starts) == 3, starts  # one bundle per source
+    assert len(starts) == 4, starts  # one bundle per source
     seen = []
     for i, (at, end) in enumerate(zip(starts, starts[1:] + [len(data)])):
         part, co = str(tmp_path / ("part%d.bin" % i)), str(tmp_path / ("part%d.co" % i))
@@ -37,5 +37,5 @@ def test_no_kernel_of_any_source_uses_scratch(tmp_path):
             assert field("vgpr_count") <= 256, name
             seen.append(name)
     for kernel in ("norm_kernel", "norm_back_kernel", "norm_long_kernel", "act_back_kernel", "fold_kernel", "skinny_epi_kernel",
-                   "epi_fill_kernel", "dma_kernel", "trans_kernel"):
+                   "epi_fill_kernel", "linear_back_kernel", "slices_kernel", "pad_rows_kernel", "dma_kernel", "trans_kernel"):
         assert any(kernel in n for n in seen), kernel

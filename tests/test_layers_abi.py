@@ -115,6 +115,35 @@ def test_act_backward_refusals(kw, want):
     assert act_back(**kw) == want
 
 
+def lin_back(dy=16, x=16, w=16, z=16, dx=16, dw=16, db=16, M=4, N=8, K=8, act=1, t=gb.BF16, zt=gb.BF16, ws=16, nbytes=1 << 30):
+    return int(gb.load().gemm_bt_linear_backward(dy, x, w, z, dx, dw, db, M, N, K, act, t, zt, ws, nbytes, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=-1), BAD), (dict(act=9), BAD), (dict(t=gb.F32), UNSUP),
+    (dict(zt=gb.INT8), UNSUP), (dict(N=1 << 21), UNSUP), (dict(K=1 << 21), UNSUP), (dict(dy=None), BAD), (dict(x=None), BAD),
+    (dict(w=None), BAD), (dict(z=None), BAD), (dict(dx=17), BAD), (dict(dw=17), BAD), (dict(db=17), BAD), (dict(x=17), BAD),
+    (dict(z=17), BAD), (dict(dx=None, dw=None, db=None), gb.OK), (dict(M=0, dw=None, db=None, dy=None), gb.OK),
+    (dict(N=0, dx=None, dy=None), gb.OK), (dict(K=0, db=None, dy=None), gb.OK),
+])
+def test_linear_backward_refusals(kw, want):
+    assert lin_back(**kw) == want
+
+
+def test_linear_backward_workspace():
+    lib, n = gb.load(), ctypes.c_size_t()
+    size = lambda *a: (lib.gemm_bt_linear_backward_workspace(*a, ctypes.byref(n)), n.value)
+    assert lib.gemm_bt_linear_backward_workspace(4, 8, 8, 0, None) == BAD
+    assert size(-1, 8, 8, 0) == (BAD, 0) and size(4, 8, 8, 7) == (BAD, 0) and size(4, 1 << 21, 8, 0) == (UNSUP, 0)
+    assert size(0, 8, 8, 1) == (gb.OK, 0)
+    assert size(4096, 4096, 4096, 3)[1] >= 4096 * 4096 * 2            # dz
+    assert size(4096, 4096, 4096, 0)[1] < 4096 * 4096 * 2             # dy is dz
+    assert size(100, 9, 8, 0)[1] >= 100 * 16 * 2                      # padded rows of dz
+    assert size(100, 8, 9, 0)[1] >= (100 + 8) * 16 * 2                # padded rows of x and w
+    # operands past 2 GiB: cut along the sum even where nothing else asks for it
+    assert size(1 << 20, 4096, 4096, 0)[1] >= 4 * 4096 * 4096 * 4
+
+
 def test_workspace_sizes():
     lib, n = gb.load(), ctypes.c_size_t()
     for f in (lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward_workspace):

@@ -393,7 +393,7 @@ def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False,
 # (M, N, K): every tile shape of the 16-bit kernels, ragged edges, K tails, odd rows of C
 SHAPES16 = [(1, 1, 1), (1, 64, 64), (3, 9, 17), (16, 200, 520), (16, 33, 4097), (17, 33, 65), (24, 4096, 8192), (31, 63, 127),
             (64, 64, 64), (64, 4100, 8192), (100, 2050, 134), (130, 264, 73), (257, 513, 129), (300, 700, 1000),
-            (512, 512, 16384), (520, 1000, 16392), (700, 3200, 130), (1000, 1000, 136), (1000, 2999, 72), (1000, 3000, 136),
+            (512, 512, 16384), (1024, 1024, 16384), (520, 1000, 16392), (700, 3200, 130), (1000, 1000, 136), (1000, 2999, 72), (1000, 3000, 136),
             (1000, 3000, 128), (1030, 1030, 202), (2000, 4000, 192), (2048, 1536, 72), (2048, 4004, 72), (3000, 1000, 72),
             (3000, 1000, 128), (4096, 4096, 130), (4100, 4100, 136), (4352, 4096, 64), (700, 2000, 1000), (1024, 4096, 128)]
 
@@ -577,11 +577,55 @@ def check_backward(gpu, M, N, K, dt, act, bias=True, seed=0):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (5, 64, 72), (17, 8, 512), (100, 256, 264), (333, 1000, 520), (1000, 512, 2048),
-                                   (2049, 1024, 72), (257, 4096, 1024)])
+                                   (2049, 1024, 72), (257, 4096, 1024),
+                                   # rows that are not whole 16-byte chunks: N, K or both
+                                   (1, 1, 1), (33, 9, 7), (64, 100, 130), (200, 1001, 64), (200, 64, 1001), (511, 2050, 333),
+                                   # 256 x 256 tiles; sums cut into slices, of either product and of both
+                                   (2048, 2048, 2050), (4096, 4096, 128), (5000, 64, 200), (70, 5000, 136), (9000, 513, 520),
+                                   (100, 9000, 264), (6000, 6000, 128), (40000, 520, 512)])
 def test_linear_backward(gpu, M, N, K):
     for i, (dt, act) in enumerate(itertools.product(("bf16", "f16"), ACTS)):
-        if (M + i) % 2 == 0 or M < 100:
+        if (M + i) % 2 == 0 and (M * N * K < 1e8 or i in (1, 2, 8)) or M < 100:
             check_backward(gpu, M, N, K, dt, act, bias=i % 3 != 0, seed=M + i)
+
+
+def test_linear_backward_slices_are_planned(gpu):
+    """The sizes above include products cut along their sums: the workspace holds their fp32 slices."""
+    import ctypes
+
+    n = ctypes.c_size_t()
+    size = lambda M, N, K: (gpu.load().gemm_bt_linear_backward_workspace(M, N, K, 0, ctypes.byref(n)), n.value)[1]
+    # besides the slices: partial sums of the bias, at most one row per row of dy
+    for M, N, K, result in ((5000, 64, 200, 64 * 200), (40000, 520, 512, 520 * 512)):   # dw = a sum over M
+        assert size(M, N, K) >= 2 * result * 4 + 4 * N
+    for M, N, K, result in ((70, 5000, 136, 70 * 136), (100, 9000, 264, 100 * 264)):     # dx = a sum over N
+        assert size(M, N, K) >= 2 * result * 4 + 4 * N
+    assert size(4096, 4096, 4096) <= 4096 * 4 * 4096  # not cut
+
+
+def test_linear_backward_parts_and_places(gpu):
+    """Each gradient alone, inputs that start off a 16-byte boundary, leading dimensions; the same bits on every run."""
+    for M, N, K in ((70, 96, 130), (300, 512, 256), (5000, 64, 200)):
+        dy, x, w, z = (randn(i, *s, std=0.3, dtype=torch.bfloat16).cuda() for i, s in enumerate(((M, N), (M, K), (N, K), (M, N))))
+        for act in ("none", "silu"):
+            p = z if act != "none" else None
+            whole = gpu.linear_backward(dy, x, w, preact=p, activation=act)
+            again = gpu.linear_backward(dy, x, w, preact=p, activation=act)
+            assert all(torch.equal(a, b) for a, b in zip(whole, again))
+            for i, kw in enumerate((dict(bias_grad=False, need_dweight=False), dict(bias_grad=False, need_dx=False),
+                                    dict(need_dx=False, need_dweight=False))):
+                part = gpu.linear_backward(dy, x, w, preact=p, activation=act, **kw)
+                assert torch.equal(part[i], whole[i]) and [g is None for g in part] == [j != i for j in range(3)]
+            off = []
+            for t in (dy, x, w, z):
+                buf = torch.zeros(t.numel() + 3, dtype=t.dtype, device="cuda")
+                buf[3:] = t.flatten()
+                off.append(buf[3:].view(t.shape))
+            moved = gpu.linear_backward(off[0], off[1], off[2], preact=off[3] if p is not None else None, activation=act)
+            assert all(torch.equal(a, b) for a, b in zip(whole, moved))
+            cube = gpu.linear_backward(dy.view(2, M // 2, N), x.view(2, M // 2, K), w, preact=None if p is None else p.view(2, M // 2, N),
+                                       activation=act)
+            assert cube.dx.shape == (2, M // 2, K) and torch.equal(cube.dx.view(M, K), whole.dx) and torch.equal(cube.dweight, whole.dweight)
 
 
 def test_linear_gradient_against_differences(gpu):
