@@ -43,7 +43,8 @@ EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layo
            "gemm_bt_plan_batched_layout", "gemm_bt_tile_coord", "gemm_bt_ws", "gemm_bt_workspace_size",
            "gemm_bt_plan_ws", "gemm_bt_noalloc", "gemm_bt_epi", "gemm_bt_rms_norm", "gemm_bt_rms_norm_backward",
            "gemm_bt_rms_norm_backward_workspace", "gemm_bt_quantize_rows", "gemm_bt_act_backward",
-           "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace")
+           "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace",
+           "gemm_bt_epi_workspace_size", "gemm_bt_plan_epi")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -122,7 +123,9 @@ def load():
             lib.gemm_bt_act_backward_workspace.argtypes = [i64, i64, szp]
             lib.gemm_bt_linear_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp, sz, vp]
             lib.gemm_bt_linear_backward_workspace.argtypes = [i64, i64, i64, ci, szp]
-            for f in (lib.gemm_bt_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
+            lib.gemm_bt_epi_workspace_size.argtypes = [i64, i64, i64, ci, ci, szp]
+            lib.gemm_bt_plan_epi.argtypes = [i64, i64, i64, ci, ci, ci, ci, ci, ctypes.POINTER(Plan)]
+            for f in (lib.gemm_bt_epi, lib.gemm_bt_epi_workspace_size, lib.gemm_bt_plan_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
                       lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
                       lib.gemm_bt_act_backward_workspace, lib.gemm_bt_linear_backward,
                       lib.gemm_bt_linear_backward_workspace):
@@ -231,6 +234,14 @@ def gemm_bt_plan_ws(M, N, K, in_dtype, out_dtype, a_align=256, b_align=256, c_al
     st = load().gemm_bt_plan_ws(M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, ctypes.byref(p))
     if st != OK:
         raise GemmBtError(st, "gemm_bt_plan_ws")
+    return p
+
+
+def gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, a_align=256, b_align=256, c_align=256):
+    p = Plan()
+    st = load().gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, ctypes.byref(p))
+    if st != OK:
+        raise GemmBtError(st, "gemm_bt_plan_epi")
     return p
 
 

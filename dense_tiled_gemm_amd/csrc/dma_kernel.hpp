@@ -869,9 +869,14 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                     constexpr int e = c0 + decltype(ec)::value;
                     constexpr int i = e / (FM * Q), jf = (e / Q) % FM, q = e % Q;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][jf][4 * q + r] =
-                            overwrite ? as_f32(x[e - c0][r]) : acc[i][jf][4 * q + r] + as_f32(x[e - c0][r]);
+                    for (int r = 0; r < 4; ++r) {
+                        const u32 w = x[e - c0][r];
+                        const float s = acc[i][jf][4 * q + r];
+                        if constexpr (IN == GEMM_BT_INT8)  // int32 sums
+                            acc[i][jf][4 * q + r] = as_f32(overwrite ? w : as_u32(s) + w);
+                        else
+                            acc[i][jf][4 * q + r] = overwrite ? as_f32(w) : s + as_f32(w);
+                    }
                 });
                 __builtin_amdgcn_sched_barrier(0);
             });

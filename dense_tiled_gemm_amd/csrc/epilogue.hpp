@@ -386,19 +386,54 @@ __device__ __forceinline__ void store_tile_epi(const typename AccBlock<MF>::type
     }
 }
 
-// One output: row i, column j of an M x N product whose sum is `s`.
-__device__ inline void store_one_epi(float s, void* C, int N, size_t i, int j, const EpiArgs& e) {
-    const size_t at = i * (size_t)N + j;
+// What an epilogue adds to outputs j .. j+n-1 (n in 0..4) of row i: fetched
+// ahead of the sums, so that its latency passes behind them.
+struct Epi4 {
+    float rs, cs[4], cb[4], res[4];
+};
+__device__ __forceinline__ Epi4 load_epi4(int N, size_t i, int j, int n, const EpiArgs& e) {
+    Epi4 v = {1.0f, {1.0f, 1.0f, 1.0f, 1.0f}, {0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
     const int md = e.mode;
-    float z = s;
-    if (md & EPI_ROW_SCALE) z *= e.row_scale[i];
-    z = __builtin_fmaf(z, md & EPI_COL_SCALE ? e.col_scale[j] : 1.0f,
-                       md & EPI_BIAS ? load1(e.bias, epi_type(md, EPI_BIAS_TYPE), j) : 0.0f);
-    if (md & EPI_PREACT) store1(e.preact, epi_type(md, EPI_PREACT_TYPE), at, z);
-    float y = z;
-    with_act(md >> EPI_ACT, [&](auto act) { y = act_value<decltype(act)::value>(z); });
-    if (md & EPI_RESIDUAL) y += load1(e.residual, epi_type(md, EPI_RESIDUAL_TYPE), at);
-    store1(C, epi_type(md, EPI_OUT_TYPE), at, y);
+    if (n > 0 && (md & EPI_ROW_SCALE)) v.rs = e.row_scale[i];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        if (x < n) {
+            if (md & EPI_COL_SCALE) v.cs[x] = e.col_scale[j + x];
+            if (md & EPI_BIAS) v.cb[x] = load1(e.bias, epi_type(md, EPI_BIAS_TYPE), j + x);
+            if (md & EPI_RESIDUAL) v.res[x] = load1(e.residual, epi_type(md, EPI_RESIDUAL_TYPE), i * N + j + x);
+        }
+    return v;
+}
+__device__ __forceinline__ void store4(void* p, int t, size_t i, int n, const float (&v)[4]) {
+    if (n == 4) {
+        if (t == GEMM_BT_F32)
+            *(u32x4_any*)((u32*)p + i) = u32x4{as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+        else if (t == GEMM_BT_BF16)
+            *(u32x2_any*)((u16*)p + i) = u32x2{pack2<GEMM_BT_BF16>(v[0], v[1]), pack2<GEMM_BT_BF16>(v[2], v[3])};
+        else
+            *(u32x2_any*)((u16*)p + i) = u32x2{pack2<GEMM_BT_F16>(v[0], v[1]), pack2<GEMM_BT_F16>(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < n) store1(p, t, i + x, v[x]);
+    }
+}
+__device__ __forceinline__ void store_epi4(const float (&s)[4], const Epi4& v, void* C, int N, size_t i, int j, int n,
+                                           const EpiArgs& e) {
+    const size_t at = i * N + j;
+    const int md = e.mode;
+    float z[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) z[x] = __builtin_fmaf(s[x] * v.rs, v.cs[x], v.cb[x]);
+    if (md & EPI_PREACT) store4(e.preact, epi_type(md, EPI_PREACT_TYPE), at, n, z);
+    with_act(md >> EPI_ACT, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[x] = act_value<decltype(act)::value>(z[x]);
+    });
+    if (md & EPI_RESIDUAL)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[x] += v.res[x];
+    store4(C, epi_type(md, EPI_OUT_TYPE), at, n, z);
 }
 
 }  // namespace gbt

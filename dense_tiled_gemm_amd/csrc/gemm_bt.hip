@@ -11,6 +11,7 @@
 #include "device.hpp"
 #include "dma_kernel.hpp"
 #include "epi_kernels.hpp"
+#include "rows.hpp"
 #include "skinny_dma.hpp"
 #ifdef GEMM_BT_TUNING
 // measured alternatives: register streaming for M <= 16, register-staged
@@ -121,6 +122,13 @@ static DmaVariant split_only_variant(const char* name) {
     return v;
 }
 
+// The same for 8-bit inputs (BK elements are BK bytes).
+template <int BM, int BN, int BK, int S, int WM, int WN, int SWZ>
+static DmaVariant split_only_variant8(const char* name) {
+    DmaVariant v = {name, BM, BN, BK, S, WM, WN, SWZ, S * (BM + BN) * BK, {}};
+    return v;
+}
+
 // Index 0 is the default for large grids, 7, 1, 8 and 9 for smaller ones, 2
 // and 6 for the smallest (see plan_impl), 3..5 the same for 8-bit inputs, float or integer
 // (128-element K steps: 128-byte tile rows, as for the 16-bit kernels; 32x32
@@ -140,6 +148,7 @@ constexpr int kThin32 = 11;   // 32 x 64 tiles of 256-byte rows, split along K o
 // The line-ring twins of the 128 x 128, 96 x 128, 128 x 96 and 64 x 64 tiers
 // (dma_kernel PH = 1), for rows that are 16-byte but not 128-byte aligned.
 constexpr int kRing128 = 12, kRingShort = 13, kRingNarrow = 14, kRing64 = 15;
+constexpr int kThin8 = 16;  // 64 x 64 tiles of 256-byte rows (8-bit inputs with an epilogue), split along K only
 static const DmaVariant* dma_variants(int* count) {
     static const DmaVariant v[] = {
         dma_variant<256, 256, 64, 2, 2, 4, 2, 6, 0, 16, true, 0, 2>("L64E16iR5s"),
@@ -159,6 +168,7 @@ static const DmaVariant* dma_variants(int* count) {
         dma_variant<96, 128, 64, 4, 2, 2, 2, 6, 0, 16, true, 0, 0, false, 1>("M96x128s4P"),
         dma_variant<128, 96, 64, 4, 2, 2, 2, 6, 0, 16, true, 0, 0, false, 1>("M128x96s4P"),
         dma_variant<64, 64, 64, 4, 2, 2, 2, 4, 0, 16, true, 0, 0, false, 1>("Q64E4m16P"),
+        split_only_variant8<64, 64, 256, 4, 2, 2, 2>("Q256F8s4"),
 #ifdef GEMM_BT_TUNING
         dma_variant<256, 256, 64, 2, 2, 4, 2, 2, 0, 16>("L64E16"),
         dma_variant<128, 128, 64, 4, 2, 2, 2, 4, 0, 16>("M64E4s4m16"),
@@ -421,8 +431,33 @@ static bool plan_split_rule(int64_t M, int64_t N, int64_t K, int num_cu, int64_t
     return plan_split(M, N, K, ring ? kRing128 : kSkVariant, num_cu, false, p);
 }
 
+// Split plan of an 8-bit product with an epilogue (whose scales make it a
+// serving product, often of few rows): where 64 x 64 tiles leave half the CUs
+// idle, each is cut along K into pieces of at least 8 steps of 256 (256-byte
+// tile rows), as many as fill the CUs.  Measured (us, int8, weights from HBM,
+// uncut vs cut; 128-byte rows in pieces of 16 steps in brackets): 64x8192x8192
+// 24.6 vs 20.1 (20.8), 16x1024x8192 17.1 vs 9.7 (10.4), 128x1024x8192 17.5 vs
+// 10.6 (11.2), 64x64x8192 17.1 vs 9.4, 256x512x4096 10.7 vs 9.2, 64x4096x4096
+// 10.8 vs 9.7; pieces of 4 steps lose (16x1024x8192 10.6, 64x512x2048 7.6 vs
+// 7.3).
+constexpr int64_t kSk8MinSteps = 8;
+static void plan_split8(int64_t K, int num_cu, gemm_bt_plan_t* p) {
+    int n = 0;
+    const DmaVariant& v = dma_variants(&n)[kThin8];
+    const int64_t T = p->tiles_m * p->tiles_n, nk = (K + v.bk - 1) / v.bk;
+    const int64_t S = std::min<int64_t>(num_cu / T, nk / kSk8MinSteps);
+    if (T * 2 > num_cu || T > kSkMaxTiles || S < 2) return;
+    p->variant = kThin8;
+    p->bk = v.bk;
+    p->stages = v.stages;
+    p->lds_bytes = v.lds_bytes;
+    p->grid = T * S;
+    p->split_tiles = T;
+    p->workspace_bytes = kSkCounterBytes + p->grid * (int64_t)p->bm * p->bn * 4;
+}
+
 static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align,
-                     int b_align, int c_align, int num_cu, bool allow_sk, gemm_bt_plan_t* p) {
+                     int b_align, int c_align, int num_cu, bool allow_sk, gemm_bt_plan_t* p, bool epi = false) {
     if (!p) return GEMM_BT_ERR_INVALID_VALUE;
     std::memset(p, 0, sizeof(*p));
     if (batch < 0 || M < 0 || N < 0 || K < 0) return GEMM_BT_ERR_INVALID_VALUE;
@@ -483,9 +518,9 @@ static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtyp
         if (r1 * tn * 8 >= waves_l * num_cu * 7 && m1 < M) {
             gemm_bt_plan_t rest;
             int st = plan_impl(1, M - m1, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk,
-                               &rest);
+                               &rest, epi);
             if (st != GEMM_BT_OK) return st;
-            st = plan_impl(1, m1, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk, p);
+            st = plan_impl(1, m1, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk, p, epi);
             if (st != GEMM_BT_OK) return st;
             p->split_rows = m1;
             if (rest.workspace_bytes > p->workspace_bytes) p->workspace_bytes = rest.workspace_bytes;
@@ -504,9 +539,9 @@ static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtyp
         if (z1 >= 1 && z1 < batch && z1 * ti * 8 >= waves_l * num_cu * 7) {
             gemm_bt_plan_t rest;
             int st = plan_impl(batch - z1, M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk,
-                               &rest);
+                               &rest, epi);
             if (st != GEMM_BT_OK) return st;
-            st = plan_impl(z1, M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk, p);
+            st = plan_impl(z1, M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, num_cu, allow_sk, p, epi);
             if (st != GEMM_BT_OK) return st;
             p->split_items = z1;
             if (rest.workspace_bytes > p->workspace_bytes) p->workspace_bytes = rest.workspace_bytes;
@@ -518,6 +553,26 @@ static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtyp
         // 16-byte aligned), always the LDS-DMA kernel
         if (K % 16 != 0 || a_align % 16 != 0 || b_align % 16 != 0) return GEMM_BT_ERR_UNSUPPORTED;
         int n = 0;
+        if (epi && M <= 16 && N > 16 * (int64_t)num_cu) {
+            // The streaming kernel in its 8-bit form, where its workgroups of 8
+            // rows of B are more than two per CU (us, against the cut 64 x 64
+            // tiles: 16x8192x8192 15.8 vs 19.2; at two per CU or fewer no
+            // better: 1x4096x4096 9.0 vs 8.7, 16x1024x8192 13.8 vs 9.7).
+            const SkinnyVariant& v = skinny_variants(&n)[0];
+            p->kernel = KIND_SKINNY;
+            p->variant = 1;
+            p->vec = 16;
+            p->bm = 16;
+            p->bn = v.bn;
+            p->bk = 2 * v.kb;
+            p->stages = v.stages;
+            p->ksplit = v.waves;
+            p->threads = 64 * v.waves;
+            p->lds_bytes = v.stages * (16 + v.bn) * v.kb * 2 + v.waves * 64 * 16;
+            p->tiles_m = 1;
+            p->tiles_n = p->grid = (N + v.bn - 1) / v.bn;
+            return GEMM_BT_OK;
+        }
         const DmaVariant* vs = dma_variants(&n);
         int use = kFp8Variants + (dma_large_tier(tiles_l, num_cu, true) ? 0 : (tiles_m128 * 2 > num_cu ? 1 : 2));
         // 256 x 256 tiles that fill at least half the CUs but not all, where
@@ -548,11 +603,19 @@ static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtyp
         p->tiles_n = (N + p->bn - 1) / p->bn;
         p->grid = p->tiles_m * p->tiles_n;
         if (p->grid * batch > 0x7FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
+        if (epi && allow_sk && f < 0 && batch == 1 && use == kFp8Variants + 2) plan_split8(K, num_cu, p);
         return GEMM_BT_OK;
     }
     p->vec = pick_vec(K, a_align, b_align);
     p->bk = 64;
-    if (M <= 16) {
+    // With an epilogue and a workspace, the streaming kernel only where its
+    // workgroups of 8 rows of B are more than two per CU; else the tiles
+    // below, cut along K where it is long (us, bf16, streaming vs tiles, weights
+    // from HBM: 16x64x8192 22.7 vs 9.2, 16x1024x8192 22.9 vs 10.1, 16x1024x4096
+    // 12.8 vs 9.2, 16x4096x4096 13.2 vs 10.9, 16x4096x8192 23.1 vs 18.8,
+    // 16x1024x2048 7.9 vs 7.3, 16x4096x1024 5.6 vs 5.0, but 16x8192x8192 25.6
+    // vs 30.1).  The plain product keeps its kernel, and so its bits.
+    if (M <= 16 && !(epi && allow_sk && N <= 16 * (int64_t)num_cu)) {
         p->kernel = KIND_SKINNY;
         p->bm = 16;
         p->tiles_m = 1;
@@ -988,7 +1051,7 @@ static SkArgs sk_args(const gemm_bt_plan_t& p, int64_t K, void* ws) {
     if (p.split_tiles > 0) {
         a.tiles = (int)p.split_tiles;
         a.pieces = (int)(p.grid / p.split_tiles);
-        a.nk = (int)(((K & ~7LL) + p.bk - 1) / p.bk);
+        a.nk = (int)(((K & ~7LL) + p.bk - 1) / p.bk);  // (8-bit inputs: K % 16 == 0)
         a.counters = (unsigned*)ws;
         a.partials = (float*)((char*)ws + kSkCounterBytes);
     }
@@ -1011,7 +1074,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
     const bool allow_sk = ws != nullptr;
     // Plan against the default CU count first: it validates the arguments
     // without touching the device.
-    int st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, 256, allow_sk, &p);
+    int st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, 256, allow_sk, &p, epi != nullptr);
     if (st != GEMM_BT_OK) return st;
     if (p.kernel == KIND_NONE) return GEMM_BT_OK;
     st = check_items(A, B, C, p.kernel, batch, M, N, stride_a, stride_b, stride_c, isz, osz);
@@ -1021,7 +1084,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
     st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
     if (num_cu != 256) {
-        st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, num_cu, allow_sk, &p);
+        st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, num_cu, allow_sk, &p, epi != nullptr);
         if (st != GEMM_BT_OK) return st;
     }
     if ((p.split_tiles > 0 || p.split_rows > 0 || p.split_items > 0) && p.workspace_bytes > 0 &&
@@ -1259,9 +1322,32 @@ int gemm_bt_ws(const void* A, const void* B, void* C, int64_t M, int64_t N, int6
     return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, out_dtype, workspace, workspace_bytes, stream);
 }
 
+// The output type that an epilogue's product is planned with: an int8 one is
+// the product with int32 sums (4 bytes per output, what any float type fits in).
+static int epi_plan_type(int in_dtype, int out_dtype) { return in_dtype == GEMM_BT_INT8 ? GEMM_BT_INT32 : out_dtype; }
+
+int gemm_bt_plan_epi(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align, int b_align, int c_align,
+                     gemm_bt_plan_t* plan) {
+    if (!float_type(out_dtype)) {
+        if (!plan) return GEMM_BT_ERR_INVALID_VALUE;
+        std::memset(plan, 0, sizeof(*plan));
+        return GEMM_BT_ERR_UNSUPPORTED;
+    }
+    return plan_impl(1, M, N, K, in_dtype, epi_plan_type(in_dtype, out_dtype), a_align, b_align, c_align, plan_cus(), true,
+                     plan, true);
+}
+
+int gemm_bt_epi_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    gemm_bt_plan_t p;
+    const int st = gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, 256, 256, 256, &p);
+    if (st == GEMM_BT_OK) *bytes = (size_t)p.workspace_bytes;
+    return st;
+}
+
 int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype,
                 const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream) {
-    auto float_type = [](int t) { return t == GEMM_BT_F32 || t == GEMM_BT_F16 || t == GEMM_BT_BF16; };
     if (!float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
     EpiArgs e = {nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype << EPI_OUT_TYPE};
     if (epilogue) {
@@ -1288,9 +1374,7 @@ int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int
             return GEMM_BT_ERR_INVALID_VALUE;
     }
     static_assert(GEMM_BT_F32 == 0, "the scales' type adds no bits");
-    // an int8 product is planned as the one with int32 sums (4 bytes per output, what any float type fits in)
-    const int plan_out = in_dtype == GEMM_BT_INT8 ? GEMM_BT_INT32 : out_dtype;
-    return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, plan_out, workspace, workspace_bytes, stream, &e);
+    return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, epi_plan_type(in_dtype, out_dtype), workspace, workspace_bytes, stream, &e);
 }
 
 int gemm_bt_noalloc(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,

@@ -46,7 +46,8 @@ static const void* epi_fn16(int variant, bool split) {
 }
 
 template <int IN>
-static const void* epi_fn8(int variant) {
+static const void* epi_fn8(int variant, bool split) {
+    if (split) return variant == 16 ? epi_fn<IN, 64, 64, 256, 4, 2, 2, 4, 32, 0, 1>() : nullptr;
     switch (variant) {
         case 3: return epi_fn<IN, 256, 256, 128, 2, 2, 4, 6, 32, 2>();
         case 4: return epi_fn<IN, 128, 128, 128, 4, 2, 2, 8, 32>();
@@ -59,23 +60,29 @@ const void* epi_dma_fn(int variant, int in_dtype, bool split) {
     switch (in_dtype) {
         case GEMM_BT_BF16: return epi_fn16<GEMM_BT_BF16>(variant, split);
         case GEMM_BT_F16: return epi_fn16<GEMM_BT_F16>(variant, split);
-        case GEMM_BT_FP8_E4M3: return epi_fn8<GEMM_BT_FP8_E4M3>(variant);
-        case GEMM_BT_FP8_E5M2: return epi_fn8<GEMM_BT_FP8_E5M2>(variant);
-        case GEMM_BT_INT8: return epi_fn8<GEMM_BT_INT8>(variant);
+        case GEMM_BT_FP8_E4M3: return epi_fn8<GEMM_BT_FP8_E4M3>(variant, split);
+        case GEMM_BT_FP8_E5M2: return epi_fn8<GEMM_BT_FP8_E5M2>(variant, split);
+        case GEMM_BT_INT8: return epi_fn8<GEMM_BT_INT8>(variant, split);
         default: return nullptr;
     }
 }
 
 const void* epi_skinny_fn(int in_dtype) {
-    return in_dtype == GEMM_BT_BF16 ? (const void*)&skinny_epi_kernel<GEMM_BT_BF16, 8, 256, 3, 1>
-                                    : (const void*)&skinny_epi_kernel<GEMM_BT_F16, 8, 256, 3, 1>;
+    switch (in_dtype) {  // 512 bytes of K per row and stage
+        case GEMM_BT_BF16: return (const void*)&skinny_epi_kernel<GEMM_BT_BF16, 8, 256, 3, 1>;
+        case GEMM_BT_F16: return (const void*)&skinny_epi_kernel<GEMM_BT_F16, 8, 256, 3, 1>;
+        case GEMM_BT_FP8_E4M3: return (const void*)&skinny_epi_kernel<GEMM_BT_FP8_E4M3, 8, 512, 3, 1>;
+        case GEMM_BT_FP8_E5M2: return (const void*)&skinny_epi_kernel<GEMM_BT_FP8_E5M2, 8, 512, 3, 1>;
+        case GEMM_BT_INT8: return (const void*)&skinny_epi_kernel<GEMM_BT_INT8, 8, 512, 3, 1>;
+        default: return nullptr;
+    }
 }
 
 // K == 0: the epilogue of empty sums.
 __global__ void epi_fill_kernel(void* C, int M, int N, const EpiArgs e) {
     const size_t n = (size_t)M * N, stride = (size_t)gridDim.x * blockDim.x;
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride)
-        store_one_epi(0.0f, C, N, i / N, (int)(i % N), e);
+        store_epi4({0.0f, 0.0f, 0.0f, 0.0f}, load_epi4(N, i / N, (int)(i % N), 1, e), C, N, i / N, (int)(i % N), 1, e);
 }
 
 const void* epi_fill_fn() { return (const void*)&epi_fill_kernel; }

@@ -41,6 +41,29 @@
 
 namespace gbt {
 
+// acc += the products of one 64-byte k-block: 16 bytes of one row per lane and
+// operand.  16-bit inputs: one 16x16x32 instruction; int8: one 16x16x64 (int32
+// sums in the accumulator's bits); 8-bit floats: two 16x16x32, one per 8-byte
+// half (the same half of A and of B, so the sum over both is the full one).
+template <int IN>
+__device__ __forceinline__ f32x4 skinny_mma(u32x4 b, u32x4 a, f32x4 c) {
+    if constexpr (IN == GEMM_BT_INT8) {
+        return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a),
+                                                                               __builtin_bit_cast(i32x4, c), 0, 0, 0));
+    } else if constexpr (in_size(IN) == 1) {
+        const long b0 = (long)b[0] | (long)b[1] << 32, b1 = (long)b[2] | (long)b[3] << 32;
+        const long a0 = (long)a[0] | (long)a[1] << 32, a1 = (long)a[2] | (long)a[3] << 32;
+        if constexpr (IN == GEMM_BT_FP8_E4M3)
+            return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b1, a1, __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b0, a0, c, 0, 0, 0), 0,
+                                                              0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_16x16x32_bf8_bf8(b1, a1, __builtin_amdgcn_mfma_f32_16x16x32_bf8_bf8(b0, a0, c, 0, 0, 0), 0,
+                                                              0, 0);
+    } else {
+        return Mfma<IN>::m16x16x32(b, a, c);
+    }
+}
+
 // The kernel's body.  `epi` is the epilogue's arguments (EpiArgs), or nothing
 // (SkinnyPlain): then the sums are rounded into C as they are.
 struct SkinnyPlain {};
@@ -48,15 +71,17 @@ template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT, class Epi
 __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
                                             int M, int N, int K, int vec_store, const Epi& epi) {
     constexpr int AR = 16;                 // rows of A held (M <= 16)
-    constexpr int CPR = KB / 8;            // 16-byte chunks per row per stage
-    constexpr int ROWB = KB * 2;           // bytes per row per stage
+    constexpr int ESZ = in_size(IN);       // bytes per input element
+    constexpr int EPC = 16 / ESZ;          // elements per 16-byte chunk
+    constexpr int CPR = KB / EPC;          // 16-byte chunks per row per stage
+    constexpr int ROWB = KB * ESZ;         // bytes per row per stage
     constexpr int RPI = 1024 / ROWB;       // rows per wave load instruction
     constexpr int BR = BN < 16 ? BN : 16;   // distinct B rows under one 16-row MFMA operand
     constexpr int BNP = BN;                 // B rows held in LDS
     constexpr int A_LOADS = AR / RPI, B_LOADS = BN / RPI;
     constexpr int LOADS = (A_LOADS + B_LOADS) / W;  // per wave per stage
     constexpr int STAGE_BYTES = (AR + BNP) * ROWB;
-    constexpr int KBLK = KB / 32;          // MFMA k-blocks per stage
+    constexpr int KBLK = ROWB / 64;        // k-blocks of 64 bytes per stage, 16 bytes per lane
     constexpr int KPW = KBLK / W;          // k-blocks per wave per stage
     constexpr int NBLK = BN < 16 ? 1 : BN / 16;
     constexpr int PEND = (STAGES - 2) * LOADS;
@@ -78,9 +103,9 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * BN;
     const int rows_a = min(AR, M), rows_b = min(BN, N - n0);
-    const i32x4 ra = rsrc_words(A, (u32)rows_a * (u32)K * 2u);
-    const i32x4 rb = rsrc_words(B + (size_t)n0 * K, (u32)rows_b * (u32)K * 2u);
-    const u32 row_bytes = (u32)K * 2u;
+    const i32x4 ra = rsrc_words(A, (u32)rows_a * (u32)K * (u32)ESZ);
+    const i32x4 rb = rsrc_words((const unsigned char*)B + (size_t)n0 * K * ESZ, (u32)rows_b * (u32)K * (u32)ESZ);
+    const u32 row_bytes = (u32)K * (u32)ESZ;
 
     // Loads: stage rows 0..15 hold A, rows 16..16+BN-1 hold B.  Load
     // instruction j (j = wave + i*W) fills stage rows j*RPI .. j*RPI+RPI-1;
@@ -98,10 +123,10 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
         const bool a = srow < AR;
         const int grow = a ? srow : srow - AR;  // row within A or within this block of B
         off[i] = (u32)grow * row_bytes + (u32)c * 16u;
-        kc[i] = c * 8;
+        kc[i] = c * EPC;
         is_a[i] = a;
     }
-    const int Kf = K & ~7;  // whole 16-byte chunks: through the LDS DMA
+    const int Kf = K & ~(EPC - 1);  // whole 16-byte chunks: through the LDS DMA (8-bit inputs: all of K)
     const int nk = (Kf + KB - 1) / KB;
     // ROT > 0: workgroup g walks the K steps starting at (g * ROT) mod nk and
     // wraps around, so that concurrent workgroups read different K offsets
@@ -129,7 +154,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     // K tail: in the extra k-block, lanes with q = 0 hold elements Kf ..
     // Kf + 7 of their row (zeros past K and for rows past M or N); the other
     // lanes' chunks are zero.  Fetched now so the loads hide behind the loop.
-    const int tail = K - Kf;
+    const int tail = ESZ == 2 ? K - Kf : 0;
     u32x4 ta = {0u, 0u, 0u, 0u}, tb[NBLK];
 #pragma unroll
     for (int b = 0; b < NBLK; ++b) tb[b] = u32x4{0u, 0u, 0u, 0u};
@@ -148,6 +173,14 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
             if (br < rows_b) tb[b] = fetch(B + (size_t)(n0 + br) * K + Kf);
         }
     }
+    // with an epilogue: what it adds to this lane's outputs, columns n0 + 4 q ..
+    // of row lane % 16 (the first block of B rows is the only one there is)
+    constexpr bool EPI = !std::is_same_v<Epi, SkinnyPlain>;
+    static_assert(!EPI || (NBLK == 1 && W == 1), "one wave stores 4 outputs per lane");
+    const int epi_n = EPI && r16 < M && 4 * q < BN ? min(4, N - n0 - 4 * q) : 0;
+    Epi4 terms;
+    if constexpr (EPI) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi);
+
     f32x4 acc[NBLK];
 #pragma unroll
     for (int b = 0; b < NBLK; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -166,7 +199,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
                 const int brow = AR + 16 * b + (r16 % BR);
                 const int chb = ((4 * kb + q) ^ (brow & 15)) * 16;
                 const u32x4 fb = *(const u32x4*)(s + brow * ROWB + chb);
-                acc[b] = Mfma<IN>::m16x16x32(fb, fa, acc[b]);
+                acc[b] = skinny_mma<IN>(fb, fa, acc[b]);
             }
         }
     };
@@ -185,8 +218,18 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     wait_vmcnt<0>();
     if (tail > 0 && wave == 0)
 #pragma unroll
-        for (int b = 0; b < NBLK; ++b) acc[b] = Mfma<IN>::m16x16x32(tb[b], ta, acc[b]);
+        for (int b = 0; b < NBLK; ++b) acc[b] = skinny_mma<IN>(tb[b], ta, acc[b]);
 
+    if constexpr (EPI) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = acc[0][e];
+            v[e] = IN == GEMM_BT_INT8 ? (float)(int)as_u32(x) : x;
+        }
+        if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi);
+        return;
+    }
 #pragma unroll
     for (int b = 0; b < NBLK; ++b) red[wave][b][lane] = acc[b];
     __syncthreads();
@@ -204,13 +247,6 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
         const u32 o = ((u32)m * (u32)N + (u32)n) * OSZ;
         const float v0 = sum[0], v1 = sum[1], v2 = sum[2], v3 = sum[3];
         if (nl >= BN) continue;
-        if constexpr (!std::is_same_v<Epi, SkinnyPlain>) {
-            const float vv[4] = {v0, v1, v2, v3};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < N) store_one_epi(vv[e], C, N, m, n + e, epi);
-            continue;
-        }
         if (vec_store) {
             if (n < N) {
                 if constexpr (OUT == GEMM_BT_F32) {
@@ -250,7 +286,7 @@ template <int IN, int BN, int KB, int STAGES, int W>
 __global__ __launch_bounds__(64 * W) void skinny_epi_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
                                                            void* __restrict__ C, int M, int N, int K,
                                                            const EpiArgs epi) {
-    skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, epi);
+    skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, epi);  // (OUT is not used)
 }
 
 }  // namespace gbt

@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, INT32, OK, GemmBtError, gemm_bt_workspace_size, load, workspace_for
+from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, OK, GemmBtError, load, workspace_for
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
@@ -280,12 +280,13 @@ def linear(x, weight, bias=None, activation="none", residual=None, x_scale=None,
     out_code = _CODES[y_dtype]
     with _on(device):
         s = _stream(device, stream)
-        nbytes = gemm_bt_workspace_size(M, N, K, in_code, INT32 if in_code == INT8 else out_code)
+        lib, need = load(), ctypes.c_size_t()
+        _check(lib.gemm_bt_epi_workspace_size(M, N, K, in_code, out_code, ctypes.byref(need)), "gemm_bt_epi_workspace_size")
         ws, ws_bytes = None, 0
-        if nbytes:
-            t = workspace_for(device, s, nbytes)
+        if need.value:
+            t = workspace_for(device, s, need.value)
             ws, ws_bytes = t.data_ptr(), t.numel()
-        _check(load().gemm_bt_epi(x.data_ptr(), weight.data_ptr(), y.data_ptr(), M, N, K, in_code, out_code, ctypes.byref(e),
+        _check(lib.gemm_bt_epi(x.data_ptr(), weight.data_ptr(), y.data_ptr(), M, N, K, in_code, out_code, ctypes.byref(e),
                                   ws, ws_bytes, s), "gemm_bt_epi")
     return (y, z) if save_preact else y
 

@@ -237,9 +237,12 @@ typedef struct {
  * they are accurate to a few units of fp32's last place.
  *   epilogue   NULL, or every pointer in it NULL and the activation none: C is
  *              the plain product (in floating point for int8 inputs too)
- *   workspace  as for gemm_bt_ws (NULL: no split along K); the plan and the
- *              sizes are those of gemm_bt_plan_ws and gemm_bt_workspace_size
- *              (for int8 inputs with out_dtype GEMM_BT_INT32)
+ *   workspace  as for gemm_bt_ws (NULL: no split along K), of
+ *              gemm_bt_epi_workspace_size bytes.  Products of 16-bit inputs are
+ *              planned as gemm_bt_ws plans them; 8-bit ones of few tiles are cut
+ *              along K too (64 x 64 tiles, pieces of at least 2048 elements).
+ *              For M <= 16 either run the streaming kernel where N is more than
+ *              16 per compute unit, else (with a workspace) tiles
  * K == 0 is the empty sum: C = act(bias) + residual, A and B are not read.
  * bias, residual and preact need the alignment of their elements only.
  * preact must not overlap C or an input.  Types that are none of the above,
@@ -248,6 +251,10 @@ typedef struct {
 int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,
                 int out_dtype, const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes,
                 void* stream);
+
+/* The workspace gemm_bt_epi needs for these sizes and types (as
+   gemm_bt_workspace_size). */
+int gemm_bt_epi_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, size_t* bytes);
 
 /*
  * Row operators around the product.  Matrices are row-major with `d` (or `n`)
@@ -401,6 +408,10 @@ int gemm_bt_plan(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, i
    runs when its workspace is not NULL). */
 int gemm_bt_plan_ws(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align,
                     int b_align, int c_align, gemm_bt_plan_t* plan);
+
+/* The plan of gemm_bt_epi given a large enough workspace. */
+int gemm_bt_plan_epi(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align, int b_align,
+                     int c_align, gemm_bt_plan_t* plan);
 
 /* The plan of gemm_bt_layout (for kernel 5 the variant is 0: A K-outer, 1: B
    K-outer, 2: both, on 128 x 128 tiles; 3, 4, 5 the same on 256 x 256 tiles). */

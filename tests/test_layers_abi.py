@@ -144,6 +144,41 @@ def test_linear_backward_workspace():
     assert size(1 << 20, 4096, 4096, 0)[1] >= 4 * 4096 * 4096 * 4
 
 
+def test_epilogue_plans():
+    """16-bit products are planned as gemm_bt_ws plans them, but for M <= 16 and few columns; 8-bit ones of few rows stream
+    or are cut along K."""
+    for i in (gb.BF16, gb.F16):
+        p = gb.gemm_bt_plan_epi(1, 4096, 4096, i, i)
+        assert (p.kernel, p.bm, p.bn, p.bk, p.split_tiles, p.grid) == (4, 32, 64, 128, 64, 128)
+        p = gb.gemm_bt_plan_epi(16, 4096, 1000, i, i)
+        assert (p.kernel, p.bm, p.bn, p.split_tiles) == (4, 32, 64, 0)
+        assert gb.gemm_bt_plan_epi(1, 4097, 4096, i, i).kernel == 3
+        assert gb.gemm_bt_plan_ws(1, 4096, 4096, i, i).kernel == 3
+    for M, N, K in ((1, 8192, 4096), (17, 4096, 4096), (64, 8192, 8192), (1024, 1024, 16384), (4096, 4096, 4096), (4352, 4096, 4096), (0, 5, 5)):
+        for i, o in ((gb.BF16, gb.F32), (gb.F16, gb.F16)):
+            assert gb.gemm_bt_plan_epi(M, N, K, i, o).as_dict() == gb.gemm_bt_plan_ws(M, N, K, i, o).as_dict()
+    for i in (gb.FP8_E4M3, gb.FP8_E5M2, gb.INT8):
+        p = gb.gemm_bt_plan_epi(16, 8192, 8192, i, gb.BF16)
+        assert (p.kernel, p.bn, p.bk, p.grid, p.workspace_bytes) == (3, 8, 512, 1024, 0)
+        p = gb.gemm_bt_plan_epi(16, 4096, 4096, i, gb.BF16)       # not more than two of its workgroups per CU
+        assert (p.kernel, p.bm, p.bk, p.split_tiles, p.grid) == (4, 64, 256, 64, 128)
+        p = gb.gemm_bt_plan_epi(64, 8192, 8192, i, gb.BF16)
+        assert (p.split_tiles, p.grid, p.workspace_bytes) == (128, 256, 16384 + 256 * 64 * 64 * 4)
+        p = gb.gemm_bt_plan_epi(64, 8192, 4080, i, gb.BF16)       # 16 steps: pieces of 8
+        assert (p.split_tiles, p.grid) == (128, 256)
+        p = gb.gemm_bt_plan_epi(64, 8192, 3840, i, gb.BF16)       # 15 steps: not cut
+        assert (p.split_tiles, p.grid, p.variant) == (0, 128, 5)
+        p = gb.gemm_bt_plan_epi(4096, 4096, 4096, i, gb.BF16)
+        assert (p.bm, p.split_tiles) == (256, 0)
+    n = ctypes.c_size_t()
+    size = lambda *a: (gb.load().gemm_bt_epi_workspace_size(*a, ctypes.byref(n)), n.value)
+    assert size(64, 8192, 8192, gb.INT8, gb.BF16) == (gb.OK, 16384 + 256 * 64 * 64 * 4)
+    assert size(64, 8192, 8192, gb.INT8, gb.INT32) == (UNSUP, 0)
+    assert size(-1, 8192, 8192, gb.BF16, gb.BF16) == (BAD, 0)
+    assert gb.load().gemm_bt_epi_workspace_size(1, 1, 1, gb.BF16, gb.BF16, None) == BAD
+    assert gb.load().gemm_bt_plan_epi(1, 1, 1, gb.BF16, gb.INT32, 16, 16, 16, None) == BAD
+
+
 def test_workspace_sizes():
     lib, n = gb.load(), ctypes.c_size_t()
     for f in (lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward_workspace):

@@ -351,7 +351,7 @@ def act64(z, act):
 
 def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False, scales=False, seed=0, offset=0, xw=None):
     """One call, every entry: the fp32 sums themselves are the plain product's (checked against the oracle elsewhere), from
-    the same tiles; what follows them is computed here in 64 bits."""
+    the same tiles, or for M <= 16 sums of the same terms in another order; what follows them is computed here in 64 bits."""
     say("linear", M, N, K, ind, outd, act, "bias", bias, "res", res, "pre", pre, "scales", scales, "seed", seed)
     if ind == "i8":
         x, w = (torch.randint(-128, 128, s, generator=gen(seed + i), dtype=torch.int8) for i, s in enumerate(((M, K), (N, K))))
@@ -373,6 +373,8 @@ def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False,
         s = gpu.mm_bt(x.cuda(), w.cuda(), out_dtype=torch.int32 if ind == "i8" else torch.float32).cpu().double()
     z = s
     tol = u * s.abs() if ind == "i8" else torch.zeros_like(s)
+    if M <= 16 and ind in DT:
+        tol = 2 * K * u * (x.double().abs() @ w.double().abs().t())
     if scales:
         z = z * xs.double()[:, None] * ws.double()
         tol = tol * xs.double()[:, None] * ws.double() + 2 * u * z.abs()
@@ -391,7 +393,7 @@ def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False,
 
 
 # (M, N, K): every tile shape of the 16-bit kernels, ragged edges, K tails, odd rows of C
-SHAPES16 = [(1, 1, 1), (1, 64, 64), (3, 9, 17), (16, 200, 520), (16, 33, 4097), (17, 33, 65), (24, 4096, 8192), (31, 63, 127),
+SHAPES16 = [(1, 1, 1), (1, 64, 64), (1, 4100, 2048), (16, 8192, 1000), (7, 5001, 333), (2, 1000, 8200), (16, 512, 8190), (3, 9, 17), (16, 200, 520), (16, 33, 4097), (17, 33, 65), (24, 4096, 8192), (31, 63, 127),
             (64, 64, 64), (64, 4100, 8192), (100, 2050, 134), (130, 264, 73), (257, 513, 129), (300, 700, 1000),
             (512, 512, 16384), (1024, 1024, 16384), (520, 1000, 16392), (700, 3200, 130), (1000, 1000, 136), (1000, 2999, 72), (1000, 3000, 136),
             (1000, 3000, 128), (1030, 1030, 202), (2000, 4000, 192), (2048, 1536, 72), (2048, 4004, 72), (3000, 1000, 72),
@@ -417,10 +419,10 @@ def test_linear_covers_every_kernel(gpu):
     """The shapes above plan each tile shape, and the forms split along K."""
     seen = set()
     for M, N, K in SHAPES16:
-        p = gpu.gemm_bt_plan_ws(M, N, K, gpu.BF16, gpu.F32)
+        p = gpu.gemm_bt_plan_epi(M, N, K, gpu.BF16, gpu.F32)
         parts = [p]
         if p.split_rows:
-            parts.append(gpu.gemm_bt_plan_ws(M - p.split_rows, N, K, gpu.BF16, gpu.F32))
+            parts.append(gpu.gemm_bt_plan_epi(M - p.split_rows, N, K, gpu.BF16, gpu.F32))
         seen |= {(q.kernel, q.variant, q.split_tiles > 0) for q in parts}
     assert {v for k, v, s in seen if k == 4 and not s} == {0, 1, 2, 6, 7, 8, 9, 12, 13, 14, 15}, seen
     assert {v for k, v, s in seen if k == 4 and s} == {1, 10, 11, 12}, seen
@@ -437,6 +439,40 @@ def test_linear_eight_bits(gpu, ind, shape):
         o["bias"] = "bf16" if o["bias"] == "own" else o["bias"]
         o["scales"] = ind == "i8" or i % 2 == 0
         check_epilogue(gpu, *shape, ind, seed=n, **o)
+
+
+@pytest.mark.parametrize("ind", ["e4m3", "e5m2", "i8"])
+@pytest.mark.parametrize("shape", [(16, 8192, 512), (1, 4104, 4096), (5, 6001, 272), (64, 512, 8192), (33, 4096, 4096), (200, 300, 8208),
+                                   (7, 70, 16384), (129, 1000, 4112)])
+def test_linear_eight_bits_thin(gpu, ind, shape):
+    """8-bit products of few rows: streaming, and cut along K (whose sums are those of other tiles, in another order)."""
+    M, N, K = shape
+    code = {"e4m3": gpu.FP8_E4M3, "e5m2": gpu.FP8_E5M2, "i8": gpu.INT8}[ind]
+    p = gpu.gemm_bt_plan_epi(M, N, K, code, gpu.BF16)
+    assert p.kernel == 3 if M <= 16 and N > 4096 else p.split_tiles > 0, p.as_dict()
+    n = sum(shape)
+    say("thin", ind, shape)
+    t = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}.get(ind)
+    if ind == "i8":
+        x, w = (torch.randint(-128, 128, s, generator=gen(n + i), dtype=torch.int8) for i, s in enumerate(((M, K), (N, K))))
+    else:
+        x, w = randn(n, M, K).to(t), randn(n + 1, N, K).to(t)
+    b, r = randn(n + 2, N, dtype=torch.bfloat16), randn(n + 3, M, N)
+    xs, ws = torch.rand(M, generator=gen(n + 4)) + 0.5, (torch.rand(N, generator=gen(n + 5)) + 0.5) * K ** -0.5 * (2.0 ** -12 if ind == "i8" else 1)
+    y, untouched = guarded((M, N), torch.float32)
+    gpu.linear(x.cuda(), w.cuda(), bias=b.cuda(), activation="silu", residual=r.cuda(), x_scale=xs.cuda(), weight_scale=ws.cuda(),
+               out=y, out_dtype=torch.float32)
+    untouched()
+    x64, w64 = x.float().double(), w.float().double()
+    s, size = x64 @ w64.t(), x64.abs() @ w64.abs().t()
+    scale = xs.double()[:, None] * ws.double()
+    z = s * scale + b.double()
+    tol = (u * s.abs() if ind == "i8" else K * u * size) * scale + 3 * u * (s * scale).abs() + u * z.abs()
+    a = act64(z, "silu") + r.double()
+    close(y, a, 1.13 * tol + 2.0 ** -20 * z.abs() + u * a.abs(), "y")
+    if ind == "i8":  # whole numbers: every sum exact, in any order
+        got = gpu.linear(x.cuda(), w.cuda(), out_dtype=torch.float32)
+        assert torch.equal(got.cpu(), s.float())
 
 
 def test_linear_every_term(gpu):
