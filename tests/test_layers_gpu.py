@@ -773,6 +773,65 @@ def test_streams(gpu):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_stream_argument(gpu):
+    """``stream``: the copies that a call makes of strided inputs are in that stream's order too."""
+    x0, w = randn(1, 64, 512, dtype=torch.bfloat16), randn(2, 256, 512, std=0.05, dtype=torch.bfloat16).cuda()
+    r0, g = randn(3, 64, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    want = gpu.linear(x0.cuda(), w, activation="silu", residual=r0.cuda())
+    wantn = gpu.add_rms_norm(want, g, residual=r0.cuda(), save_rstd=True)
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        xt = torch.empty(512, 64, dtype=torch.bfloat16, device="cuda")
+        rt = torch.empty(256, 64, dtype=torch.bfloat16, device="cuda")
+        xs, rs = x0.t().contiguous().cuda(), r0.t().contiguous().cuda()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy = torch.randn(2048, 2048, device="cuda")
+            for _ in range(20):
+                busy = busy @ busy * 0.01
+            xt.copy_(xs)
+            rt.copy_(rs)
+        got = gpu.linear(xt.t(), w, activation="silu", residual=rt.t(), stream=handle)
+        n = gpu.add_rms_norm(got, g, residual=rt.t(), save_rstd=True, stream=handle)
+        q = gpu.quantize_rows(got, torch.int8, stream=handle)
+        dx, dw = gpu.add_rms_norm_backward(got, n.h, g, n.rstd, dh=rt.t(), stream=handle)
+        b = gpu.linear_backward(got, xt.t(), w, preact=got, activation="silu", stream=handle)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(n.y, wantn.y) and torch.equal(n.h, wantn.h)
+        assert torch.equal(q.q, gpu.quantize_rows(want, torch.int8).q)
+        wdx, wdw = gpu.add_rms_norm_backward(want, wantn.h, g, wantn.rstd, dh=r0.cuda())
+        wb = gpu.linear_backward(want, x0.cuda(), w, preact=want, activation="silu")
+        assert torch.equal(dx, wdx) and torch.equal(dw, wdw) and all(torch.equal(a, c) for a, c in zip(b, wb))
+
+
+def test_graph_without_a_warm_up(gpu):
+    """A product that is cut along K, captured before any call on that stream: its counters are the graph's own, whatever
+    runs on the stream in between and in whichever order two graphs are replayed."""
+    for dt in (torch.bfloat16, torch.int8):
+        x, w = randn(1, 8, 8192, std=3.0).to(dt).cuda(), randn(2, 512, 8192, std=3.0).to(dt).cuda()
+        code = {torch.bfloat16: gpu.BF16, torch.int8: gpu.INT8}[dt]
+        assert gpu.gemm_bt_plan_epi(8, 512, 8192, code, gpu.BF16).split_tiles > 0
+        want = gpu.linear(x, w)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        graphs, outs = [], []
+        for _ in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                outs.append(gpu.linear(x, w))
+        with torch.cuda.stream(side):
+            eager = gpu.linear(x, w)
+        side.synchronize()
+        assert torch.equal(eager, want)
+        for i in (1, 0, 1, 1, 0):
+            outs[i].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], want), i
+            with torch.cuda.stream(side):
+                assert torch.equal(gpu.linear(x, w), want)
+
+
 def test_graph_replays(gpu):
     t = block_inputs(gpu)
     want = [o.clone() for o in block(gpu, t)]
