@@ -45,10 +45,8 @@ __host__ __device__ inline int epi_type(int mode, int shift) { return (mode >> s
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
-template <bool NT = false>
-__device__ __forceinline__ u32x4 load16(const void* p) {
-    if constexpr (NT) return __builtin_nontemporal_load((const u32x4_any*)p);
-    else return *(const u32x4_any*)p;
+__device__ __forceinline__ u32x4 load16(const void* p, bool nt = false) {
+    return nt ? __builtin_nontemporal_load((const u32x4_any*)p) : *(const u32x4_any*)p;
 }
 __device__ __forceinline__ void store16_nt(void* p, u32x4 v) { __builtin_nontemporal_store(v, (u32x4_any*)p); }
 
@@ -69,15 +67,14 @@ struct Raw8 {
 };
 
 // Elements i .. i+n-1 (n in 1..8) of an array of type t; the rest are zero.
-// NT: read once, not kept in the caches.
-template <bool NT = false>
-__device__ __forceinline__ Raw8 load_raw8(const void* p, int t, size_t i, int n) {
+// nt: read once, not kept in the caches.
+__device__ __forceinline__ Raw8 load_raw8(const void* p, int t, size_t i, int n, bool nt = false) {
     Raw8 r = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
     if (t == GEMM_BT_F32) {
         const u32* s = (const u32*)p + i;
         if (n >= 8) {
-            r.a = load16<NT>(s);
-            r.b = load16<NT>(s + 4);
+            r.a = load16(s, nt);
+            r.b = load16(s + 4, nt);
         } else {
             n = renew(n);
 #pragma unroll
@@ -89,7 +86,7 @@ __device__ __forceinline__ Raw8 load_raw8(const void* p, int t, size_t i, int n)
     } else {
         const u16* s = (const u16*)p + i;
         if (n >= 8) {
-            r.a = load16<NT>(s);
+            r.a = load16(s, nt);
         } else {
             n = renew(n);
 #pragma unroll

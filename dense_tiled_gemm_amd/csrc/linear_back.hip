@@ -33,13 +33,15 @@ struct BackProduct {
     int blocks;   // workgroups: tiles_m * tiles_n * pieces, padded to whole rounds of the 8 dies
     int shifted;  // rows of `out` are not whole 16-byte chunks (of `parts`: shifted_parts)
     int shifted_parts;
+
+    int steps() const { return blocks ? std::min(per, (depth + 63) / 64) : 0; }  // of its longest run
 };
 struct BackArgs {
     BackProduct dw, dx;
     FoldArgs fold;  // out == nullptr: none
 };
 
-template <int IN, bool TA, int BT, int WN>
+template <int IN, bool TA, int BT, int WN, int S>
 __device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigned char* lds) {
     const int total = p.tiles_m * p.tiles_n * p.pieces;
     if (pid >= total) return;
@@ -53,21 +55,21 @@ __device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigne
     const u16* a = TA ? p.a + (size_t)k0 * p.lda : p.a + k0;
     const u16* b = p.b + (size_t)k0 * p.ldb;
     if (p.pieces == 1)
-        trans_body<IN, IN, TA, true, BT, BT, 2, WN>(a, b, p.out, p.rows, p.cols, depth, p.lda, p.ldb, (int)tm * BT,
+        trans_body<IN, IN, TA, true, BT, BT, 2, WN, S>(a, b, p.out, p.rows, p.cols, depth, p.lda, p.ldb, (int)tm * BT,
                                                     (int)tn * BT, p.shifted, lds);
     else
-        trans_body<IN, GEMM_BT_F32, TA, true, BT, BT, 2, WN>(a, b, p.parts + (size_t)j * p.rows * p.cols, p.rows, p.cols,
+        trans_body<IN, GEMM_BT_F32, TA, true, BT, BT, 2, WN, S>(a, b, p.parts + (size_t)j * p.rows * p.cols, p.rows, p.cols,
                                                              depth, p.lda, p.ldb, (int)tm * BT, (int)tn * BT,
                                                              p.shifted_parts, lds);
 }
 
-template <int IN, int BT, int WN>
+template <int IN, int BT, int WN, int S>
 __global__ __launch_bounds__(128 * WN) void linear_back_kernel(const BackArgs a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * 2 * BT * 64 * 2];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S * 2 * BT * 64 * 2];
     int blk = blockIdx.x;
-    if (blk < a.dw.blocks) return back_tile<IN, true, BT, WN>(a.dw, blk, lds);
+    if (blk < a.dw.blocks) return back_tile<IN, true, BT, WN, S>(a.dw, blk, lds);
     blk -= a.dw.blocks;
-    if (blk < a.dx.blocks) return back_tile<IN, false, BT, WN>(a.dx, blk, lds);
+    if (blk < a.dx.blocks) return back_tile<IN, false, BT, WN, S>(a.dx, blk, lds);
     fold_columns<128 * WN>(a.fold, blk - a.dx.blocks, (float(*)[17])lds);
 }
 
@@ -138,7 +140,9 @@ struct BackPlan {
 // all tiles of both products would take `fair` steps on every CU: a tile much
 // longer than that is cut into runs of about that length, each of which leaves
 // fp32 sums; the cut costs a launch that adds them, so only a gain of `least`
-// steps is taken.  `most` steps is what a run may hold (2 GiB of an operand).
+// steps is taken (128 x 128 tiles, us, at 24, 12 and 6: 131x1536x192 21.1, 15.9,
+// 15.9; 2048x1024x1024 30.3, 28.4, 28.1; 1024x1024x1024 20.4, 20.3, 25.9;
+// 1000x512x2048 19.3, 19.2, 20.9).  `most` steps is what a run may hold (2 GiB of an operand).
 static void cut(int64_t steps, int64_t fair, int64_t least, int64_t most, int* pieces, int* per) {
     int64_t run = steps;
     if (steps - fair >= least) run = std::max<int64_t>(fair, 8);
@@ -164,7 +168,7 @@ static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu)
     const int64_t steps_w = (M + 63) / 64, steps_x = (N + 63) / 64;
     const int64_t work = tiles(N, K, p.bt) * steps_w + tiles(M, K, p.bt) * steps_x;
     const int64_t fair = (work + num_cu - 1) / num_cu;
-    const int64_t least = use_big ? 12 : 24;
+    const int64_t least = 12;
     const int64_t most = 0x7FFFFFFFLL / (128 * std::max(p.ldz, p.ldk));  // steps of 64 rows below 2 GiB
     cut(steps_w, fair, least, std::max<int64_t>(1, most), &p.pieces_w, &p.per_w);
     cut(steps_x, fair, least, std::max<int64_t>(1, most), &p.pieces_x, &p.per_x);
@@ -255,9 +259,18 @@ static int linear_backward(const void* dy, const void* x, const void* w, const v
         grid += fold_blocks(N);
     }
     if (grid == 0) return GEMM_BT_OK;
-    const bool bf = type == GEMM_BT_BF16;
-    const void* fn = p.bt == 256 ? (bf ? (const void*)&linear_back_kernel<GEMM_BT_BF16, 256, 4> : (const void*)&linear_back_kernel<GEMM_BT_F16, 256, 4>)
-                                 : (bf ? (const void*)&linear_back_kernel<GEMM_BT_BF16, 128, 2> : (const void*)&linear_back_kernel<GEMM_BT_F16, 128, 2>);
+    // 128 x 128 tiles that leave every CU at most one workgroup, and 16 or more
+    // steps: a ring of four stages in place of two workgroups' worth of two (us:
+    // 1024x1024x1024 22.6 vs 20.4, 2048x1024x1024 35.0 vs 30.3; with 8 steps
+    // the longer start loses, 4096x512x512 25.1 vs 28.5)
+    const bool deep = p.bt == 128 && a.dw.blocks + a.dx.blocks <= num_cu && std::max(a.dw.steps(), a.dx.steps()) >= 16;
+    auto pick = [&](auto in) -> const void* {
+        constexpr int IN = decltype(in)::value;
+        if (p.bt == 256) return (const void*)&linear_back_kernel<IN, 256, 4, 2>;
+        return deep ? (const void*)&linear_back_kernel<IN, 128, 2, 4> : (const void*)&linear_back_kernel<IN, 128, 2, 2>;
+    };
+    const void* fn = type == GEMM_BT_BF16 ? pick(std::integral_constant<int, GEMM_BT_BF16>{})
+                                          : pick(std::integral_constant<int, GEMM_BT_F16>{});
     void* args[] = {&a};
     st = launch(fn, dim3(grid), p.bt == 256 ? 512 : 256, args, stream);
     if (st != GEMM_BT_OK) return st;

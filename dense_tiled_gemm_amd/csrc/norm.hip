@@ -310,6 +310,11 @@ struct NormBackArgs {
     float* partials;  // gridDim.x rows of d sums of dy * xhat
     long long rows, ld_dy, ldh, ld_dh;
     int d;
+    // rows of whole 16-byte chunks: dy, h and dh are read past the caches (8192
+    // x 8192 bf16 100.3 -> 93.6 us).  Rows that are not share lines between
+    // neighbouring lanes, which would then be fetched twice (1110 x 1317 18.6 us
+    // against 9.6 at 1320).
+    int nt;
 };
 
 // With xhat = h rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + dh, and
@@ -351,9 +356,9 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 const int n = min(8, d - i);
-                r.dy[u] = load_raw8<true>(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
-                r.h[u] = load_raw8<true>(a.h, XT, (size_t)(row * a.ldh) + i, n);
-                if (AHEAD && a.dh) r.dh[u] = load_raw8<true>(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
+                r.dy[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n, a.nt);
+                r.h[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n, a.nt);
+                if (AHEAD && a.dh) r.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n, a.nt);
             }
         });
     };
@@ -431,11 +436,121 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
         const int i = (u * T + t) * 8;
         if (i < d) {
             float* p = a.partials + (size_t)blockIdx.x * d + i;
+            if (i + 8 <= d) {
+                *(u32x4_any*)p = u32x4{as_u32(dw[u][0]), as_u32(dw[u][1]), as_u32(dw[u][2]), as_u32(dw[u][3])};
+                *(u32x4_any*)(p + 4) = u32x4{as_u32(dw[u][4]), as_u32(dw[u][5]), as_u32(dw[u][6]), as_u32(dw[u][7])};
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e < d) p[e] = dw[u][e];
+                for (int e = 0; e < 7; ++e)
+                    if (i + e < d) p[e] = dw[u][e];
+            }
         }
     });
+}
+
+// Few rows: the first a.rows workgroups (WAVE: a wave each) make dx, one row
+// each; the others make dw itself, 64 columns each over all rows, from dy and
+// h as the caches hold them.  One launch, no partial sums.
+template <int XT, int WT, int U, bool WAVE>
+__global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs a, int row_blocks, void* dweight) {
+    __shared__ float part[16];
+    __shared__ float joined[128][65];
+    const int d = a.d;
+    if ((int)blockIdx.x < row_blocks) {
+        const int T = WAVE ? 64 : blockDim.x;
+        const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+        const long long row = WAVE ? (long long)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
+        if (row >= a.rows) return;
+        Raw8 dyr[U], hr[U], dhr[U], wr[U];
+        const float rstd = a.rstd[row];
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                const int n = min(8, d - i);
+                dyr[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
+                hr[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n);
+                wr[u] = load_raw8(a.weight, WT, (size_t)i, n);
+                if (a.dh) dhr[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
+            }
+        });
+        float xhat[U][8], g[U][8], c = 0.0f;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            if ((u * T + renew(t)) * 8 < d) {
+                float w[8];
+                decode8(wr[u], WT, w);
+                decode8(hr[u], XT, xhat[u]);
+                decode8(dyr[u], XT, g[u]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    xhat[u][e] *= rstd;
+                    g[u][e] *= w[e];
+                    c = __builtin_fmaf(g[u][e], xhat[u][e], c);
+                }
+            }
+        });
+        c = row_join<SumOp, WAVE>(c, part) / (float)d;
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
+                if (a.dh) {
+                    float v[8];
+                    decode8(dhr[u], XT, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += v[e];
+                }
+                store8(a.dx, XT, (size_t)(row * d) + i, min(8, d - i), o);
+            }
+        });
+        return;
+    }
+    // dw of 64 columns: 8 lanes of 8 columns, blockDim / 8 groups of them over the rows
+    const int G = blockDim.x >> 3, l = threadIdx.x & 7, k = threadIdx.x >> 3;
+    const int j = ((int)blockIdx.x - row_blocks) * 64 + l * 8;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    if (j < d) {
+        const int n = min(8, d - j);
+        for (int r = k; r < a.rows; r += 4 * G) {
+            Raw8 dyr[4], hr[4];
+            float rs[4];
+            static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const long long row = r + u * G;
+                if (row < a.rows) {
+                    rs[u] = a.rstd[row];
+                    dyr[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + j, n);
+                    hr[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + j, n);
+                }
+            });
+            static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                if (r + u * G < a.rows) {
+                    float y[8], h[8];
+                    decode8(dyr[u], XT, y);
+                    decode8(hr[u], XT, h);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(y[e], h[e] * rs[u], sum[e]);
+                }
+            });
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) joined[k][l * 8 + e] = sum[e];
+    __syncthreads();
+    // the groups' sums, halved in number until one is left
+    for (int half = G >> 1; half > 0; half >>= 1) {
+        for (int i = threadIdx.x; i < half * 64; i += blockDim.x) joined[i >> 6][i & 63] += joined[(i >> 6) + half][i & 63];
+        __syncthreads();
+    }
+    const int col = ((int)blockIdx.x - row_blocks) * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < d) store1(dweight, WT, (size_t)col, joined[0][threadIdx.x]);
 }
 
 // Rows too long for a workgroup's registers: dw is summed in the workgroup's
@@ -506,8 +621,8 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
                 for (int e = 0; e < 8; ++e) sum[e] += v[e];
             };
             auto load = [&](long long row, Raw8& dyr, Raw8& zr) __attribute__((always_inline)) {
-                dyr = load_raw8<true>(a.dy, a.type, (size_t)(row * a.n) + j, n);
-                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8<true>(a.preact, a.preact_type, (size_t)(row * a.n) + j, n);
+                dyr = load_raw8(a.dy, a.type, (size_t)(row * a.n) + j, n, a.nt);
+                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8(a.preact, a.preact_type, (size_t)(row * a.n) + j, n, a.nt);
             };
             // four rows in flight: each is fetched again as soon as it is used
             Raw8 dyr[4], zr[4];
@@ -542,6 +657,8 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
 
 // ---- host ------------------------------------------------------------------------
 
+// Rows `ld` elements apart that all start on a 16-byte boundary.
+static bool whole_chunks(const void* p, int64_t ld, int t) { return (uintptr_t)p % 16 == 0 && ld * elem_size(t) % 16 == 0; }
 static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld < (1LL << 40); }
 
 struct RowPlan {
@@ -604,13 +721,37 @@ static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
 static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
     return with_types(x_type, w_type, [&](auto x, auto w) { return norm_back_plan<x(), w()>(d); });
 }
+// The kernel for few rows, or none: while dy and h stay in the caches, reading
+// them twice costs less than a second launch and its partial sums, as long as
+// each group of lanes has at most 16 rows to sum (us, bf16, two launches vs
+// one: 1 x 4096 5.4 vs 3.2, 128 x 8192 10.4 vs 5.3, 512 x 4096 15.3 vs 8.8, 1024
+// x 4096 17.6 vs 14.7, 512 x 8192 17.5 vs 13.7; with 32 rows to a group 1000 x
+// 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
+// last step halves their groups.
+template <int XT, int WT>
+static RowPlan norm_back_few(int64_t rows, int64_t d) {
+    const int64_t chunks = (d + 7) / 8;
+    auto pow2 = [](int64_t n) {
+        int t = 256;
+        while (t < n) t *= 2;
+        return t;
+    };
+    if (chunks > 2048 || rows * d > (4 << 20)) return {nullptr, 0, 0};
+    RowPlan p;
+    if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true>, 256, 4};
+    else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false>, pow2(chunks), 1};
+    else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false>, 1024, 1};
+    if (rows > 2 * p.threads) return {nullptr, 0, 0};
+    return p;
+}
+
 // Workgroups of the backward pass, each of which leaves one row of partial
-// sums: about 512 threads per CU, and the same number of rows for all of them
-// but the last ones.  (8192 x 4096 bf16, us: 512 threads per CU 53.6, 768 59.0,
+// sums: about 512 threads per CU (all of them resident), and the same number
+// of rows for all but the last ones.  (8192 x 4096 bf16, us: 512 threads per CU 53.6, 768 59.0,
 // 1024 63.6; 16384 x 1024 28.3, 29.6, 32.6: more workgroups do not read faster,
 // and each leaves d fp32 sums more to write and fold.)
 static int64_t norm_back_grid(const RowPlan& p, int64_t rows, int num_cu) {
-    const int64_t most = std::max<int64_t>(num_cu, (int64_t)num_cu * 512 / p.threads) * p.rows_per_block;
+    const int64_t most = (int64_t)num_cu * std::max(1, 512 / p.threads) * p.rows_per_block;
     const int64_t per = (rows + most - 1) / most * p.rows_per_block;  // rows of a workgroup
     return per > 0 ? (rows + per - 1) / per : 0;
 }
@@ -656,6 +797,7 @@ int64_t act_back_parts(int64_t rows, int64_t n, int num_cu) { return act_back_pl
 int launch_act_back(ActBackArgs a, int num_cu, void* stream) {
     const ActBackPlan p = act_back_plan(a.rows, a.n, num_cu);
     a.rows_per_block = p.rows_per_block;
+    a.nt = whole_chunks(a.dy, a.n, a.type) && whole_chunks(a.preact, a.n, a.preact_type);
     void* args[] = {&a};
     return launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
 }
@@ -700,6 +842,8 @@ int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) 
     *bytes = 0;
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
     if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    // (the plans do not depend on the types)
+    if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16>(rows, d).fn) return GEMM_BT_OK;
     *bytes = (size_t)(norm_back_grid(norm_back_plan_of(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * 4);
     return GEMM_BT_OK;
 }
@@ -713,7 +857,7 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
     if (d == 0) return GEMM_BT_OK;
     if (!dweight || !aligned(dweight, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
     if (rows > 0) {
-        if (!dy || !h || !weight || !rstd || !dx || !workspace) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!dy || !h || !weight || !rstd || !dx || dx == dy) return GEMM_BT_ERR_INVALID_VALUE;
         if (!stride_ok(ld_dy, d) || !stride_ok(ldh, d) || (dh && !stride_ok(ld_dh, d))) return GEMM_BT_ERR_INVALID_VALUE;
         if (!aligned(dy, x_dtype) || !aligned(h, x_dtype) || !aligned(dh, x_dtype) || !aligned(dx, x_dtype) ||
             !aligned(weight, w_dtype) || !aligned(rstd, GEMM_BT_F32) || !aligned(workspace, GEMM_BT_F32))
@@ -724,10 +868,18 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
     if (st != GEMM_BT_OK) return st;
     int64_t grid = 0;
     if (rows > 0) {
+        const RowPlan few = with_types(x_dtype, w_dtype, [&](auto x, auto w) { return norm_back_few<x(), w()>(rows, d); });
+        if (few.fn) {
+            NormBackArgs a = {dy, h, weight, rstd, dh, dx, nullptr, rows, ld_dy, ldh, ld_dh, (int)d, 0};
+            int row_blocks = (int)((rows + few.rows_per_block - 1) / few.rows_per_block);
+            void* args[] = {&a, &row_blocks, &dweight};
+            return launch(few.fn, dim3((unsigned)(row_blocks + (d + 63) / 64)), few.threads, args, stream);
+        }
         const RowPlan p = norm_back_plan_of(x_dtype, w_dtype, d);
         grid = norm_back_grid(p, rows, num_cu);
-        if (workspace_bytes < (size_t)(grid * d * 4)) return GEMM_BT_ERR_INVALID_VALUE;
-        NormBackArgs a = {dy, h, weight, rstd, dh, dx, (float*)workspace, rows, ld_dy, ldh, ld_dh, (int)d};
+        if (!workspace || workspace_bytes < (size_t)(grid * d * 4)) return GEMM_BT_ERR_INVALID_VALUE;
+        NormBackArgs a = {dy, h, weight, rstd, dh, dx, (float*)workspace, rows, ld_dy, ldh, ld_dh, (int)d,
+                          whole_chunks(dy, ld_dy, x_dtype) && whole_chunks(h, ldh, x_dtype) && whole_chunks(dh, ld_dh, x_dtype)};
         void* args[] = {&a};
         st = launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
         if (st != GEMM_BT_OK) return st;

@@ -59,6 +59,7 @@ struct ActBackArgs {
     int ldz;             // row pitch of dz, n or that rounded up to whole groups of 8 (the rest is zeros)
     int rows_per_block;  // set by launch_act_back
     int type, preact_type, act;
+    int nt;              // set by launch_act_back: read past the caches
 };
 int64_t act_back_parts(int64_t rows, int64_t n, int num_cu);
 int launch_act_back(ActBackArgs a, int num_cu, void* stream);

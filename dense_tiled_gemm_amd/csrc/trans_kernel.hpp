@@ -62,11 +62,13 @@ struct OpGeom {
 // One tile of one product, or of a range of its K: the tile at rows m0,
 // columns n0 of C, summed over k in [0, K) of operands that start there.  lda
 // and ldb are the row pitches in elements (A: M or K of the whole matrix, or
-// more; likewise B).  `lds` holds 2 * (GA + GB) bytes.  A K-inner row of K
+// more; likewise B).  `lds` holds S * (GA + GB) bytes, S >= 2 stages: with more
+// than two, the transfers of S - 1 steps are in flight, for grids that leave a
+// compute unit one workgroup and nothing else to cover their latency.  A K-inner row of K
 // elements is read in whole 16-byte chunks, so with K % 8 != 0 its pitch
 // covers them and the elements past K are zeros; a K-outer row likewise past
 // M or N, with any values there.
-template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int WM, int WN>
+template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int WM, int WN, int S = 2>
 __device__ __forceinline__ void trans_body(const u16* A, const u16* B, void* C, int M, int N, int K, int lda, int ldb,
                                            int m0, int n0, bool shifted, unsigned char* lds) {
     constexpr int T = 64 * WM * WN, BK = 64;
@@ -181,25 +183,47 @@ __device__ __forceinline__ void trans_body(const u16* A, const u16* B, void* C, 
         });
     };
 
-    // Two LDS stages: the transfers of tile kt+1 go out into the other stage
-    // (free since the last barrier) before tile kt is multiplied; each wave
-    // then waits for its own transfers and the barrier makes all of them,
-    // and the end of every wave's reads of stage kt, visible.
     const int nk = (K + BK - 1) / BK;
-    issue(0, 0);
-    wait_vmcnt<0>();
-    barrier_no_fence();
-    for (int kt = 0; kt < nk; ++kt) {
-        const int cur = kt & 1;
-        if (kt + 1 < nk) issue(cur ^ 1, kt + 1);
-        compute(cur);
+    if constexpr (S == 2) {
+        // Two LDS stages: the transfers of tile kt+1 go out into the other stage
+        // (free since the last barrier) before tile kt is multiplied; each wave
+        // then waits for its own transfers and the barrier makes all of them,
+        // and the end of every wave's reads of stage kt, visible.
+        issue(0, 0);
+        wait_vmcnt<0>();
+        barrier_no_fence();
+        for (int kt = 0; kt < nk; ++kt) {
+            const int cur = kt & 1;
+            if (kt + 1 < nk) issue(cur ^ 1, kt + 1);
+            compute(cur);
+            wait_vmcnt<0>();
+            barrier_no_fence();
+        }
+    } else {
+        // A ring of S stages: every step issues the same number of transfers
+        // (past the last tile out of range ones, which leave zeros), so "tile kt
+        // has landed" is a fixed count of younger ones.  The stage refilled in
+        // step kt is the one that every wave was done with at its barrier.
+        constexpr int PER = (GA::BYTES + GB::BYTES) / 1024 / W;  // transfers per wave and stage
+        static_assert((S - 2) * PER < 64, "vmcnt range");
+#pragma unroll
+        for (int st = 0; st < S - 1; ++st) issue(st, st);
+        int cs = 0, ls = S - 1;
+        for (int kt = 0; kt < nk; ++kt) {
+            wait_vmcnt<(S - 2) * PER>();
+            barrier_no_fence();
+            issue(ls, kt + S - 1);
+            compute(cs);
+            cs = cs + 1 == S ? 0 : cs + 1;
+            ls = ls + 1 == S ? 0 : ls + 1;
+        }
         wait_vmcnt<0>();
         barrier_no_fence();
     }
 
     // the loop ended on a barrier: LDS is free for the whole-row epilogue
     // (shifted when rows of C are not 16-byte aligned)
-    store_tile_lds<OUT, FN, FM, BM, BN, WM, T, 2 * STAGE, 16>(acc, lds, C, M, N, m0, n0, wm * TM, wn * TN, wm, tid,
+    store_tile_lds<OUT, FN, FM, BM, BN, WM, T, S * STAGE, 16>(acc, lds, C, M, N, m0, n0, wm * TM, wn * TN, wm, tid,
                                                              shifted);
 }
 

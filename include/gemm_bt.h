@@ -302,10 +302,11 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
  * dx is the gradient of x and of residual alike.
  *   h, rstd    as gemm_bt_rms_norm left them (x itself where there was no residual)
  *   dh         the gradient that reaches h from elsewhere, or NULL
- *   dx         rows x d of x_dtype; may be dy or dh itself where its rows are dense
+ *   dx         rows x d of x_dtype; may be dh itself where its rows are dense,
+ *              not dy (INVALID_VALUE)
  *   dweight    d elements of w_dtype
- *   workspace  at least gemm_bt_rms_norm_backward_workspace bytes, 4-byte
- *              aligned, any contents (not used for rows == 0)
+ *   workspace  at least gemm_bt_rms_norm_backward_workspace bytes (0 for few
+ *              rows), 4-byte aligned, any contents
  */
 int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight,
                               const float* rstd, const void* dh, int64_t ld_dh, void* dx, void* dweight,

@@ -84,7 +84,7 @@ def test_quantize_refusals():
     assert q(None, 8, None, None, 0, 8, gb.BF16, gb.INT8) == gb.OK
 
 
-def norm_back(dy=16, h=16, w=16, rstd=16, dh=None, dx=16, dw=16, rows=2, d=8, xt=gb.BF16, wt=gb.BF16, ws=16, n=1 << 20,
+def norm_back(dy=16, h=16, w=16, rstd=16, dh=None, dx=32, dw=16, rows=2, d=8, xt=gb.BF16, wt=gb.BF16, ws=16, n=1 << 20,
               ld=(8, 8, 8)):
     return int(gb.load().gemm_bt_rms_norm_backward(dy, ld[0], h, ld[1], w, rstd, dh, ld[2], dx, dw, rows, d, xt, wt, ws, n,
                                                    None))
@@ -93,7 +93,7 @@ def norm_back(dy=16, h=16, w=16, rstd=16, dh=None, dx=16, dw=16, rows=2, d=8, xt
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), BAD), (dict(d=-1), BAD), (dict(xt=gb.INT8), UNSUP), (dict(wt=gb.F16), UNSUP),
     (dict(dy=None), BAD), (dict(h=None), BAD), (dict(w=None), BAD), (dict(rstd=None), BAD), (dict(dx=None), BAD),
-    (dict(dw=None), BAD), (dict(dw=17), BAD), (dict(ws=None), BAD), (dict(ws=18), BAD), (dict(dx=17), BAD), (dict(rstd=18), BAD),
+    (dict(dw=None), BAD), (dict(dw=17), BAD), (dict(ws=18), BAD), (dict(dx=16), BAD), (dict(dx=17), BAD), (dict(rstd=18), BAD),
     (dict(ld=(7, 8, 8)), BAD), (dict(ld=(8, 7, 8)), BAD), (dict(dh=16, ld=(8, 8, 7)), BAD), (dict(dh=17), BAD),
     (dict(d=0, dw=None), gb.OK),
 ])
@@ -154,6 +154,13 @@ def test_epilogue_plans():
         assert (p.kernel, p.bm, p.bn, p.split_tiles) == (4, 32, 64, 0)
         assert gb.gemm_bt_plan_epi(1, 4097, 4096, i, i).kernel == 3
         assert gb.gemm_bt_plan_ws(1, 4096, 4096, i, i).kernel == 3
+    for i in (gb.BF16, gb.F16):
+        p = gb.gemm_bt_plan_epi(1213, 91, 4279, i, i)             # 38 tiles of 64 x 64, 34 steps of 128
+        assert (p.bm, p.bn, p.bk, p.split_tiles, p.grid) == (64, 64, 128, 38, 38 * 4)
+        assert p.workspace_bytes == 16384 + p.grid * 64 * 64 * 4
+        assert gb.gemm_bt_plan_epi(512, 512, 2944, i, i).split_tiles == 0   # 23 steps
+        assert gb.gemm_bt_plan_epi(512, 512, 2952, i, i).split_tiles == 64
+        assert gb.gemm_bt_plan_epi(1024, 600, 8192, i, i).split_tiles != 160  # more than half the CUs have a tile
     for M, N, K in ((1, 8192, 4096), (17, 4096, 4096), (64, 8192, 8192), (1024, 1024, 16384), (4096, 4096, 4096), (4352, 4096, 4096), (0, 5, 5)):
         for i, o in ((gb.BF16, gb.F32), (gb.F16, gb.F16)):
             assert gb.gemm_bt_plan_epi(M, N, K, i, o).as_dict() == gb.gemm_bt_plan_ws(M, N, K, i, o).as_dict()
@@ -186,11 +193,16 @@ def test_workspace_sizes():
         assert f(-1, 8, ctypes.byref(n)) == BAD and n.value == 0
         assert f(2, 2 ** 31 - 1, ctypes.byref(n)) == UNSUP
         assert f(0, 4096, ctypes.byref(n)) == gb.OK and n.value == 0
-        for rows, d in ((1, 1), (1000, 2050), (100000, 64), (1 << 31, 8), (3, 100000)):
+        for rows, d in ((1, 1), (1000, 2050), (512, 8192), (513, 8192), (512, 8), (513, 8), (100000, 64), (1 << 31, 8), (3, 100000), (8192, 4096)):
             assert f(rows, d, ctypes.byref(n)) == gb.OK
-            # whole rows of fp32 sums, at most one per row of input
-            assert n.value % (4 * d) == 0 and 1 <= n.value // (4 * d) <= rows
+            # whole rows of fp32 sums, at most one per row of input; none for the norm of few rows
+            threads = 256
+            while threads < min(1024, -(-d // 8)):
+                threads *= 2
+            few = (f is lib.gemm_bt_rms_norm_backward_workspace and rows <= 2 * threads and d <= 16384 and rows * d <= 1 << 22)
+            assert n.value % (4 * d) == 0 and (0 if few else 1) <= n.value // (4 * d) <= rows
             assert n.value // (4 * d) <= 65535
+            assert n.value == 0 if few else n.value > 0
 
 
 def test_wrappers_check_before_the_library():

@@ -319,6 +319,31 @@ def test_norm_gradient_against_differences(gpu):
         assert abs(float(dw[j]) - float(want)) <= 1e-5 * (1 + abs(float(want)))
 
 
+@pytest.mark.parametrize("rows,d", [(300, 512), (4000, 512), (2, 20000)])
+def test_norm_backward_into_dh(gpu, rows, d):
+    """dx may take the place of dh; not of dy, which the weight's gradient still reads."""
+    import ctypes
+
+    lib = gpu.load()
+    dy, h, dh = (randn(i, rows, d, dtype=torch.bfloat16).cuda() for i in range(3))
+    w, rstd = randn(3, d, dtype=torch.bfloat16).cuda(), (randn(4, rows).abs() + 0.5).cuda()
+    want = gpu.add_rms_norm_backward(dy, h, w, rstd, dh=dh)
+    need = ctypes.c_size_t()
+    assert lib.gemm_bt_rms_norm_backward_workspace(rows, d, ctypes.byref(need)) == gpu.OK
+    ws = torch.empty(max(need.value, 16), dtype=torch.uint8, device="cuda")
+    dw = torch.empty_like(w)
+
+    def call(dx, nbytes):
+        return lib.gemm_bt_rms_norm_backward(dy.data_ptr(), d, h.data_ptr(), d, w.data_ptr(), rstd.data_ptr(), dh.data_ptr(), d,
+                                             dx.data_ptr(), dw.data_ptr(), rows, d, gpu.BF16, gpu.BF16, ws.data_ptr(), nbytes,
+                                             torch.cuda.current_stream().cuda_stream)
+    assert call(dy, need.value) == gpu.ERR_INVALID_VALUE
+    if need.value:
+        assert call(dh, need.value - 4) == gpu.ERR_INVALID_VALUE
+    assert call(dh, need.value) == gpu.OK
+    assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+
+
 def test_norm_backward_layouts_and_no_rows(gpu):
     wide = randn(40, 30, 400, dtype=torch.bfloat16)
     dy, h, dh = wide[:, 1:130], wide[:, 130:259], wide[:, 260:389]
@@ -351,7 +376,7 @@ def act64(z, act):
 
 def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False, scales=False, seed=0, offset=0, xw=None):
     """One call, every entry: the fp32 sums themselves are the plain product's (checked against the oracle elsewhere), from
-    the same tiles, or for M <= 16 sums of the same terms in another order; what follows them is computed here in 64 bits."""
+    the same tiles (else sums of the same terms in another order); what follows them is computed here in 64 bits."""
     say("linear", M, N, K, ind, outd, act, "bias", bias, "res", res, "pre", pre, "scales", scales, "seed", seed)
     if ind == "i8":
         x, w = (torch.randint(-128, 128, s, generator=gen(seed + i), dtype=torch.int8) for i, s in enumerate(((M, K), (N, K))))
@@ -373,8 +398,10 @@ def check_epilogue(gpu, M, N, K, ind, outd, act, bias=None, res=None, pre=False,
         s = gpu.mm_bt(x.cuda(), w.cuda(), out_dtype=torch.int32 if ind == "i8" else torch.float32).cpu().double()
     z = s
     tol = u * s.abs() if ind == "i8" else torch.zeros_like(s)
-    if M <= 16 and ind in DT:
-        tol = 2 * K * u * (x.double().abs() @ w.double().abs().t())
+    if ind in DT:
+        c = {"bf16": gpu.BF16, "f16": gpu.F16}[ind]
+        if gpu.gemm_bt_plan_epi(M, N, K, c, gpu.F32).as_dict() != gpu.gemm_bt_plan_ws(M, N, K, c, gpu.F32).as_dict():
+            tol = 2 * K * u * (x.double().abs() @ w.double().abs().t())
     if scales:
         z = z * xs.double()[:, None] * ws.double()
         tol = tol * xs.double()[:, None] * ws.double() + 2 * u * z.abs()
@@ -397,7 +424,8 @@ SHAPES16 = [(1, 1, 1), (1, 64, 64), (1, 4100, 2048), (16, 8192, 1000), (7, 5001,
             (64, 64, 64), (64, 4100, 8192), (100, 2050, 134), (130, 264, 73), (257, 513, 129), (300, 700, 1000),
             (512, 512, 16384), (1024, 1024, 16384), (520, 1000, 16392), (700, 3200, 130), (1000, 1000, 136), (1000, 2999, 72), (1000, 3000, 136),
             (1000, 3000, 128), (1030, 1030, 202), (2000, 4000, 192), (2048, 1536, 72), (2048, 4004, 72), (3000, 1000, 72),
-            (3000, 1000, 128), (4096, 4096, 130), (4100, 4100, 136), (4352, 4096, 64), (700, 2000, 1000), (1024, 4096, 128)]
+            (3000, 1000, 128), (4096, 4096, 130), (4100, 4100, 136), (4352, 4096, 64), (700, 2000, 1000), (1024, 4096, 128),
+            (1213, 91, 4279), (100, 64, 4096), (300, 333, 8192), (65, 1000, 3000)]
 
 
 def options(i):
