@@ -77,12 +77,26 @@ __device__ __forceinline__ void store_codes(void* p, int qt, size_t i, int n, co
     }
 }
 
-// A row's scale, from the bits of its largest magnitude: amax / 448 (E4M3) or
-// amax / 127 (int8), kept above 2^-100 so that its reciprocal is finite; NaN
-// for a row that holds an infinity or a NaN.
-__device__ __forceinline__ float row_scale_of(float amax, int qt) {
-    if (as_u32(amax) >= 0x7F800000u) return as_f32(0x7FC00000u);
-    return __builtin_fmaxf(amax / (qt == GEMM_BT_FP8_E4M3 ? 448.0f : 127.0f), 0x1p-100f);
+// Rows in 8 bits are taken from t = (h p) w instead of y = h rstd w, p the power
+// of two below rstd: t has one rounding where y has two, the factor that y has
+// more, rstd / p, is one of the whole row, and codes do not depend on it.
+__device__ __forceinline__ float power_below(float rstd) {
+    return __builtin_fmaxf(as_f32(as_u32(rstd) & 0x7F800000u), 0x1p-126f);
+}
+
+// The scale of a row of values t * rest, and what t is multiplied by for its
+// codes, from the largest |t|: scale = amax rest / Q, Q = 448 (E4M3) or 127
+// (int8), kept above 2^-100 so that its reciprocal is finite; NaN for a row that
+// holds an infinity or a NaN.
+struct RowScale {
+    float scale, code;
+};
+__device__ __forceinline__ RowScale row_scale_of(float amax, float rest, int qt) {
+    const float q = qt == GEMM_BT_FP8_E4M3 ? 448.0f : 127.0f, nan = as_f32(0x7FC00000u);
+    if (as_u32(amax) >= 0x7F800000u) return {nan, nan};
+    const float s = amax * rest / q;
+    if (!(s >= 0x1p-100f)) return {0x1p-100f, rest * 0x1p100f};
+    return {s, q / amax};
 }
 
 // ---- norm and quantisation, forward ----------------------------------------------
@@ -182,6 +196,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             });
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
+        const bool codes = is_code_type(a.y_type);
+        const float factor = codes && a.weight ? power_below(rstd) : rstd;
         float amax = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
@@ -191,23 +207,23 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
                     float w[8];
                     decode8(wr[u], WT, w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * rstd * w[e];
+                    for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * factor * w[e];
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[u][e]));
-                if (!is_code_type(a.y_type)) store8(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
+                if (!codes) store8(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
             }
         });
-        if (is_code_type(a.y_type)) {
+        if (codes) {
             amax = row_join<MaxBitsOp, WAVE>(amax, part[2 + flip]);
-            const float s = row_scale_of(amax, a.y_type), inv = 1.0f / s;
-            if (t == 0) a.scale[row] = s;
+            const RowScale s = row_scale_of(amax, rstd / factor, a.y_type);
+            if (t == 0) a.scale[row] = s.scale;
             static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
                 constexpr int u = decltype(uc)::value;
                 const int i = (u * T + renew(t)) * 8;
                 if (i < d) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[u][e] *= inv;
+                    for (int e = 0; e < 8; ++e) h[u][e] *= s.code;
                     store_codes(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
                 }
             });
@@ -234,16 +250,17 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
                 for (int e = 0; e < 8; ++e) h[e] += v[e];
             }
         };
-        auto load_y = [&](int i, int n, float rstd, float (&h)[8]) __attribute__((always_inline)) {
+        auto load_y = [&](int i, int n, float factor, float (&h)[8]) __attribute__((always_inline)) {
             load_h(i, n, h);
             if (a.weight) {
                 float w[8];
                 decode8(load_raw8(a.weight, WT, (size_t)i, n), WT, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = h[e] * rstd * w[e];
+                for (int e = 0; e < 8; ++e) h[e] = h[e] * factor * w[e];
             }
         };
-        float rstd = 1.0f, inv = 1.0f, h[8];
+        const bool codes = is_code_type(a.y_type);
+        float rstd = 1.0f, code = 1.0f, h[8];
         if (a.weight) {
             float ss = 0.0f;
             for (long long i = t * 8; i < a.d; i += T * 8) {
@@ -261,17 +278,18 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
             });
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
-        if (is_code_type(a.y_type)) {
+        const float factor = codes && a.weight ? power_below(rstd) : rstd;
+        if (codes) {
             float amax = 0.0f;
             for (long long i = t * 8; i < a.d; i += T * 8) {
-                load_y((int)i, min(8, a.d - (int)i), rstd, h);
+                load_y((int)i, min(8, a.d - (int)i), factor, h);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[e]));
             }
             amax = row_join<MaxBitsOp, false>(amax, part[2 + flip]);
-            const float s = row_scale_of(amax, a.y_type);
-            inv = 1.0f / s;
-            if (t == 0) a.scale[row] = s;
+            const RowScale s = row_scale_of(amax, rstd / factor, a.y_type);
+            code = s.code;
+            if (t == 0) a.scale[row] = s.scale;
         }
         for (long long i = t * 8; i < a.d; i += T * 8) {
             const int n = min(8, a.d - (int)i);
@@ -279,16 +297,16 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
             if (a.h) {
                 load_h((int)i, n, h);
                 float y[8];
-                load_y((int)i, n, rstd, y);
+                load_y((int)i, n, factor, y);
                 store8(a.h, XT, at, n, h);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = y[e];
             } else {
-                load_y((int)i, n, rstd, h);
+                load_y((int)i, n, factor, h);
             }
-            if (is_code_type(a.y_type)) {
+            if (codes) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] *= inv;
+                for (int e = 0; e < 8; ++e) h[e] *= code;
                 store_codes(a.y, a.y_type, at, n, h);
             } else {
                 store8(a.y, a.y_type, at, n, h);
@@ -723,10 +741,10 @@ static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
 }
 // The kernel for few rows, or none: while dy and h stay in the caches, reading
 // them twice costs less than a second launch and its partial sums, as long as
-// each group of lanes has at most 16 rows to sum (us, bf16, two launches vs
-// one: 1 x 4096 5.4 vs 3.2, 128 x 8192 10.4 vs 5.3, 512 x 4096 15.3 vs 8.8, 1024
-// x 4096 17.6 vs 14.7, 512 x 8192 17.5 vs 13.7; with 32 rows to a group 1000 x
-// 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
+// each group of lanes has at most 8 rows to sum (us, bf16, two launches vs
+// one: 1 x 4096 5.4 vs 3.2, 128 x 8192 10.4 vs 5.3, 512 x 4096 15.3 vs 8.8, 512 x
+// 8192 17.5 vs 13.7; with 16 rows to a group 1000 x 2050 fp32 16.0 vs 19.6, with
+// 32 1000 x 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
 // last step halves their groups.
 template <int XT, int WT>
 static RowPlan norm_back_few(int64_t rows, int64_t d) {
@@ -741,7 +759,7 @@ static RowPlan norm_back_few(int64_t rows, int64_t d) {
     if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true>, 256, 4};
     else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false>, pow2(chunks), 1};
     else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false>, 1024, 1};
-    if (rows > 2 * p.threads) return {nullptr, 0, 0};
+    if (rows > p.threads) return {nullptr, 0, 0};
     return p;
 }
 

@@ -193,13 +193,13 @@ def test_workspace_sizes():
         assert f(-1, 8, ctypes.byref(n)) == BAD and n.value == 0
         assert f(2, 2 ** 31 - 1, ctypes.byref(n)) == UNSUP
         assert f(0, 4096, ctypes.byref(n)) == gb.OK and n.value == 0
-        for rows, d in ((1, 1), (1000, 2050), (512, 8192), (513, 8192), (512, 8), (513, 8), (100000, 64), (1 << 31, 8), (3, 100000), (8192, 4096)):
+        for rows, d in ((1, 1), (1000, 2050), (512, 8192), (512, 8193), (512, 4096), (513, 4096), (256, 8), (257, 8), (100000, 64), (1 << 31, 8), (3, 100000), (8192, 4096)):
             assert f(rows, d, ctypes.byref(n)) == gb.OK
             # whole rows of fp32 sums, at most one per row of input; none for the norm of few rows
             threads = 256
             while threads < min(1024, -(-d // 8)):
                 threads *= 2
-            few = (f is lib.gemm_bt_rms_norm_backward_workspace and rows <= 2 * threads and d <= 16384 and rows * d <= 1 << 22)
+            few = (f is lib.gemm_bt_rms_norm_backward_workspace and rows <= threads and d <= 16384 and rows * d <= 1 << 22)
             assert n.value % (4 * d) == 0 and (0 if few else 1) <= n.value // (4 * d) <= rows
             assert n.value // (4 * d) <= 65535
             assert n.value == 0 if few else n.value > 0
