@@ -19,7 +19,7 @@
 
 namespace gbt {
 
-// One of the two products, in tiles of BT x BT, each tile's K steps of 64 in
+// One of the two products, in tiles of BM x BN, each tile's K steps of 64 in
 // `pieces` runs of `per` steps.  A single piece is rounded into `out`; of
 // several, piece j leaves fp32 sums in `parts` + j * rows * cols.
 struct BackProduct {
@@ -38,10 +38,11 @@ struct BackProduct {
 };
 struct BackArgs {
     BackProduct dw, dx;
+    int dx_first;   // the product whose runs are longer goes first, so that the shorter ones fill what it leaves
     FoldArgs fold;  // out == nullptr: none
 };
 
-template <int IN, bool TA, int BT, int WN, int S>
+template <int IN, bool TA, int BM, int BN, int WN, int S>
 __device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigned char* lds) {
     const int total = p.tiles_m * p.tiles_n * p.pieces;
     if (pid >= total) return;
@@ -55,22 +56,23 @@ __device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigne
     const u16* a = TA ? p.a + (size_t)k0 * p.lda : p.a + k0;
     const u16* b = p.b + (size_t)k0 * p.ldb;
     if (p.pieces == 1)
-        trans_body<IN, IN, TA, true, BT, BT, 2, WN, S>(a, b, p.out, p.rows, p.cols, depth, p.lda, p.ldb, (int)tm * BT,
-                                                    (int)tn * BT, p.shifted, lds);
+        trans_body<IN, IN, TA, true, BM, BN, 2, WN, S>(a, b, p.out, p.rows, p.cols, depth, p.lda, p.ldb, (int)tm * BM,
+                                                       (int)tn * BN, p.shifted, lds);
     else
-        trans_body<IN, GEMM_BT_F32, TA, true, BT, BT, 2, WN, S>(a, b, p.parts + (size_t)j * p.rows * p.cols, p.rows, p.cols,
-                                                             depth, p.lda, p.ldb, (int)tm * BT, (int)tn * BT,
-                                                             p.shifted_parts, lds);
+        trans_body<IN, GEMM_BT_F32, TA, true, BM, BN, 2, WN, S>(a, b, p.parts + (size_t)j * p.rows * p.cols, p.rows, p.cols,
+                                                                depth, p.lda, p.ldb, (int)tm * BM, (int)tn * BN,
+                                                                p.shifted_parts, lds);
 }
 
-template <int IN, int BT, int WN, int S>
+template <int IN, int BM, int BN, int WN, int S>
 __global__ __launch_bounds__(128 * WN) void linear_back_kernel(const BackArgs a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[S * 2 * BT * 64 * 2];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S * (BM + BN) * 64 * 2];
     int blk = blockIdx.x;
-    if (blk < a.dw.blocks) return back_tile<IN, true, BT, WN, S>(a.dw, blk, lds);
-    blk -= a.dw.blocks;
-    if (blk < a.dx.blocks) return back_tile<IN, false, BT, WN, S>(a.dx, blk, lds);
-    fold_columns<128 * WN>(a.fold, blk - a.dx.blocks, (float(*)[17])lds);
+    const int w0 = a.dx_first ? a.dx.blocks : 0, x0 = a.dx_first ? 0 : a.dw.blocks;
+    if (blk >= w0 && blk < w0 + a.dw.blocks) return back_tile<IN, true, BM, BN, WN, S>(a.dw, blk - w0, lds);
+    if (blk >= x0 && blk < x0 + a.dx.blocks) return back_tile<IN, false, BM, BN, WN, S>(a.dx, blk - x0, lds);
+    blk -= a.dw.blocks + a.dx.blocks;
+    fold_columns<128 * WN>(a.fold, blk, (float(*)[17])lds);
 }
 
 // out = sum of `pieces` slices of n fp32 sums, in order, rounded once.
@@ -128,7 +130,7 @@ static int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // parts lie in the workspace (byte offsets; the sizes do not depend on which
 // gradients are asked for).
 struct BackPlan {
-    int bt;
+    int bm, bn;
     bool make_dz, pad;
     int64_t ldz, ldk;  // row pitches of dz, and of X and W (elements)
     int pieces_w, per_w, pieces_x, per_x;
@@ -153,25 +155,67 @@ static void cut(int64_t steps, int64_t fair, int64_t least, int64_t most, int* p
     *pieces = (int)std::max<int64_t>(1, (steps + *per - 1) / *per);
 }
 
+// Steps until the last of `cu` compute units is done, when t1 runs of s1 steps
+// and then t2 of s2 <= s1 go to whichever is free first.
+static int64_t makespan(int64_t t1, int64_t s1, int64_t t2, int64_t s2, int64_t cu) {
+    const int64_t rounds = t1 / cu, rest = t1 % cu;
+    int64_t T = std::max((rest ? rounds + 1 : rounds) * s1, (t1 * s1 + t2 * s2 + cu - 1) / cu);
+    if (t2 == 0) return T;
+    auto fits = [&](int64_t at) {  // runs of s2 done by then
+        const int64_t late = std::max<int64_t>(0, at - (rounds + 1) * s1) / s2, early = std::max<int64_t>(0, at - rounds * s1) / s2;
+        return rest * late + (cu - rest) * early >= t2;
+    };
+    while (!fits(T)) ++T;
+    return T;
+}
+
+// The tile shapes, and what one of their K steps takes on a compute unit that
+// is kept busy (us; 128 x 128: of two workgroups on a unit, per workgroup).
+struct BackTile {
+    int bm, bn;
+    double step, ragged;  // ragged: where rows of dz, X or W do not start on 128-byte lines (narrow tiles then fetch
+                          // more lines for the same columns)
+};
+constexpr BackTile kBackTiles[] = {{128, 128, 0.60, 0.69}, {128, 256, 1.05, 1.15}, {256, 256, 1.5, 1.57}};
+
+// The plan with the shortest estimate: the longest unit's steps (each run three
+// more, for its start and its stores), and the slices' way to memory and back.
+// Whole calls on 128 x 128, 128 x 256 and 256 x 256 tiles (M x N x K, us, bf16):
+// 2048^3 49.1, 46.4, 61.6; 4096x4096x1024 99.4, 91.4, 107.0; 528x1728x7040 50.8,
+// 55.8, 62.0; 8192x1024x4096 167.7, 159.8, 152.9; 4096^3 302.6, 284.1, 236.8.
+// The longer runs first, instead of dW always: 2048x4096x4096 147.8 -> 129.5,
+// 1024x4096x4096 92.4 -> 79.8, 528x1728x7040 50.8 -> 45.8.
 static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu) {
     BackPlan p = {};
     p.make_dz = act || N % 8 != 0;
     p.pad = K % 8 != 0;
     p.ldz = up8(N);
     p.ldk = up8(K);
-    auto tiles = [](int64_t r, int64_t c, int64_t bt) { return ((r + bt - 1) / bt) * ((c + bt - 1) / bt); };
-    // the tile rule of the products with operands stored K-outer, for the tiles
-    // of both products together
-    const int64_t big = tiles(M, K, 256) + tiles(N, K, 256), small = tiles(M, K, 128) + tiles(N, K, 128);
-    const bool use_big = big == num_cu || big * 8 > (int64_t)num_cu * 11 || (big < num_cu && big * 2 >= num_cu && small > num_cu);
-    p.bt = use_big ? 256 : 128;
     const int64_t steps_w = (M + 63) / 64, steps_x = (N + 63) / 64;
-    const int64_t work = tiles(N, K, p.bt) * steps_w + tiles(M, K, p.bt) * steps_x;
-    const int64_t fair = (work + num_cu - 1) / num_cu;
-    const int64_t least = 12;
-    const int64_t most = 0x7FFFFFFFLL / (128 * std::max(p.ldz, p.ldk));  // steps of 64 rows below 2 GiB
-    cut(steps_w, fair, least, std::max<int64_t>(1, most), &p.pieces_w, &p.per_w);
-    cut(steps_x, fair, least, std::max<int64_t>(1, most), &p.pieces_x, &p.per_x);
+    const int64_t most = std::max<int64_t>(1, 0x7FFFFFFFLL / (128 * std::max(p.ldz, p.ldk)));  // steps of 64 rows below 2 GiB
+    double best = 0.0;
+    for (const BackTile& t : kBackTiles) {
+        auto tiles = [&](int64_t r, int64_t c) { return ((r + t.bm - 1) / t.bm) * ((c + t.bn - 1) / t.bn); };
+        const int64_t tiles_w = tiles(N, K), tiles_x = tiles(M, K);
+        const int64_t fair = (tiles_w * steps_w + tiles_x * steps_x + num_cu - 1) / num_cu;
+        int pieces_w, per_w, pieces_x, per_x;
+        cut(steps_w, fair, 12, most, &pieces_w, &per_w);
+        cut(steps_x, fair, 12, most, &pieces_x, &per_x);
+        const int64_t runs_w = tiles_w * pieces_w, runs_x = tiles_x * pieces_x;
+        const int64_t span = per_w >= per_x ? makespan(runs_w, per_w + 3, runs_x, per_x + 3, num_cu)
+                                            : makespan(runs_x, per_x + 3, runs_w, per_w + 3, num_cu);
+        const double slices = (pieces_w > 1 ? (double)pieces_w * N * K : 0.0) + (pieces_x > 1 ? (double)pieces_x * M * K : 0.0);
+        const bool lines = p.ldz % 64 == 0 && p.ldk % 64 == 0;
+        const double time = (lines ? t.step : t.ragged) * span + slices * 8.0 / 4e6 + (slices > 0.0 ? 3.0 : 0.0);
+        if (best > 0.0 && time >= best) continue;
+        best = time;
+        p.bm = t.bm;
+        p.bn = t.bn;
+        p.pieces_w = pieces_w;
+        p.per_w = per_w;
+        p.pieces_x = pieces_x;
+        p.per_x = per_x;
+    }
     p.sums_parts = M > 0 && N > 0 ? act_back_parts(M, N, num_cu) : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -241,8 +285,8 @@ static int linear_backward(const void* dy, const void* x, const void* w, const v
         q.depth = (int)depth;
         q.lda = (int)lda;
         q.ldb = (int)ldb;
-        q.tiles_m = (int)((rows + p.bt - 1) / p.bt);
-        q.tiles_n = (int)((cols + p.bt - 1) / p.bt);
+        q.tiles_m = (int)((rows + p.bm - 1) / p.bm);
+        q.tiles_n = (int)((cols + p.bn - 1) / p.bn);
         q.pieces = pieces;
         q.per = per;
         q.blocks = (q.tiles_m * q.tiles_n * pieces + 7) / 8 * 8;
@@ -253,6 +297,7 @@ static int linear_backward(const void* dy, const void* x, const void* w, const v
     BackArgs a = {};
     a.dw = product(dz, x, dw, (float*)(ws + p.off_parts_w), N, K, M, p.ldz, p.ldk, p.pieces_w, p.per_w);
     a.dx = product(dz, w, dx, (float*)(ws + p.off_parts_x), M, K, N, p.ldz, p.ldk, p.pieces_x, p.per_x);
+    a.dx_first = a.dx.steps() > a.dw.steps();
     unsigned grid = (unsigned)(a.dw.blocks + a.dx.blocks);
     if (dbias) {
         a.fold = {(const float*)(ws + p.off_sums), dbias, N, (int)p.sums_parts, type};
@@ -263,16 +308,17 @@ static int linear_backward(const void* dy, const void* x, const void* w, const v
     // steps: a ring of four stages in place of two workgroups' worth of two (us:
     // 1024x1024x1024 22.6 vs 20.4, 2048x1024x1024 35.0 vs 30.3; with 8 steps
     // the longer start loses, 4096x512x512 25.1 vs 28.5)
-    const bool deep = p.bt == 128 && a.dw.blocks + a.dx.blocks <= num_cu && std::max(a.dw.steps(), a.dx.steps()) >= 16;
+    const bool deep = p.bn == 128 && a.dw.blocks + a.dx.blocks <= num_cu && std::max(a.dw.steps(), a.dx.steps()) >= 16;
     auto pick = [&](auto in) -> const void* {
         constexpr int IN = decltype(in)::value;
-        if (p.bt == 256) return (const void*)&linear_back_kernel<IN, 256, 4, 2>;
-        return deep ? (const void*)&linear_back_kernel<IN, 128, 2, 4> : (const void*)&linear_back_kernel<IN, 128, 2, 2>;
+        if (p.bm == 256) return (const void*)&linear_back_kernel<IN, 256, 256, 4, 2>;
+        if (p.bn == 256) return (const void*)&linear_back_kernel<IN, 128, 256, 4, 3>;
+        return deep ? (const void*)&linear_back_kernel<IN, 128, 128, 2, 4> : (const void*)&linear_back_kernel<IN, 128, 128, 2, 2>;
     };
     const void* fn = type == GEMM_BT_BF16 ? pick(std::integral_constant<int, GEMM_BT_BF16>{})
                                           : pick(std::integral_constant<int, GEMM_BT_F16>{});
     void* args[] = {&a};
-    st = launch(fn, dim3(grid), p.bt == 256 ? 512 : 256, args, stream);
+    st = launch(fn, dim3(grid), p.bn == 256 ? 512 : 256, args, stream);
     if (st != GEMM_BT_OK) return st;
     SliceArgs s = {};
     s.type = type;
