@@ -64,6 +64,8 @@ __device__ __forceinline__ void back_tile(const BackProduct& p, int pid, unsigne
                                                                 p.shifted_parts, lds);
 }
 
+// Bound by the tiles' operand reads (see trans_kernel.hpp): 4096^3 bf16, both
+// products, 220 us (1250 TFLOP/s); 2048^3 38 us; 1000x512x2048 12 us.
 template <int IN, int BM, int BN, int WN, int S>
 __global__ __launch_bounds__(128 * WN) void linear_back_kernel(const BackArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[S * (BM + BN) * 64 * 2];

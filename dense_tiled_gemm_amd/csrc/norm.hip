@@ -142,6 +142,12 @@ struct NormArgs {
 
 __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
 
+// h = x + residual; y = h rstd w: one pass over x and the residual, whose row
+// stays in registers between its statistics and its results.  Bound by HBM:
+// 8192 x 8192 bf16 with residual 92 us (5.8 TB/s; a plain copy reaches 5.1),
+// to E4M3 83 us, 4096 x 4096 quantised alone 11.4 us; one row of 4096 2.8 us, a
+// launch.  Inputs are read through the caches, where the kernel before may have
+// left them (8192 x 8192 without residual 43 us against 50 past them).
 // The T threads that hold a row, U chunks of 8 elements each (T * U * 8 >= d),
 // are a wave (WAVE; a workgroup is up to 4 of them, each with rows of its own) or
 // the whole workgroup, of as many waves as the row fills.
@@ -335,6 +341,8 @@ struct NormBackArgs {
     int nt;
 };
 
+// Bound by HBM: 8192 x 4096 bf16 with dh 49 us for this kernel and 4 for the
+// fold of its partial sums (5.1 TB/s in all).
 // With xhat = h rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + dh, and
 // dw = sum over rows of dy xhat.  Layout as in norm_kernel; each thread sums
 // dw of its own columns over the workgroup's rows in registers, and the
@@ -608,6 +616,7 @@ __global__ __launch_bounds__(512) void fold_kernel(const FoldArgs a) {
 
 // ---- activation and bias, backward -------------------------------------------------
 
+// Bound by HBM: 4096 x 4096 bf16 22 us (4.6 TB/s), 8192 x 8192 77 (5.2).
 // dz = dy act'(z), and the sums of dz over a block of rows.  L lanes hold 8
 // columns each; a workgroup's 256 / L groups of lanes take its rows in turn.
 template <int L>

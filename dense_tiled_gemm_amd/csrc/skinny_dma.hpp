@@ -282,6 +282,8 @@ __global__ __launch_bounds__(64 * W) void skinny_dma_kernel(const u16* __restric
     skinny_body<IN, OUT, BN, KB, STAGES, W, ROT>(A, B, C, M, N, K, vec_store, SkinnyPlain{});
 }
 
+// With an epilogue, in any input type: bound by one read of B (16 x 8192 x 8192
+// bf16 with bias and silu 26.1 us, 5.2 TB/s, as without; int8 15.8 us, 4.2).
 template <int IN, int BN, int KB, int STAGES, int W>
 __global__ __launch_bounds__(64 * W) void skinny_epi_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
                                                            void* __restrict__ C, int M, int N, int K,
