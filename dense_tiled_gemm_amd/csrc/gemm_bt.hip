@@ -1225,7 +1225,7 @@ using namespace gbt;
 
 extern "C" {
 
-int gemm_bt_version(void) { return 20000; }
+int gemm_bt_version(void) { return 20100; }
 
 const char* gemm_bt_status_string(int status) {
     switch (status) {
@@ -1406,10 +1406,16 @@ int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int
             return GEMM_BT_ERR_INVALID_VALUE;
     }
     static_assert(GEMM_BT_F32 == 0, "the scales' type adds no bits");
-    // nothing to do to the sums of a floating-point product on the plain plan:
-    // the plain kernel (4096^3 bf16 94 us, through the epilogue 102)
-    const bool plain = e.mode == out_dtype << EPI_OUT_TYPE && (in_dtype == GEMM_BT_BF16 || in_dtype == GEMM_BT_F16) && M > 64;
-    if (plain) return gemm_bt_ws(A, B, C, M, N, K, in_dtype, out_dtype, workspace, workspace_bytes, stream);
+    // nothing to do to the sums of a 16-bit product that is planned as the plain
+    // one: its kernel (4096^3 bf16 94 us, through the epilogue 102)
+    if (e.mode == out_dtype << EPI_OUT_TYPE && (in_dtype == GEMM_BT_BF16 || in_dtype == GEMM_BT_F16)) {
+        gemm_bt_plan_t plain, with;
+        const int cus = plan_cus(), a_al = align_of(A), b_al = align_of(B), c_al = align_of(C);
+        const int st1 = plan_impl(1, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, cus, workspace != nullptr, &plain);
+        const int st2 = plan_impl(1, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, cus, workspace != nullptr, &with, true);
+        if (st1 == st2 && std::memcmp(&plain, &with, sizeof(plain)) == 0)
+            return gemm_bt_ws(A, B, C, M, N, K, in_dtype, out_dtype, workspace, workspace_bytes, stream);
+    }
     return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, epi_plan_type(in_dtype, out_dtype), workspace, workspace_bytes, stream, &e);
 }
 

@@ -237,7 +237,10 @@ static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu)
 static bool sizes_ok(int64_t M, int64_t N, int64_t K) {
     // 32-bit buffer offsets inside one panel of 256 rows, and of 64 steps of K
     const int64_t most = 0x7FFFFFFFLL / 1024;
-    return M <= 0x7FFFFFFF - 256 && N <= most && K <= most;
+    if (M > 0x7FFFFFFF - 256 || N > most || K > most) return false;
+    // and a grid of at most 2^32 threads, 512 or fewer to a tile: 2^21 tiles of 128 x 128 of each product
+    const int64_t tiles = ((M + 127) / 128) * ((K + 127) / 128), tiles_w = ((N + 127) / 128) * ((K + 127) / 128);
+    return tiles <= 1 << 21 && tiles_w <= 1 << 21;
 }
 
 static int fill_zero(void* out, int64_t n, void* stream) {

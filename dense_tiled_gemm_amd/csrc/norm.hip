@@ -684,6 +684,9 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
 
 // ---- host ------------------------------------------------------------------------
 
+// One thread per 16 columns and row group of the fold, in a grid of at most 2^32
+// threads; int offsets inside a row.
+constexpr int64_t kMaxColumns = 1 << 26;
 // Rows `ld` elements apart that all start on a 16-byte boundary.
 static bool whole_chunks(const void* p, int64_t ld, int t) { return (uintptr_t)p % 16 == 0 && ld * elem_size(t) % 16 == 0; }
 static bool stride_ok(int64_t ld, int64_t d) { return ld >= d && ld < (1LL << 40); }
@@ -841,7 +844,7 @@ int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t l
     if (rows < 0 || d < 0 || !(eps >= 0.0f)) return GEMM_BT_ERR_INVALID_VALUE;
     const bool codes = y_dtype == GEMM_BT_FP8_E4M3 || y_dtype == GEMM_BT_INT8;
     if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype) || !(codes || float_type(y_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
-    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (rows == 0 || d == 0) return GEMM_BT_OK;
     if (!x || !weight || !y || (codes && !scale)) return GEMM_BT_ERR_INVALID_VALUE;
     if (!stride_ok(ldx, d) || (residual && !stride_ok(ldr, d))) return GEMM_BT_ERR_INVALID_VALUE;
@@ -856,7 +859,7 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
                           int q_dtype, void* stream) {
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
     if (!float_type(x_dtype) || (q_dtype != GEMM_BT_FP8_E4M3 && q_dtype != GEMM_BT_INT8)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (rows == 0 || d == 0) return GEMM_BT_OK;
     if (!x || !q || !scale || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
     if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
@@ -868,7 +871,7 @@ int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) 
     if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
     *bytes = 0;
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
-    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     // (the plans do not depend on the types)
     if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16>(rows, d).fn) return GEMM_BT_OK;
     *bytes = (size_t)(norm_back_grid(norm_back_plan_of(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * 4);
@@ -880,7 +883,7 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
                               int64_t d, int x_dtype, int w_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
     if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (d > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (d == 0) return GEMM_BT_OK;
     if (!dweight || !aligned(dweight, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
     if (rows > 0) {
@@ -918,7 +921,7 @@ int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes) {
     if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
     *bytes = 0;
     if (rows < 0 || n < 0) return GEMM_BT_ERR_INVALID_VALUE;
-    if (n > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (n > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (rows > 0 && n > 0) *bytes = (size_t)(act_back_plan(rows, n, plan_cus()).blocks * n * 4);
     return GEMM_BT_OK;
 }
@@ -931,7 +934,7 @@ int gemm_bt_act_backward(const void* dy, const void* preact, void* dz, void* dbi
     const bool act = activation != GEMM_BT_ACT_NONE;
     if (!float_type(dtype) || (act && !float_type(preact_dtype)) || (dbias && !float_type(bias_dtype)))
         return GEMM_BT_ERR_UNSUPPORTED;
-    if (n > 0x7FFFFFFF - 8192 || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (n > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (n == 0) return GEMM_BT_OK;
     if (dbias && !aligned(dbias, bias_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
     if (rows > 0) {

@@ -262,8 +262,8 @@ int gemm_bt_epi_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, in
  * >= d), outputs are dense.  x, residual and h share x_dtype; a weight is of
  * x_dtype or GEMM_BT_F32 (else UNSUPPORTED).  Pointers need the alignment of
  * their elements only; every size from 0 up is served (no rows: nothing is
- * written but a gradient's zeros; up to 2^31 - 8193 columns and 2^31 rows,
- * else UNSUPPORTED).  Statistics are held in fp32 and every output is rounded
+ * written but a gradient's zeros; up to 2^26 columns and 2^31 rows, else
+ * UNSUPPORTED).  Statistics are held in fp32 and every output is rounded
  * once.  Results are the same bits on every run on the same device.  Calls
  * are asynchronous on `stream`, allocate nothing and report argument errors
  * before anything is enqueued, as the products do.
@@ -343,7 +343,7 @@ int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes);
  *   dx, dw, dbias  M x K, N x K and N elements of dtype; NULL: not wanted
  *   workspace  at least gemm_bt_linear_backward_workspace bytes, 16-byte
  *              aligned, any contents
- * N and K up to 2^21 - 1.  x, w and (for GEMM_BT_ACT_NONE with N % 8 == 0) dy
+ * N and K up to 2^21 - 1, dx and dw up to 2^21 tiles of 128 x 128 each.  x, w and (for GEMM_BT_ACT_NONE with N % 8 == 0) dy
  * need 16-byte alignment where K % 8 == 0 (else UNSUPPORTED); the rest needs
  * the alignment of its elements.  A gradient whose sum has no terms is zeros.
  * The gradient of an epilogue's residual is dy itself.

@@ -121,6 +121,7 @@ def lin_back(dy=16, x=16, w=16, z=16, dx=16, dw=16, db=16, M=4, N=8, K=8, act=1,
 
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=-1), BAD), (dict(act=9), BAD), (dict(t=gb.F32), UNSUP),
+    (dict(M=1 << 30, K=1 << 20), UNSUP), (dict(N=(1 << 21) - 1, K=(1 << 21) - 1), UNSUP),
     (dict(zt=gb.INT8), UNSUP), (dict(N=1 << 21), UNSUP), (dict(K=1 << 21), UNSUP), (dict(dy=None), BAD), (dict(x=None), BAD),
     (dict(w=None), BAD), (dict(z=None), BAD), (dict(dx=17), BAD), (dict(dw=17), BAD), (dict(db=17), BAD), (dict(x=17), BAD),
     (dict(z=17), BAD), (dict(dx=None, dw=None, db=None), gb.OK), (dict(M=0, dw=None, db=None, dy=None), gb.OK),
@@ -191,7 +192,7 @@ def test_workspace_sizes():
     for f in (lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward_workspace):
         assert f(1000, 2050, None) == BAD
         assert f(-1, 8, ctypes.byref(n)) == BAD and n.value == 0
-        assert f(2, 2 ** 31 - 1, ctypes.byref(n)) == UNSUP
+        assert f(2, 2 ** 31 - 1, ctypes.byref(n)) == UNSUP and f(2, (1 << 26) + 1, ctypes.byref(n)) == UNSUP
         assert f(0, 4096, ctypes.byref(n)) == gb.OK and n.value == 0
         for rows, d in ((1, 1), (1000, 2050), (512, 8192), (512, 8193), (512, 4096), (513, 4096), (256, 8), (257, 8), (100000, 64), (1 << 31, 8), (3, 100000), (8192, 4096)):
             assert f(rows, d, ctypes.byref(n)) == gb.OK

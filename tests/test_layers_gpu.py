@@ -510,6 +510,10 @@ def test_linear_every_term(gpu):
         check_epilogue(gpu, 9, 141, 96, "f16", outd, act, bias="bf16", res="f32", pre=True, scales=True, seed=2)
     for outd in DT:
         check_epilogue(gpu, 300, 260, 64, "bf16", outd, "none", seed=3)
+    # no terms at all, where the plain product and the one with an epilogue are planned alike and where they are not
+    for M, N, K in ((1, 64, 64), (16, 512, 8200), (64, 300, 8192), (512, 1024, 32768), (1024, 1024, 16384), (1213, 91, 4279),
+                    (100, 64, 4096), (4352, 4096, 64)):
+        check_epilogue(gpu, M, N, K, "bf16", "bf16", "none", seed=4)
 
 
 def test_linear_empty_sums_and_no_rows(gpu):
