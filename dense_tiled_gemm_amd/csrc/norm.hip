@@ -45,6 +45,32 @@ __device__ __forceinline__ float row_join(float v, float* part) {
     return v;
 }
 
+// ---- rows in chunks of 8 ---------------------------------------------------------
+
+// Elements i .. i+7 of a row of d that starts at element `base` of p.  RAGGED
+// (d >= 8, no multiple of 8): the last chunk is loaded from element d - 8 on and
+// moved into place when it is decoded.  A load is then one instruction for
+// every lane, and nothing waits for it before its use, where a branch that put
+// single elements together waits for everything in flight.  Rows of whole
+// chunks have kernels without the moves.
+template <bool RAGGED>
+__device__ __forceinline__ Raw8 load_chunk(const void* p, int t, long long base, int i, int d, bool nt = false) {
+    if constexpr (RAGGED) return load_raw8(p, t, (size_t)(base + min(i, d - 8)), 8, nt);
+    return load_raw8(p, t, (size_t)base + i, min(8, d - i), nt);
+}
+template <bool RAGGED>
+__device__ __forceinline__ void decode_chunk(const Raw8& r, int t, int i, int d, float (&v)[8]) {
+    decode8(r, t, v);
+    if constexpr (RAGGED) {
+        const int k = i + 8 - d;  // v holds k elements before the chunk's first
+        if (k > 0)
+#pragma unroll
+            for (int b = 4; b > 0; b >>= 1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = k & b ? (e + b < 8 ? v[e + b] : 0.0f) : v[e];
+    }
+}
+
 // ---- 8-bit codes ---------------------------------------------------------------
 
 typedef u32x2 u32x2_byte __attribute__((aligned(1)));
@@ -151,7 +177,7 @@ __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t =
 // The T threads that hold a row, U chunks of 8 elements each (T * U * 8 >= d),
 // are a wave (WAVE; a workgroup is up to 4 of them, each with rows of its own) or
 // the whole workgroup, of as many waves as the row fills.
-template <int XT, int WT, int U, bool WAVE>
+template <int XT, int WT, int U, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs a) {
     __shared__ float part[8][16];
     const int T = WAVE ? 64 : blockDim.x, RB = WAVE ? blockDim.x >> 6 : 1;
@@ -165,10 +191,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                const int n = min(8, d - i);
-                xr[u] = load_raw8(a.x, XT, (size_t)(row * a.ldx) + i, n);
-                if (a.residual) rr[u] = load_raw8(a.residual, XT, (size_t)(row * a.ldr) + i, n);
-                if (a.weight) wr[u] = load_raw8(a.weight, WT, (size_t)i, n);
+                xr[u] = load_chunk<RAGGED>(a.x, XT, row * a.ldx, i, d);
+                if (a.residual) rr[u] = load_chunk<RAGGED>(a.residual, XT, row * a.ldr, i, d);
+                if (a.weight) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
             }
         });
         float h[U][8], ss = 0.0f;
@@ -176,10 +201,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                decode8(xr[u], XT, h[u]);
+                decode_chunk<RAGGED>(xr[u], XT, i, d, h[u]);
                 if (a.residual) {
                     float v[8];
-                    decode8(rr[u], XT, v);
+                    decode_chunk<RAGGED>(rr[u], XT, i, d, v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] += v[e];
                 }
@@ -211,7 +236,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             if (i < d) {
                 if (a.weight) {
                     float w[8];
-                    decode8(wr[u], WT, w);
+                    decode_chunk<RAGGED>(wr[u], WT, i, d, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * factor * w[e];
                 }
@@ -349,7 +374,7 @@ struct NormBackArgs {
 // workgroup leaves one row of partial sums.  AHEAD: the next row is fetched
 // while this one is worked on, and the weight stays in registers; without it
 // (rows that fill the registers) both are read when they are needed.
-template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST>
+template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST, bool RAGGED>
 __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
     constexpr int RB = WAVE ? MOST / 64 : 1;
     __shared__ float part[2][16];
@@ -363,7 +388,7 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
-            if (i < d) wr[u] = load_raw8(a.weight, WT, (size_t)i, min(8, d - i));
+            if (i < d) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
         });
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -381,10 +406,9 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                const int n = min(8, d - i);
-                r.dy[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n, a.nt);
-                r.h[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n, a.nt);
-                if (AHEAD && a.dh) r.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n, a.nt);
+                r.dy[u] = load_chunk<RAGGED>(a.dy, XT, row * a.ld_dy, i, d, a.nt);
+                r.h[u] = load_chunk<RAGGED>(a.h, XT, row * a.ldh, i, d, a.nt);
+                if (AHEAD && a.dh) r.dh[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d, a.nt);
             }
         });
     };
@@ -405,10 +429,10 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 float w[8];
-                if constexpr (!AHEAD) wr[u] = load_raw8(a.weight, WT, (size_t)i, min(8, d - i));
-                decode8(now.h[u], XT, xhat[u]);
-                decode8(now.dy[u], XT, g[u]);
-                decode8(wr[u], WT, w);
+                if constexpr (!AHEAD) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
+                decode_chunk<RAGGED>(now.h[u], XT, i, d, xhat[u]);
+                decode_chunk<RAGGED>(now.dy[u], XT, i, d, g[u]);
+                decode_chunk<RAGGED>(wr[u], WT, i, d, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     xhat[u][e] *= now.rstd;
@@ -428,8 +452,8 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
                 for (int e = 0; e < 8; ++e) o[e] = now.rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
                 if (a.dh) {
                     float v[8];
-                    if constexpr (!AHEAD) now.dh[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, min(8, d - i));
-                    decode8(now.dh[u], XT, v);
+                    if constexpr (!AHEAD) now.dh[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d);
+                    decode_chunk<RAGGED>(now.dh[u], XT, i, d, v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] += v[e];
                 }
@@ -477,7 +501,7 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
 // Few rows: the first a.rows workgroups (WAVE: a wave each) make dx, one row
 // each; the others make dw itself, 64 columns each over all rows, from dy and
 // h as the caches hold them.  One launch, no partial sums.
-template <int XT, int WT, int U, bool WAVE>
+template <int XT, int WT, int U, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs a, int row_blocks, void* dweight) {
     __shared__ float part[16];
     __shared__ float joined[128][65];
@@ -493,21 +517,21 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                const int n = min(8, d - i);
-                dyr[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + i, n);
-                hr[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + i, n);
-                wr[u] = load_raw8(a.weight, WT, (size_t)i, n);
-                if (a.dh) dhr[u] = load_raw8(a.dh, XT, (size_t)(row * a.ld_dh) + i, n);
+                dyr[u] = load_chunk<RAGGED>(a.dy, XT, row * a.ld_dy, i, d);
+                hr[u] = load_chunk<RAGGED>(a.h, XT, row * a.ldh, i, d);
+                wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
+                if (a.dh) dhr[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d);
             }
         });
         float xhat[U][8], g[U][8], c = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
-            if ((u * T + renew(t)) * 8 < d) {
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
                 float w[8];
-                decode8(wr[u], WT, w);
-                decode8(hr[u], XT, xhat[u]);
-                decode8(dyr[u], XT, g[u]);
+                decode_chunk<RAGGED>(wr[u], WT, i, d, w);
+                decode_chunk<RAGGED>(hr[u], XT, i, d, xhat[u]);
+                decode_chunk<RAGGED>(dyr[u], XT, i, d, g[u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     xhat[u][e] *= rstd;
@@ -526,7 +550,7 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
                 for (int e = 0; e < 8; ++e) o[e] = rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
                 if (a.dh) {
                     float v[8];
-                    decode8(dhr[u], XT, v);
+                    decode_chunk<RAGGED>(dhr[u], XT, i, d, v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] += v[e];
                 }
@@ -542,7 +566,6 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
     if (j < d) {
-        const int n = min(8, d - j);
         for (int r = k; r < a.rows; r += 4 * G) {
             Raw8 dyr[4], hr[4];
             float rs[4];
@@ -551,16 +574,16 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
                 const long long row = r + u * G;
                 if (row < a.rows) {
                     rs[u] = a.rstd[row];
-                    dyr[u] = load_raw8(a.dy, XT, (size_t)(row * a.ld_dy) + j, n);
-                    hr[u] = load_raw8(a.h, XT, (size_t)(row * a.ldh) + j, n);
+                    dyr[u] = load_chunk<RAGGED>(a.dy, XT, row * a.ld_dy, j, d);
+                    hr[u] = load_chunk<RAGGED>(a.h, XT, row * a.ldh, j, d);
                 }
             });
             static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
                 constexpr int u = decltype(uc)::value;
                 if (r + u * G < a.rows) {
                     float y[8], h[8];
-                    decode8(dyr[u], XT, y);
-                    decode8(hr[u], XT, h);
+                    decode_chunk<RAGGED>(dyr[u], XT, j, d, y);
+                    decode_chunk<RAGGED>(hr[u], XT, j, d, h);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(y[e], h[e] * rs[u], sum[e]);
                 }
@@ -619,27 +642,26 @@ __global__ __launch_bounds__(512) void fold_kernel(const FoldArgs a) {
 // Bound by HBM: 4096 x 4096 bf16 22 us (4.6 TB/s), 8192 x 8192 77 (5.2).
 // dz = dy act'(z), and the sums of dz over a block of rows.  L lanes hold 8
 // columns each; a workgroup's 256 / L groups of lanes take its rows in turn.
-template <int L>
+template <int L, bool RAGGED>
 __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
     constexpr int G = 256 / L;
     __shared__ float joined[G][L * 8];
     const int l = threadIdx.x % L, g = threadIdx.x / L;
     const int j = (blockIdx.x * L + l) * 8;
-    const int n = min(8, a.n - j);
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
     const long long first = (long long)blockIdx.y * a.rows_per_block;
     const long long last = min(a.rows, first + a.rows_per_block);
-    if (n > 0)
+    if (j < a.n)
         with_act(a.preact ? a.act : GEMM_BT_ACT_NONE, [&](auto act) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
             auto one = [&](const Raw8& dyr, const Raw8& zr, long long row) __attribute__((always_inline)) {
                 float v[8];
-                decode8(dyr, a.type, v);
+                decode_chunk<RAGGED>(dyr, a.type, j, a.n, v);
                 if constexpr (ACT != GEMM_BT_ACT_NONE) {
                     float z[8];
-                    decode8(zr, a.preact_type, z);
+                    decode_chunk<RAGGED>(zr, a.preact_type, j, a.n, z);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= act_slope<ACT>(z[e]);
                 }
@@ -648,8 +670,8 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
                 for (int e = 0; e < 8; ++e) sum[e] += v[e];
             };
             auto load = [&](long long row, Raw8& dyr, Raw8& zr) __attribute__((always_inline)) {
-                dyr = load_raw8(a.dy, a.type, (size_t)(row * a.n) + j, n, a.nt);
-                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_raw8(a.preact, a.preact_type, (size_t)(row * a.n) + j, n, a.nt);
+                dyr = load_chunk<RAGGED>(a.dy, a.type, row * a.n, j, a.n, a.nt);
+                if constexpr (ACT != GEMM_BT_ACT_NONE) zr = load_chunk<RAGGED>(a.preact, a.preact_type, row * a.n, j, a.n, a.nt);
             };
             // four rows in flight: each is fetched again as soon as it is used
             Raw8 dyr[4], zr[4];
@@ -699,57 +721,68 @@ struct RowPlan {
 // Whole waves that hold `chunks` groups of 8 elements, U of them per thread.
 static int threads_for(int64_t chunks, int U) { return (int)((chunks + 64 * U - 1) / (64 * U) * 64); }
 
-template <int XT, int WT>
+template <int XT, int WT, bool R>
 static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
     const int64_t chunks = (d + 7) / 8;
     // Few rows (at most two per CU): one chunk per thread, so that one load's
     // latency is all that is waited for.
     const bool few = rows <= 2 * num_cu;
     if (chunks <= 64)
-        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true>, 64, 1}
-                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true>, 256, 4};
-    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true>, 256, 4};
+        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R>, 64, 1}
+                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R>, 256, 4};
+    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true, R>, 256, 4};
     if (chunks <= 256 || (few && chunks <= 1024))
-        return {(const void*)&norm_kernel<XT, WT, 1, false>, threads_for(chunks, 1), 1};
-    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false>, threads_for(chunks, 2), 1};
+        return {(const void*)&norm_kernel<XT, WT, 1, false, R>, threads_for(chunks, 1), 1};
+    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false, R>, threads_for(chunks, 2), 1};
     return {(const void*)&norm_long_kernel<XT, WT>, 1024, 1};
 }
 
-template <int XT, int WT>
+template <int XT, int WT, bool R>
 static RowPlan norm_back_plan(int64_t d) {
     const int64_t chunks = (d + 7) / 8;
-    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 1, true, true, 256>, 256, 4};
-    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 2, true, true, 256>, 256, 4};
-    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 1, false, true, 256>, threads_for(chunks, 1), 1};
-    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 2, false, true, 512>, threads_for(chunks, 2), 1};
-    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 2, false, false, 1024>, threads_for(chunks, 2), 1};
+    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 1, true, true, 256, R>, 256, 4};
+    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 2, true, true, 256, R>, 256, 4};
+    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 1, false, true, 256, R>, threads_for(chunks, 1), 1};
+    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 2, false, true, 512, R>, threads_for(chunks, 2), 1};
+    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 2, false, false, 1024, R>, threads_for(chunks, 2), 1};
     return {(const void*)&norm_back_long_kernel<XT, WT>, 1024, 1};
 }
 
-// f<x_type, w_type>() for the weight types there are kernels for: x's own and fp32.
+// Rows that end inside a chunk of 8 (those below 8 have no chunk to load from).
+// Kernels of their own for them, against one kernel that puts the last chunk
+// together element by element (us, bf16): norm 32768 x 511 57 -> 29 (512: 22),
+// backward 139 -> 37 (28), 16384 x 1023 77 -> 33 (29), 8191 x 4097 114 -> 80
+// (54), activation backward 16384 x 1023 61 -> 31 (25).  With the moves in the
+// kernels for whole chunks too, those lost: 32768 x 512 backward 28 -> 47.
+static bool ragged(int64_t d) { return d >= 8 && d % 8 != 0; }
+
 static bool weight_type_ok(int x_type, int w_type) { return w_type == x_type || w_type == GEMM_BT_F32; }
+// f(x_type, w_type, ragged) for the weight types there are kernels for (x's own
+// and fp32) and rows of d elements.
 template <class F>
-static RowPlan with_types(int x_type, int w_type, F&& f) {
+static RowPlan with_types(int x_type, int w_type, int64_t d, F&& f) {
+    auto g = [&](auto x, auto w) { return ragged(d) ? f(x, w, std::true_type{}) : f(x, w, std::false_type{}); };
     typedef std::integral_constant<int, GEMM_BT_F32> F32;
     typedef std::integral_constant<int, GEMM_BT_F16> F16;
     typedef std::integral_constant<int, GEMM_BT_BF16> BF16;
-    if (x_type == GEMM_BT_F32) return f(F32{}, F32{});
-    if (x_type == GEMM_BT_F16) return w_type == GEMM_BT_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
-    return w_type == GEMM_BT_F32 ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
+    if (x_type == GEMM_BT_F32) return g(F32{}, F32{});
+    if (x_type == GEMM_BT_F16) return w_type == GEMM_BT_F32 ? g(F16{}, F32{}) : g(F16{}, F16{});
+    return w_type == GEMM_BT_F32 ? g(BF16{}, F32{}) : g(BF16{}, BF16{});
 }
 
 static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
     int num_cu = 0;
     const int st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
-    const RowPlan p = with_types(x_type, w_type, [&](auto x, auto w) { return norm_plan<x(), w()>(a.rows, a.d, num_cu); });
+    const RowPlan p = with_types(
+        x_type, w_type, a.d, [&](auto x, auto w, auto r) { return norm_plan<x(), w(), r()>(a.rows, a.d, num_cu); });
     const int64_t grid = std::min<int64_t>((a.rows + p.rows_per_block - 1) / p.rows_per_block, 1 << 20);
     void* args[] = {&a};
     return launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
 }
 
 static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
-    return with_types(x_type, w_type, [&](auto x, auto w) { return norm_back_plan<x(), w()>(d); });
+    return with_types(x_type, w_type, d, [&](auto x, auto w, auto r) { return norm_back_plan<x(), w(), r()>(d); });
 }
 // The kernel for few rows, or none: while dy and h stay in the caches, reading
 // them twice costs less than a second launch and its partial sums, as long as
@@ -758,7 +791,7 @@ static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
 // 8192 17.5 vs 13.7; with 16 rows to a group 1000 x 2050 fp32 16.0 vs 19.6, with
 // 32 1000 x 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
 // last step halves their groups.
-template <int XT, int WT>
+template <int XT, int WT, bool R>
 static RowPlan norm_back_few(int64_t rows, int64_t d) {
     const int64_t chunks = (d + 7) / 8;
     auto pow2 = [](int64_t n) {
@@ -768,9 +801,9 @@ static RowPlan norm_back_few(int64_t rows, int64_t d) {
     };
     if (chunks > 2048 || rows * d > (4 << 20)) return {nullptr, 0, 0};
     RowPlan p;
-    if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true>, 256, 4};
-    else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false>, pow2(chunks), 1};
-    else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false>, 1024, 1};
+    if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true, R>, 256, 4};
+    else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false, R>, pow2(chunks), 1};
+    else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false, R>, 1024, 1};
     if (rows > p.threads) return {nullptr, 0, 0};
     return p;
 }
@@ -795,16 +828,23 @@ struct ActBackPlan {
 static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu) {
     ActBackPlan p;
     int lanes = 64;
-    if (n <= 64) { lanes = 8; p.fn = (const void*)&act_back_kernel<8>; }
-    else if (n <= 128) { lanes = 16; p.fn = (const void*)&act_back_kernel<16>; }
-    else if (n <= 256) { lanes = 32; p.fn = (const void*)&act_back_kernel<32>; }
-    else p.fn = (const void*)&act_back_kernel<64>;
+    const bool r = ragged(n);
+    auto kernel = [&](auto l) {
+        lanes = l();
+        p.fn = r ? (const void*)&act_back_kernel<l(), true> : (const void*)&act_back_kernel<l(), false>;
+    };
+    if (n <= 64) kernel(std::integral_constant<int, 8>{});
+    else if (n <= 128) kernel(std::integral_constant<int, 16>{});
+    else if (n <= 256) kernel(std::integral_constant<int, 32>{});
+    else kernel(std::integral_constant<int, 64>{});
     const int groups = 256 / lanes;  // rows a workgroup takes at a time
     p.strips = (n + lanes * 8 - 1) / (lanes * 8);
-    // about four workgroups per CU, each with whole rounds of its groups (4096 x
-    // 4096 bf16, gelu_tanh, us: two per CU 34.1, four 26.3, eight 28.5, which
-    // also leave twice the partial sums)
-    const int64_t want = std::max<int64_t>(1, 4 * num_cu / p.strips);
+    // as many workgroups as run at once, four per CU, each with whole rounds of its
+    // groups (4096 x 4096 bf16, gelu_tanh, us: two per CU 34.1, four 26.3, eight
+    // 28.5, which also leave twice the partial sums); the kernels for ragged rows
+    // take 150 registers and run three (8191 x 4097: three 60.2, four 75.6; 16384 x
+    // 1023: 30.7, 35.6)
+    const int64_t want = std::max<int64_t>(1, (r ? 3 : 4) * num_cu / p.strips);
     int64_t per = (rows + want - 1) / want;
     per = std::max<int64_t>(groups, (per + groups - 1) / groups * groups);
     p.blocks = (rows + per - 1) / per;
@@ -872,8 +912,8 @@ int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) 
     *bytes = 0;
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
     if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
-    // (the plans do not depend on the types)
-    if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16>(rows, d).fn) return GEMM_BT_OK;
+    // (the plans' grids do not depend on the types, nor on whole chunks)
+    if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16, false>(rows, d).fn) return GEMM_BT_OK;
     *bytes = (size_t)(norm_back_grid(norm_back_plan_of(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * 4);
     return GEMM_BT_OK;
 }
@@ -898,7 +938,8 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
     if (st != GEMM_BT_OK) return st;
     int64_t grid = 0;
     if (rows > 0) {
-        const RowPlan few = with_types(x_dtype, w_dtype, [&](auto x, auto w) { return norm_back_few<x(), w()>(rows, d); });
+        const RowPlan few = with_types(
+            x_dtype, w_dtype, d, [&](auto x, auto w, auto r) { return norm_back_few<x(), w(), r()>(rows, d); });
         if (few.fn) {
             NormBackArgs a = {dy, h, weight, rstd, dh, dx, nullptr, rows, ld_dy, ldh, ld_dh, (int)d, 0};
             int row_blocks = (int)((rows + few.rows_per_block - 1) / few.rows_per_block);

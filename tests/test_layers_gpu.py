@@ -294,6 +294,71 @@ def test_norm_backward_many_rows(gpu, rows, d):
         close(got[1], dw, tol_dw, ("dw", rows, d, dt))
 
 
+@pytest.mark.parametrize("rows,d", [(1300, 505), (1300, 506), (1100, 1021), (600, 2042), (530, 4099), (520, 8188), (513, 9999),
+                                    (3, 13), (70, 1022), (9, 9007)])
+def test_ragged_rows(gpu, rows, d):
+    """Rows that end inside a chunk, wider apart than they are long and with NaN between them, dx in place of dh."""
+    import ctypes
+
+    lib, need = gpu.load(), ctypes.c_size_t()
+    codes = {torch.float32: gpu.F32, torch.float16: gpu.F16, torch.bfloat16: gpu.BF16}
+    for dt, wt in (("bf16", "own"), ("f16", "f32"), ("f32", "own")):
+        say("ragged rows", rows, d, dt, wt)
+        wide = [torch.full((rows, d + 3 + i), math.nan, dtype=DT[dt]) for i in range(4)]
+        x, r, dy, dh = (w[:, 1 + i % 3:1 + i % 3 + d] for i, w in enumerate(wide))
+        for i, (t, std) in enumerate(((x, 2.0), (r, 1.0), (dy, 0.1), (dh, 0.1))):
+            t.copy_(randn(d + i, rows, d, std=std, dtype=DT[dt]))
+        w = (1 + randn(d + 4, d, std=0.3)).to(DT[dt] if wt == "own" else torch.float32)
+        gx, gr, gdy, gdh = (wide[i].cuda()[:, 1 + i % 3:1 + i % 3 + d] for i in range(4))
+        got = gpu.add_rms_norm(gx, w.cuda(), residual=gr, eps=1e-5, save_rstd=True)
+        h64, rstd64, y64 = norm64(x, r, w, 1e-5)
+        close(got.h, h64, 2 * u * h64.abs(), "h")
+        close(got.rstd, rstd64[:, 0], y_rel(d) * rstd64[:, 0], "rstd")
+        close(got.y, y64, y_rel(d) * y64.abs(), "y")
+        q = gpu.quantize_rows(gx, torch.int8)
+        check_codes(q[0], q[1], x.double(), "i8", y_rel(d), (rows, d, dt))
+        h, rstd = got.h.cpu(), got.rstd.cpu()
+        dx, dw = gpu.add_rms_norm_backward(gdy, got.h, w.cuda(), got.rstd, dh=gdh)
+        want, tol_dx, want_dw, tol_dw = norm_back64(dy, h, w, rstd, dh)
+        close(dx, want, tol_dx, ("dx", rows, d, dt))
+        close(dw, want_dw, tol_dw, ("dw", rows, d, dt))
+        there, gw, again = gdh.contiguous(), w.cuda(), torch.empty(d, dtype=w.dtype, device="cuda")
+        assert lib.gemm_bt_rms_norm_backward_workspace(rows, d, ctypes.byref(need)) == gpu.OK
+        ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        assert lib.gemm_bt_rms_norm_backward(gdy.data_ptr(), gdy.stride(0), got.h.data_ptr(), d, gw.data_ptr(), got.rstd.data_ptr(),
+                                             there.data_ptr(), d, there.data_ptr(), again.data_ptr(), rows, d, codes[DT[dt]],
+                                             codes[w.dtype], ws.data_ptr(), need.value,
+                                             torch.cuda.current_stream().cuda_stream) == gpu.OK
+        assert torch.equal(there, dx) and torch.equal(again, dw)
+
+
+@pytest.mark.parametrize("rows,n", [(5000, 60), (3000, 121), (2500, 250), (2100, 1022), (1700, 2051), (1100, 4097)])
+def test_act_backward_ragged_many_rows(gpu, rows, n):
+    """More rows than the lanes of a launch, so that each lane goes on through its rows."""
+    import ctypes
+
+    lib = gpu.load()
+    for code, dt in ((gpu.BF16, "bf16"), (gpu.F32, "f32")):
+        say("act backward ragged", rows, n, dt)
+        dy, z = randn(n, rows, n, dtype=DT[dt]), randn(n + 1, rows, n, std=2.5, dtype=DT[dt])
+        need = ctypes.c_size_t()
+        assert lib.gemm_bt_act_backward_workspace(rows, n, ctypes.byref(need)) == gpu.OK
+        ws, ws_ok = guarded((need.value,), torch.uint8)
+        dz, dz_ok = guarded((rows, n), DT[dt], offset=n % 3)
+        db, db_ok = guarded((n,), torch.float32)
+        gdy, gz = dy.cuda(), z.cuda()
+        assert lib.gemm_bt_act_backward(gdy.data_ptr(), gz.data_ptr(), dz.data_ptr(), db.data_ptr(), rows, n, ACTS.index("silu"),
+                                        code, code, gpu.F32, ws.data_ptr(), need.value,
+                                        torch.cuda.current_stream().cuda_stream) == gpu.OK
+        for ok in (ws_ok, dz_ok, db_ok):
+            ok()
+        z64, dy64 = z.double(), dy.double()
+        slope = slope64(z64, "silu")
+        tol = dy64.abs() * 2.0 ** -20 * (1 + z64.abs() ** 3) + u * (dy64 * slope).abs()
+        close(dz, dy64 * slope, tol, ("dz", rows, n, dt))
+        close(db, (dy64 * slope).sum(0), tol.sum(0) + (rows + 4) * u * (dy64 * slope).abs().sum(0), ("db", rows, n, dt))
+
+
 def test_norm_gradient_against_differences(gpu):
     """dx, dresidual and dw of L = sum(y * dy) + sum(h * dh) against central differences of the 64-bit forward pass."""
     rows, d = 3, 37
