@@ -360,9 +360,8 @@ struct NormBackArgs {
     long long rows, ld_dy, ldh, ld_dh;
     int d;
     // rows of whole 16-byte chunks: dy, h and dh are read past the caches (8192
-    // x 8192 bf16 100.3 -> 93.6 us).  Rows that are not share lines between
-    // neighbouring lanes, which would then be fetched twice (1110 x 1317 18.6 us
-    // against 9.6 at 1320).
+    // x 8192 bf16 100.3 -> 93.6 us).  Elsewhere neighbouring chunks share lines, and
+    // it makes no difference (8191 x 4097 80.5 against 80.9).
     int nt;
 };
 
@@ -788,8 +787,8 @@ static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
 // them twice costs less than a second launch and its partial sums, as long as
 // each group of lanes has at most 8 rows to sum (us, bf16, two launches vs
 // one: 1 x 4096 5.4 vs 3.2, 128 x 8192 10.4 vs 5.3, 512 x 4096 15.3 vs 8.8, 512 x
-// 8192 17.5 vs 13.7; with 16 rows to a group 1000 x 2050 fp32 16.0 vs 19.6, with
-// 32 1000 x 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
+// 8192 17.5 vs 13.7; with 16 rows to a group 1000 x 2050 fp32 13.1 vs 14.3, 400 x
+// 1023 bf16 7.0 vs 9.2, with 32 1000 x 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
 // last step halves their groups.
 template <int XT, int WT, bool R>
 static RowPlan norm_back_few(int64_t rows, int64_t d) {
