@@ -811,9 +811,13 @@ static RowPlan norm_back_few(int64_t rows, int64_t d) {
 // sums: about 512 threads per CU (all of them resident), and the same number
 // of rows for all but the last ones.  (8192 x 4096 bf16, us: 512 threads per CU 53.6, 768 59.0,
 // 1024 63.6; 16384 x 1024 28.3, 29.6, 32.6: more workgroups do not read faster,
-// and each leaves d fp32 sums more to write and fold.)
+// and each leaves d fp32 sums more to write and fold.  Workgroups of 192, two or
+// three per CU: 16384 x 2560 72.7, 64.3, 16384 x 1536 46.4, 41.5, 4000 x 2056 21.2,
+// 20.1, 8192 x 3000 42.2, 43.5; of 320, one or two: 8192 x 5120 65.5, 69.4, 8191 x
+// 4104 59.4, 61.5, 8191 x 4097 80.3, 72.6.)
 static int64_t norm_back_grid(const RowPlan& p, int64_t rows, int num_cu) {
-    const int64_t most = (int64_t)num_cu * std::max(1, 512 / p.threads) * p.rows_per_block;
+    const int per_cu = p.threads <= 256 ? (512 + p.threads / 2) / p.threads : 1;
+    const int64_t most = (int64_t)num_cu * per_cu * p.rows_per_block;
     const int64_t per = (rows + most - 1) / most * p.rows_per_block;  // rows of a workgroup
     return per > 0 ? (rows + per - 1) / per : 0;
 }

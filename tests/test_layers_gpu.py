@@ -295,7 +295,7 @@ def test_norm_backward_many_rows(gpu, rows, d):
 
 
 @pytest.mark.parametrize("rows,d", [(1300, 505), (1300, 506), (1100, 1021), (600, 2042), (530, 4099), (520, 8188), (513, 9999),
-                                    (3, 13), (70, 1022), (9, 9007)])
+                                    (3, 13), (70, 1022), (9, 9007), (1900, 1321), (2000, 2050)])
 def test_ragged_rows(gpu, rows, d):
     """Rows that end inside a chunk, wider apart than they are long and with NaN between them, dx in place of dh."""
     import ctypes
