@@ -347,6 +347,16 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
     }
 }
 
+// Rows of no elements: their squares' mean is 0, and so is their largest
+// magnitude.
+__global__ __launch_bounds__(256) void empty_rows_kernel(float* scale, float* rstd, long long rows, float eps) {
+    const long long step = (long long)gridDim.x * 256;
+    for (long long row = (long long)blockIdx.x * 256 + threadIdx.x; row < rows; row += step) {
+        if (scale) scale[row] = 0x1p-100f;
+        if (rstd) rstd[row] = 1.0f / __builtin_sqrtf(eps);
+    }
+}
+
 // ---- norm, backward --------------------------------------------------------------
 
 struct NormBackArgs {
@@ -780,6 +790,18 @@ static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
     return launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
 }
 
+// Rows of no elements leave their scales and rstd, where there are any.
+static int empty_rows(float* scale, float* rstd, long long rows, float eps, void* stream) {
+    if (!aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!scale && !rstd) return GEMM_BT_OK;
+    int num_cu = 0;
+    const int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    void* args[] = {&scale, &rstd, &rows, &eps};
+    return launch((const void*)&empty_rows_kernel, dim3((unsigned)std::min<int64_t>((rows + 255) / 256, 8 * num_cu)), 256, args,
+                  stream);
+}
+
 static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
     return with_types(x_type, w_type, d, [&](auto x, auto w, auto r) { return norm_back_plan<x(), w(), r()>(d); });
 }
@@ -888,8 +910,10 @@ int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t l
     const bool codes = y_dtype == GEMM_BT_FP8_E4M3 || y_dtype == GEMM_BT_INT8;
     if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype) || !(codes || float_type(y_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
     if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (rows == 0 || d == 0) return GEMM_BT_OK;
-    if (!x || !weight || !y || (codes && !scale)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (rows == 0) return GEMM_BT_OK;
+    if (codes && !scale) return GEMM_BT_ERR_INVALID_VALUE;
+    if (d == 0) return empty_rows(codes ? scale : nullptr, rstd, rows, eps, stream);
+    if (!x || !weight || !y) return GEMM_BT_ERR_INVALID_VALUE;
     if (!stride_ok(ldx, d) || (residual && !stride_ok(ldr, d))) return GEMM_BT_ERR_INVALID_VALUE;
     if (!aligned(x, x_dtype) || !aligned(residual, x_dtype) || !aligned(h, x_dtype) || !aligned(weight, w_dtype) ||
         (!codes && !aligned(y, y_dtype)) || !aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32))
@@ -903,8 +927,10 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
     if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
     if (!float_type(x_dtype) || (q_dtype != GEMM_BT_FP8_E4M3 && q_dtype != GEMM_BT_INT8)) return GEMM_BT_ERR_UNSUPPORTED;
     if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (rows == 0 || d == 0) return GEMM_BT_OK;
-    if (!x || !q || !scale || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (rows == 0) return GEMM_BT_OK;
+    if (!scale) return GEMM_BT_ERR_INVALID_VALUE;
+    if (d == 0) return empty_rows(scale, nullptr, rows, 0.0f, stream);
+    if (!x || !q || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
     if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
     NormArgs a = {x, nullptr, nullptr, q, nullptr, scale, nullptr, rows, ldx, 0, (int)d, 0.0f, q_dtype};
     return launch_norm(a, x_dtype, x_dtype, stream);

@@ -70,7 +70,7 @@ def _rows(t, what):
     if not shape:
         raise ValueError("%s needs at least one dimension" % what)
     d = shape[-1]
-    rows = t.numel() // d if d else 0
+    rows = t.numel() // d if d else shape[:-1].numel()
     if t.is_contiguous():
         return t, d, rows, d
     if len(shape) == 2 and t.stride(1) == 1 and t.stride(0) >= d:

@@ -284,6 +284,8 @@ int gemm_bt_epi_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, in
  *          residual itself where that one's rows are dense; y may not
  *   scale  rows fp32 (8-bit y; else not used)
  *   rstd   rows fp32, or NULL: receives 1 / sqrt(...) for the backward pass
+ * A row of no elements (d == 0) has mean 0 and amax 0: rstd = 1 / sqrt(eps),
+ * scale = 2^-100.
  *   eps    >= 0 (else INVALID_VALUE)
  */
 int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* y,

@@ -1,0 +1,73 @@
+"""The row operators and the product with an epilogue at the edges of what they take: sizes of zero, operands in each
+other's place, large extents, tails of the activations.  Tolerances stand beside the checks."""
+import ctypes
+import itertools
+import math
+
+import pytest
+
+import dense_tiled_gemm_amd as gb
+
+torch = pytest.importorskip("torch")
+
+BAD, UNSUP = gb.ERR_INVALID_VALUE, gb.ERR_UNSUPPORTED
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+u = 2.0 ** -24
+
+
+def say(*a):
+    print("[case]", *a, flush=True)
+
+
+def randn(seed, *shape, std=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype)
+
+
+def handle():
+    return torch.cuda.current_stream().cuda_stream
+
+
+# ------------------------------------------------------------------ rows of no elements
+
+def test_rows_of_no_elements_need_a_place_for_their_scales():
+    lib = gb.load()
+    assert lib.gemm_bt_quantize_rows(None, 0, None, None, 3, 0, gb.BF16, gb.INT8, None) == BAD
+    assert lib.gemm_bt_rms_norm(None, 0, None, 0, None, None, None, None, None, 3, 0, 1e-6, gb.BF16, gb.BF16, gb.INT8,
+                                None) == BAD
+    assert lib.gemm_bt_rms_norm(None, 0, None, 0, None, None, None, None, 18, 3, 0, 1e-6, gb.BF16, gb.BF16, gb.BF16,
+                                None) == BAD
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 5, 3000])
+def test_rows_of_no_elements(gpu, rows):
+    """Their scales are the smallest there is and their rstd that of a mean of 0; a product with them is the empty sum."""
+    lib = gpu.load()
+    for eps, rstd_want in ((1e-6, 1e3), (0.25, 2.0), (0.0, float("inf"))):
+        say("empty rows", rows, eps)
+        scale, rstd = torch.full((rows + 1,), 7.0, device="cuda"), torch.full((rows + 1,), 7.0, device="cuda")
+        assert lib.gemm_bt_rms_norm(None, 0, None, 0, None, None, None, scale.data_ptr(), rstd.data_ptr(), rows, 0, eps, gpu.BF16,
+                                    gpu.BF16, gpu.INT8, handle()) == gpu.OK
+        assert bool((scale[:rows] == 2.0 ** -100).all())
+        # eps is rounded to fp32, then a root and a quotient: 3 u
+        got = rstd[:rows].double()
+        assert bool((got == rstd_want).all()) if math.isinf(rstd_want) else bool(((got - rstd_want).abs() <= 3 * u * rstd_want).all())
+        assert float(scale[rows]) == 7.0 and float(rstd[rows]) == 7.0
+        rstd.fill_(7.0)  # float rows: no scales, which are left as they are
+        scale.fill_(7.0)
+        assert lib.gemm_bt_rms_norm(None, 0, None, 0, None, None, None, scale.data_ptr(), rstd.data_ptr(), rows, 0, eps, gpu.F32,
+                                    gpu.F32, gpu.F32, handle()) == gpu.OK
+        assert bool((scale == 7.0).all()) and bool((rstd[:rows] != 7.0).all())
+    scale = torch.full((rows,), float("nan"), device="cuda")
+    assert lib.gemm_bt_quantize_rows(None, 0, None, scale.data_ptr(), rows, 0, gpu.F32, gpu.FP8_E4M3, handle()) == gpu.OK
+    assert bool((scale == 2.0 ** -100).all())
+    x, w = torch.empty(rows, 0, dtype=torch.bfloat16, device="cuda"), torch.empty(0, dtype=torch.bfloat16, device="cuda")
+    q = gpu.quantize_rows(x.view(1, rows, 0), torch.int8)
+    assert q.q.shape == (1, rows, 0) and q.scale.shape == (1, rows) and bool((q.scale == 2.0 ** -100).all())
+    n = gpu.add_rms_norm(x, w, residual=x, eps=0.25, out_dtype=torch.int8, save_rstd=True)
+    assert n.h.shape == (rows, 0) and bool((n.scale == 2.0 ** -100).all()) and bool((n.rstd == 2.0).all())
+    b = randn(1, 9).cuda()
+    y = gpu.linear(n.y, torch.empty(9, 0, dtype=torch.int8, device="cuda"), bias=b, x_scale=n.scale, out_dtype=torch.float32)
+    assert torch.equal(y, b.expand(rows, 9))
+    dx, dw = gpu.add_rms_norm_backward(x, x, w, n.rstd)
+    assert dx.shape == (rows, 0) and dw.shape == (0,)
