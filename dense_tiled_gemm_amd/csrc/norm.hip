@@ -956,7 +956,8 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
     if (d == 0) return GEMM_BT_OK;
     if (!dweight || !aligned(dweight, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
     if (rows > 0) {
-        if (!dy || !h || !weight || !rstd || !dx || dx == dy) return GEMM_BT_ERR_INVALID_VALUE;
+        // (the few-rows kernel's sums for dweight read dy and h while dx is written)
+        if (!dy || !h || !weight || !rstd || !dx || dx == dy || dx == h) return GEMM_BT_ERR_INVALID_VALUE;
         if (!stride_ok(ld_dy, d) || !stride_ok(ldh, d) || (dh && !stride_ok(ld_dh, d))) return GEMM_BT_ERR_INVALID_VALUE;
         if (!aligned(dy, x_dtype) || !aligned(h, x_dtype) || !aligned(dh, x_dtype) || !aligned(dx, x_dtype) ||
             !aligned(weight, w_dtype) || !aligned(rstd, GEMM_BT_F32) || !aligned(workspace, GEMM_BT_F32))

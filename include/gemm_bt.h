@@ -305,7 +305,7 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
  *   h, rstd    as gemm_bt_rms_norm left them (x itself where there was no residual)
  *   dh         the gradient that reaches h from elsewhere, or NULL
  *   dx         rows x d of x_dtype; may be dh itself where its rows are dense,
- *              not dy (INVALID_VALUE)
+ *              not dy or h, which dweight's sums read (INVALID_VALUE)
  *   dweight    d elements of w_dtype
  *   workspace  at least gemm_bt_rms_norm_backward_workspace bytes (0 for few
  *              rows), 4-byte aligned, any contents

@@ -71,3 +71,14 @@ def test_rows_of_no_elements(gpu, rows):
     assert torch.equal(y, b.expand(rows, 9))
     dx, dw = gpu.add_rms_norm_backward(x, x, w, n.rstd)
     assert dx.shape == (rows, 0) and dw.shape == (0,)
+
+
+# ------------------------------------------------------------------ operands in each other's place
+
+@pytest.mark.parametrize("rows,d", [(2, 8), (256, 4096), (8192, 4096), (2, 100000)])
+def test_norm_backward_not_in_place_of_h(rows, d):
+    """dweight is summed from dy and h by other workgroups than those that write dx: neither may be overwritten."""
+    f = gb.load().gemm_bt_rms_norm_backward
+    call = lambda dx, dh: f(16, d, 32, d, 16, 16, dh, d, dx, 16, rows, d, gb.BF16, gb.BF16, 16, 1 << 40, None)
+    for dh in (None, 48, 32):
+        assert call(16, dh) == BAD and call(32, dh) == BAD
