@@ -299,17 +299,32 @@ _ws_cache = {}
 def workspace_for(device, stream: int, nbytes: int):
     """A zero-initialised uint8 device tensor of at least `nbytes` for gemm_bt_ws calls on `stream`, kept per
     (device, stream) and reused: calls on one stream run in order, and each call leaves the counter area zero
-    again.  Grows (a new zeroed tensor) when a larger size is asked for."""
+    again.  Grows (a new zeroed tensor) when a larger size is asked for.  It is allocated, cleared and later freed in
+    `stream`'s own order, whichever stream is torch's current one.  Under graph capture the tensor is the graph's own and
+    not kept: its counters are cleared whenever the graph runs, not before, and the graph goes on using its address."""
     import torch
 
-    key = (torch.device(device).index, int(stream))
-    with _ws_lock:
-        ws = _ws_cache.get(key)
-        if ws is None or ws.numel() < nbytes:
-            with torch.cuda.device(device):
-                ws = torch.zeros(max(nbytes, SK_COUNTER_BYTES), dtype=torch.uint8, device=device)
-            _ws_cache[key] = ws
+    device, stream = torch.device(device), int(stream)
+    if torch.cuda.is_current_stream_capturing():
+        with _in_order_of(device, stream):
+            ws = torch.empty(max(nbytes, SK_COUNTER_BYTES), dtype=torch.uint8, device=device)
+            ws[:SK_COUNTER_BYTES].zero_()
         return ws
+    with _ws_lock:
+        ws = _ws_cache.get((device.index, stream))
+        if ws is None or ws.numel() < nbytes:
+            with _in_order_of(device, stream):
+                ws = torch.zeros(max(nbytes, SK_COUNTER_BYTES), dtype=torch.uint8, device=device)
+            _ws_cache[device.index, stream] = ws
+        return ws
+
+
+def _in_order_of(device, stream):
+    """The context in which `stream` (a handle) is torch's current stream of `device`."""
+    import torch
+
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
 
 
 def mm_bt(a, b, out_dtype=None, out=None, stream=None, split_k=True):

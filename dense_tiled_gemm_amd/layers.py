@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, SK_COUNTER_BYTES, GemmBtError, load, workspace_for
+from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, GemmBtError, load, workspace_for
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
@@ -123,16 +123,6 @@ def _on_stream(stream, like, call):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return call()
-
-
-def _split_workspace(like, stream, nbytes):
-    """The zeroed workspace of a split product: the stream's own (workspace_for), but under graph capture one of the graph's,
-    cleared whenever the graph runs, since a captured clearing does not run before then."""
-    if torch.cuda.is_current_stream_capturing():
-        ws = like.new_empty(nbytes, dtype=torch.uint8)
-        ws[:SK_COUNTER_BYTES].zero_()
-        return ws
-    return workspace_for(like.device, stream, nbytes)
 
 
 def _ptr(t):
@@ -335,7 +325,7 @@ def linear(x, weight, bias=None, activation="none", residual=None, x_scale=None,
         need = _epi_bytes(M, N, K, in_code, out_code, device.index)
         ws, ws_bytes = None, 0
         if need:
-            t = _split_workspace(x, s, need)
+            t = workspace_for(device, s, need)
             ws, ws_bytes = t.data_ptr(), t.numel()
         st = load().gemm_bt_epi(x.data_ptr(), weight.data_ptr(), y.data_ptr(), M, N, K, in_code, out_code, ctypes.byref(e), ws,
                                 ws_bytes, s)

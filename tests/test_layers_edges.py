@@ -82,3 +82,70 @@ def test_norm_backward_not_in_place_of_h(rows, d):
     call = lambda dx, dh: f(16, d, 32, d, 16, 16, dh, d, dx, 16, rows, d, gb.BF16, gb.BF16, 16, 1 << 40, None)
     for dh in (None, 48, 32):
         assert call(16, dh) == BAD and call(32, dh) == BAD
+
+
+# ------------------------------------------------------------------ the workspace of split products
+
+def split_operands(N=512, K=8192, seed=1):
+    return (randn(seed, 8, K, std=3.0, dtype=torch.bfloat16).cuda(), randn(seed + 1, N, K, std=3.0, dtype=torch.bfloat16).cuda())
+
+
+@pytest.mark.gpu
+def test_workspace_is_cleared_in_the_order_of_its_stream(gpu):
+    """A split product on an idle stream, called while torch's current stream is busy and memory holds other values."""
+    a, b = randn(3, 512, 32768, dtype=torch.bfloat16).cuda(), randn(4, 1024, 32768, dtype=torch.bfloat16).cuda()
+    assert gpu.gemm_bt_workspace_size(512, 1024, 32768, gpu.BF16, gpu.F32) > 0
+    want = gpu.mm_bt(a, b, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        say("mm_bt on another stream")
+        side = torch.cuda.Stream()
+        gpu._ws_cache.pop((a.device.index, side.cuda_stream), None)
+        out = torch.empty_like(want)
+        left = [torch.full((20 << 20,), 0x5B, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del left  # what the next tensors are made of
+        busy = torch.randn(2048, 2048, device="cuda")
+        for _ in range(20):
+            busy = busy @ busy * 0.01
+        gpu.mm_bt(a, b, out_dtype=torch.float32, out=out, stream=side.cuda_stream)
+        side.synchronize()
+        assert torch.equal(out, want)
+        torch.cuda.synchronize()
+        assert int(gpu.workspace_for(a.device, side.cuda_stream, 0)[:gpu.SK_COUNTER_BYTES].count_nonzero()) == 0
+
+
+@pytest.mark.gpu
+def test_workspace_of_a_captured_product_is_the_graphs(gpu):
+    """Split products captured before and after eager ones on the same stream: neither shares the other's counters, and a
+    larger workspace later on takes nothing from the graph."""
+    x, w = split_operands()
+    p, q = randn(5, 64, 8192, dtype=torch.bfloat16).cuda(), randn(6, 8192, 8192, dtype=torch.bfloat16).cuda()
+    small = gpu.gemm_bt_plan_epi(8, 512, 8192, gpu.BF16, gpu.BF16)
+    assert small.split_tiles > 0 and gpu.gemm_bt_workspace_size(64, 8192, 8192, gpu.BF16, gpu.BF16) > small.workspace_bytes
+    wide = randn(7, 512, 32768, dtype=torch.bfloat16).cuda(), randn(8, 1024, 32768, dtype=torch.bfloat16).cuda()
+    want, want_wide, want_q = gpu.linear(x, w), gpu.mm_bt(*wide), gpu.mm_bt(p, q)
+    torch.cuda.synchronize()
+    for first in (False, True):  # an eager product on the stream before the capture, or none
+        say("captured mm_bt and linear", first)
+        side = torch.cuda.Stream()
+        gpu._ws_cache.pop((x.device.index, side.cuda_stream), None)
+        if first:
+            with torch.cuda.stream(side):
+                gpu.linear(x, w)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got_wide, got = gpu.mm_bt(*wide), gpu.linear(x, w)
+        with torch.cuda.stream(side):
+            assert torch.equal(gpu.linear(x, w), want)  # before the graph has run
+            assert torch.equal(gpu.mm_bt(p, q), want_q)  # a larger workspace
+        for _ in range(3):
+            junk = torch.full((64 << 20,), 0x5B, dtype=torch.uint8, device="cuda")
+            got.zero_(), got_wide.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(got_wide, want_wide)
+            with torch.cuda.stream(side):
+                assert torch.equal(gpu.linear(x, w), want)
+            del junk
