@@ -320,11 +320,12 @@ def workspace_for(device, stream: int, nbytes: int):
 
 
 def _in_order_of(device, stream):
-    """The context in which `stream` (a handle) is torch's current stream of `device`."""
+    """The context in which `stream` (a handle, or torch's object) is torch's current stream of `device`."""
     import torch
 
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
-                             else torch.cuda.default_stream(device))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def mm_bt(a, b, out_dtype=None, out=None, stream=None, split_k=True):
@@ -336,8 +337,9 @@ def mm_bt(a, b, out_dtype=None, out=None, stream=None, split_k=True):
     inputs need K % 16 == 0; int8 also K <= 131071).  ``out_dtype`` defaults
     to a's dtype (bfloat16 for 8-bit float inputs, which are not an output
     format; int32, the only one allowed, for int8); ``out`` may be a preallocated
-    contiguous M×N (Z×M×N) tensor.  The call is asynchronous on ``stream``
-    (default: torch's current stream of a's device).  With ``split_k`` (the
+    contiguous M×N (Z×M×N) tensor.  The call is asynchronous on ``stream`` (a
+    handle or torch's object; default: torch's current stream of a's device),
+    the copies of strided operands and the allocation of C included.  With ``split_k`` (the
     default) a single product goes through gemm_bt_ws with a workspace kept
     per stream (``workspace_for``), so shapes whose tiles leave compute units
     idle are split along K (stream-K); ``split_k=False`` calls gemm_bt.
@@ -353,6 +355,9 @@ def mm_bt(a, b, out_dtype=None, out=None, stream=None, split_k=True):
         raise TypeError("a and b must share one dtype")
     if not a.is_cuda or not b.is_cuda or a.device != b.device:
         raise ValueError("a and b must be on the same GPU")
+    if stream is not None:
+        with _in_order_of(a.device, stream):
+            return mm_bt(a, b, out_dtype, out, split_k=split_k)
     in_code = _torch_code(a.dtype)
     default_out = BF16 if in_code in (FP8_E4M3, FP8_E5M2) else (INT32 if in_code == INT8 else in_code)
     out_code = default_out if out_dtype is None else (_torch_code(out_dtype) if not isinstance(out_dtype, int)
@@ -368,8 +373,7 @@ def mm_bt(a, b, out_dtype=None, out=None, stream=None, split_k=True):
         out = torch.empty(shape, dtype=_torch_dtype(out_code), device=a.device)
     elif tuple(out.shape) != shape or not out.is_contiguous() or out.dtype != _torch_dtype(out_code):
         raise ValueError("out must be a contiguous %s %s tensor" % ("x".join(map(str, shape)), _torch_dtype(out_code)))
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = torch.cuda.current_stream(a.device).cuda_stream
     with torch.cuda.device(a.device):
         if batched:
             st = gemm_bt_batched(a.data_ptr(), b.data_ptr(), out.data_ptr(), Z, M, N, K, sa, sb, M * N, in_code,
@@ -391,7 +395,7 @@ def mm_layout(a, b, a_layout=K_INNER, b_layout=K_INNER, out_dtype=None, out=None
     """C = op(a) @ op(b).T for 16-bit tensors: a is (M,K) for K_INNER or (K,M) for K_OUTER, b is (N,K) for
     K_INNER or (K,N) for K_OUTER.  Either may carry a leading batch dimension Z (then C is (Z,M,N)); a 2-D
     operand, or one expanded along the batch, is shared by every item.  Operands stored K-outer are
-    transposed inside the kernel."""
+    transposed inside the kernel.  ``stream`` as for mm_bt."""
     import torch
 
     if a.dim() not in (2, 3) or b.dim() not in (2, 3):
@@ -406,6 +410,9 @@ def mm_layout(a, b, a_layout=K_INNER, b_layout=K_INNER, out_dtype=None, out=None
         raise TypeError("a and b must share one dtype")
     if not a.is_cuda or not b.is_cuda or a.device != b.device:
         raise ValueError("a and b must be on the same GPU")
+    if stream is not None:
+        with _in_order_of(a.device, stream):
+            return mm_layout(a, b, a_layout, b_layout, out_dtype, out)
     in_code = _torch_code(a.dtype)
     out_code = in_code if out_dtype is None else (_torch_code(out_dtype) if not isinstance(out_dtype, int)
                                                   else out_dtype)
@@ -418,8 +425,7 @@ def mm_layout(a, b, a_layout=K_INNER, b_layout=K_INNER, out_dtype=None, out=None
         out = torch.empty(shape, dtype=_torch_dtype(out_code), device=a.device)
     elif tuple(out.shape) != shape or not out.is_contiguous() or out.dtype != _torch_dtype(out_code):
         raise ValueError("out must be a contiguous %s %s tensor" % ("x".join(map(str, shape)), _torch_dtype(out_code)))
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+    stream = torch.cuda.current_stream(a.device).cuda_stream
     with torch.cuda.device(a.device):
         st = gemm_bt_batched_layout(a.data_ptr(), b.data_ptr(), out.data_ptr(), Z, M, N, K, sa, sb, M * N, a_layout,
                                     b_layout, in_code, out_code, stream)

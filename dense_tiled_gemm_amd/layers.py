@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, GemmBtError, load, workspace_for
+from . import BF16, F16, F32, FP8_E4M3, FP8_E5M2, INT8, GemmBtError, _in_order_of, load, workspace_for
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
@@ -118,10 +118,7 @@ _stream = torch._C._cuda_getCurrentRawStream
 def _on_stream(stream, like, call):
     """call() with `stream` (a handle, or torch's object) as the current stream of like's device, so that every copy and
     every allocation of the call is in its order too."""
-    device = like.device
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with _in_order_of(like.device, stream):
         return call()
 
 

@@ -149,3 +149,27 @@ def test_workspace_of_a_captured_product_is_the_graphs(gpu):
             with torch.cuda.stream(side):
                 assert torch.equal(gpu.linear(x, w), want)
             del junk
+
+
+@pytest.mark.gpu
+def test_products_on_a_stream_copy_their_operands_there(gpu):
+    """mm_bt and mm on a stream whose operands are strided and still being written on it, while torch's current stream is idle."""
+    a0, b0 = randn(1, 96, 512, dtype=torch.bfloat16), randn(2, 256, 512, dtype=torch.bfloat16)
+    want = gpu.mm_bt(a0.cuda(), b0.cuda())
+    want2 = gpu.mm(a0.cuda(), b0.t().contiguous().cuda())
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        say("mm_bt and mm of strided operands", type(stream).__name__)
+        at, bt = torch.zeros(512, 96, dtype=torch.bfloat16, device="cuda"), torch.zeros(256, 1024, dtype=torch.bfloat16, device="cuda")
+        src_a, src_b = a0.t().contiguous().cuda(), b0.cuda()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy = torch.randn(2048, 2048, device="cuda")
+            for _ in range(20):
+                busy = busy @ busy * 0.01
+            at.copy_(src_a)
+            bt[:, ::2].copy_(src_b)
+        got = gpu.mm_bt(at.t(), bt[:, ::2], stream=stream)
+        got2 = gpu.mm(at.t(), bt[:, ::2].t(), stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(got2, want2)
