@@ -194,15 +194,19 @@ static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu)
     p.ldz = up8(N);
     p.ldk = up8(K);
     const int64_t steps_w = (M + 63) / 64, steps_x = (N + 63) / 64;
-    const int64_t most = std::max<int64_t>(1, 0x7FFFFFFFLL / (128 * std::max(p.ldz, p.ldk)));  // steps of 64 rows below 2 GiB
+    // steps of 64 rows that one run may take of its K-outer operands: 2 GiB of
+    // each (dW: dz and X; dX: W alone, dz is read row by row; with dz's limit on
+    // dX too, ms: 4096x128256x4096 8.5, without 7.2; 8192x128256x4096 18.3, 14.4)
+    auto steps_of = [](int64_t ld) { return std::max<int64_t>(1, 0x7FFFFFFFLL / (128 * std::max<int64_t>(1, ld))); };
+    const int64_t most_w = steps_of(std::max(p.ldz, p.ldk)), most_x = steps_of(p.ldk);
     double best = 0.0;
     for (const BackTile& t : kBackTiles) {
         auto tiles = [&](int64_t r, int64_t c) { return ((r + t.bm - 1) / t.bm) * ((c + t.bn - 1) / t.bn); };
         const int64_t tiles_w = tiles(N, K), tiles_x = tiles(M, K);
         const int64_t fair = (tiles_w * steps_w + tiles_x * steps_x + num_cu - 1) / num_cu;
         int pieces_w, per_w, pieces_x, per_x;
-        cut(steps_w, fair, 12, most, &pieces_w, &per_w);
-        cut(steps_x, fair, 12, most, &pieces_x, &per_x);
+        cut(steps_w, fair, 12, most_w, &pieces_w, &per_w);
+        cut(steps_x, fair, 12, most_x, &pieces_x, &per_x);
         const int64_t runs_w = tiles_w * pieces_w, runs_x = tiles_x * pieces_x;
         const int64_t span = per_w >= per_x ? makespan(runs_w, per_w + 3, runs_x, per_x + 3, num_cu)
                                             : makespan(runs_x, per_x + 3, runs_w, per_w + 3, num_cu);

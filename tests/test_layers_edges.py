@@ -173,3 +173,43 @@ def test_products_on_a_stream_copy_their_operands_there(gpu):
         got2 = gpu.mm(at.t(), bt[:, ::2].t(), stream=stream)
         side.synchronize()
         assert torch.equal(got, want) and torch.equal(got2, want2)
+
+
+# ------------------------------------------------------------------ wide results: the backward pass of a large vocabulary
+
+def back_bytes(M, N, K, act=0):
+    n = ctypes.c_size_t()
+    assert gb.load().gemm_bt_linear_backward_workspace(M, N, K, act, ctypes.byref(n)) == gb.OK
+    return n.value
+
+
+def test_wide_linear_backward_is_not_cut_for_its_width():
+    """dX = dz W reads dz row by row and W in steps of 64 rows: only a run of W past 2 GiB has to be cut, however wide dz
+    is.  dW = dz^T X reads dz in steps of 64 rows and is cut past 2 GiB of it.  Without slices (these dX have tiles enough
+    for every compute unit) the workspace holds the bias's partial sums alone, a few rows of them."""
+    for M, N, K in ((8192, 128256, 4096), (4096, 151936, 4096), (8192, 40000, 4096), (4096, 256000, 2304)):
+        assert M * N * 2 < 1 << 31
+        assert back_bytes(M, N, K) < 64 * N * 4, (M, N, K)
+    for M, N, K in ((16384, 128256, 4096), (8192, 151936, 4096)):  # dW in two slices, dX still whole
+        assert 2 * N * K * 4 <= back_bytes(M, N, K) < 2 * N * K * 4 + 64 * N * 4, (M, N, K)
+    M, N, K = 8192, 1 << 20, 2048  # W itself past 2 GiB: dX in slices too (and dW in 9)
+    assert back_bytes(M, N, K) >= 2 * M * K * 4 + 9 * N * K * 4
+
+
+@pytest.mark.gpu
+def test_wide_linear_backward(gpu):
+    """All of dX and dW of a wide result, in one run each, against 64 bits on the GPU: sums of N and M terms, N u and M u
+    times the sum of magnitudes, then one rounding into bf16 (2^-8 relative, a little over half its last place)."""
+    M, N, K = 4096, 33000, 4096
+    say("linear backward", M, N, K)
+    assert back_bytes(M, N, K) < 64 * N * 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy, x, w = ((torch.randn(*s, generator=g, device="cuda") * std).bfloat16() for s, std in (((M, N), 0.1), ((M, K), 1.0), ((N, K), 0.02)))
+    got = gpu.linear_backward(dy, x, w)
+    for name, g, (a, b), terms in (("dx", got.dx, (dy, w), N), ("dw", got.dweight, (dy.t(), x), M)):
+        a, b = a.double().contiguous(), b.double()
+        want = a @ b
+        bound = 2.0 ** -8 * want.abs() + terms * u * (a.abs() @ b.abs())
+        assert bool(((g.double() - want).abs() <= bound).all()), name
+    want = dy.double().sum(0)
+    assert bool(((got.dbias.double() - want).abs() <= 2.0 ** -8 * want.abs() + (M + 8) * u * dy.double().abs().sum(0)).all())
