@@ -639,11 +639,15 @@ static int plan_impl(int64_t batch, int64_t M, int64_t N, int64_t K, int in_dtyp
     p->bk = 64;
     // With an epilogue and a workspace, the streaming kernel only where its
     // workgroups of 8 rows of B are more than two per CU; else the tiles
-    // below, cut along K where it is long (us, bf16, streaming vs tiles, weights
-    // from HBM: 16x64x8192 22.7 vs 9.2, 16x1024x8192 22.9 vs 10.1, 16x1024x4096
-    // 12.8 vs 9.2, 16x4096x4096 13.2 vs 10.9, 16x4096x8192 23.1 vs 18.8,
-    // 16x1024x2048 7.9 vs 7.3, 16x4096x1024 5.6 vs 5.0, but 16x8192x8192 25.6
-    // vs 30.1).  The plain product keeps its kernel, and so its bits.
+    // below, cut along K where it is long (us, bf16, streaming vs cut tiles,
+    // weights from HBM, in brackets from the caches: 16x64x8192 23.0 vs 11.3
+    // (23.1 vs 9.6), 16x1024x8192 23.7 vs 13.3 (23.4 vs 10.7), 16x1024x4096
+    // 13.7 vs 11.9 (13.5 vs 9.6), 16x4096x8192 24.2 vs 20.7 (23.7 vs 15.9),
+    // 16x4096x4096 14.5 vs 14.5 (14.1 vs 10.6), but 16x8192x8192 25.6 vs 30.1).
+    // Tiles that are not cut gain from the caches only (16x1024x2048 8.7 vs 11.3
+    // (8.4 vs 7.7), 16x4096x1024 6.6 vs 7.8 (6.2 vs 5.5)): a caller without a
+    // workspace, as one who asked for its size and was told 0, streams.  The
+    // plain product keeps its kernel, and so its bits.
     if (M <= 16 && !(epi && allow_sk && N <= 16 * (int64_t)num_cu)) {
         p->kernel = KIND_SKINNY;
         p->bm = 16;

@@ -320,7 +320,7 @@ def linear(x, weight, bias=None, activation="none", residual=None, x_scale=None,
     with _on(device):
         s = _stream(device.index)
         need = _epi_bytes(M, N, K, in_code, out_code, device.index)
-        ws, ws_bytes = None, 0
+        ws, ws_bytes = None, 0  # 16-bit products of few rows that need none: without one they stream their weight
         if need:
             t = workspace_for(device, s, need)
             ws, ws_bytes = t.data_ptr(), t.numel()

@@ -242,7 +242,9 @@ typedef struct {
  *              planned as gemm_bt_ws plans them; 8-bit ones of few tiles are cut
  *              along K too (64 x 64 tiles, pieces of at least 2048 elements).
  *              For M <= 16 either run the streaming kernel where N is more than
- *              16 per compute unit, else (with a workspace) tiles
+ *              16 per compute unit, and 16-bit ones without a workspace (the
+ *              faster choice where the size is 0, unless B is in the caches)
+ *              for any N; else tiles
  * K == 0 is the empty sum: C = act(bias) + residual, A and B are not read.
  * bias, residual and preact need the alignment of their elements only.
  * preact must not overlap C or an input.  Types that are none of the above,
@@ -412,7 +414,8 @@ int gemm_bt_plan(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, i
 int gemm_bt_plan_ws(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align,
                     int b_align, int c_align, gemm_bt_plan_t* plan);
 
-/* The plan of gemm_bt_epi given a large enough workspace. */
+/* The plan of gemm_bt_epi given a workspace (not NULL, also where its size is 0)
+   that is large enough. */
 int gemm_bt_plan_epi(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align, int b_align,
                      int c_align, gemm_bt_plan_t* plan);
 

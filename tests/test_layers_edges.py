@@ -213,3 +213,34 @@ def test_wide_linear_backward(gpu):
         assert bool(((g.double() - want).abs() <= bound).all()), name
     want = dy.double().sum(0)
     assert bool(((got.dbias.double() - want).abs() <= 2.0 ** -8 * want.abs() + (M + 8) * u * dy.double().abs().sum(0)).all())
+
+
+# ------------------------------------------------------------------ few rows
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_few_rows_with_and_without_a_workspace(gpu, dt):
+    """16-bit products of 16 rows and fewer whose plan needs no workspace: streamed without one, as the torch wrapper calls
+    them, and on tiles with one.  The sum of K terms is within K u of the sum of their magnitudes, the bias adds u."""
+    from dense_tiled_gemm_amd.layers import Epilogue
+
+    lib, code = gpu.load(), {"bf16": gpu.BF16, "f16": gpu.F16}[dt]
+    for M, N, K in ((16, 4096, 1024), (16, 4096, 1000), (16, 1024, 2048), (8, 2048, 1024), (1, 4096, 1536), (3, 1111, 1999), (16, 4096, 0)):
+        say("few rows", M, N, K, dt)
+        p = gpu.gemm_bt_plan_epi(M, N, K, code, gpu.F32)
+        assert p.workspace_bytes == 0 and p.kernel != 3
+        x, w, b = randn(1, M, K, dtype=DT[dt]), randn(2, N, K, dtype=DT[dt]), randn(3, N)
+        want = x.double() @ w.double().t() + b.double()
+        bound = (K + 1) * u * (x.double().abs() @ w.double().abs().t()) + 2 * u * want.abs()
+        x, w, b = x.cuda(), w.cuda(), b.cuda()
+        e = Epilogue(bias=b.data_ptr(), bias_dtype=gpu.F32)
+        ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+        got = [gpu.linear(x, w, bias=b, out_dtype=torch.float32)]
+        for at, size in ((None, 0), (ws.data_ptr(), ws.numel())):
+            got.append(torch.full((M, N), float("nan"), device="cuda"))
+            assert lib.gemm_bt_epi(x.data_ptr(), w.data_ptr(), got[-1].data_ptr(), M, N, K, code, gpu.F32, ctypes.byref(e), at, size,
+                                   handle()) == gpu.OK
+        assert torch.equal(got[0], got[1])
+        for c in got:
+            assert bool(((c.cpu().double() - want).abs() <= bound).all())
+        assert int(ws.count_nonzero()) == 0
