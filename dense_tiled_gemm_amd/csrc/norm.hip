@@ -113,14 +113,15 @@ __device__ __forceinline__ float power_below(float rstd) {
 // The scale of a row of values t * rest, and what t is multiplied by for its
 // codes, from the largest |t|: scale = amax rest / Q, Q = 448 (E4M3) or 127
 // (int8), kept above 2^-100 so that its reciprocal is finite; NaN for a row that
-// holds an infinity or a NaN.
+// holds an infinity or a NaN, one that t * rest overflows to included.
 struct RowScale {
     float scale, code;
 };
 __device__ __forceinline__ RowScale row_scale_of(float amax, float rest, int qt) {
     const float q = qt == GEMM_BT_FP8_E4M3 ? 448.0f : 127.0f, nan = as_f32(0x7FC00000u);
-    if (as_u32(amax) >= 0x7F800000u) return {nan, nan};
-    const float s = amax * rest / q;
+    const float top = amax * rest;
+    if (as_u32(top) >= 0x7F800000u) return {nan, nan};
+    const float s = top / q;
     if (!(s >= 0x1p-100f)) return {0x1p-100f, rest * 0x1p100f};
     return {s, q / amax};
 }

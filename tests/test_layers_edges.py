@@ -244,3 +244,27 @@ def test_few_rows_with_and_without_a_workspace(gpu, dt):
         for c in got:
             assert bool(((c.cpu().double() - want).abs() <= bound).all())
         assert int(ws.count_nonzero()) == 0
+
+
+# ------------------------------------------------------------------ 8-bit rows whose values leave fp32's range
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [2, 9, 600, 4096, 20000])
+def test_rows_that_overflow_have_no_scale(gpu, d):
+    """y = h rstd w past fp32's largest value is an infinity, and so the row's scale a NaN; the rows beside it, below that
+    value, keep theirs: amax / Q within the norm's own (64 + d / 2048) u and 4 u for the scale's steps."""
+    x = torch.zeros(4, d)
+    x[0, 0], x[1, d - 1], x[3, 0], x[3, d // 2] = 1.0, -3.0, 1.0, 1.0
+    w = torch.ones(d)
+    # rstd is sqrt(d): the largest y is sqrt(d) w, 1.06 times the largest fp32 value in row 0 (w[0]); finite in row 1
+    w[0], w[d - 1] = 1.06 * torch.finfo(torch.float32).max / math.sqrt(d), 0.9 * torch.finfo(torch.float32).max / math.sqrt(d)
+    say("overflow", d)
+    assert bool(torch.isinf(gpu.add_rms_norm(x.cuda(), w.cuda(), eps=0.0).y[0, 0]))
+    for qt, q in ((torch.float8_e4m3fn, 448.0), (torch.int8, 127.0)):
+        n = gpu.add_rms_norm(x.cuda(), w.cuda(), eps=0.0, out_dtype=qt)
+        s = n.scale.cpu().double()
+        assert math.isnan(s[0]) and math.isnan(s[2])  # (a row of zeros without eps: 0 / 0)
+        for row in (1, 3):
+            y = x[row].double() / x[row].double().square().mean().sqrt() * w.double()
+            want = float(y.abs().max()) / q
+            assert abs(float(s[row]) - want) <= (64 + d / 2048 + 4) * u * want, (row, d)
