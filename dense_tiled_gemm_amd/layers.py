@@ -3,9 +3,11 @@ rows with scales, the product with bias, activation and residual in its epilogue
 
 As in the rest of the binding, every arithmetic step runs in the library's HIP kernels; torch supplies device memory
 and the stream.  Leading dimensions count as rows: an input of shape (..., d) is (rows, d), and its results have its
-leading dimensions.  Rows may lie any number of elements apart; other layouts are made contiguous first.  Calls are
-asynchronous on torch's current stream, or on ``stream`` (a handle or torch's object), on which their results are then
-allocated; inputs that another stream still writes have to be waited for by the caller, as with torch's own operators.
+leading dimensions.  The inputs of the norm and of the quantisation may have evenly spaced rows any number of elements
+apart (a slice of a wider tensor's last dimension, say); other layouts, and every strided input of the product, are made
+contiguous first.  Calls are asynchronous on torch's current stream, or on ``stream`` (a handle or torch's object), on
+which their results are then allocated; inputs that another stream still writes have to be waited for by the caller, as
+with torch's own operators.
 """
 from __future__ import annotations
 
@@ -73,8 +75,21 @@ def _rows(t, what):
     rows = t.numel() // d if d else shape[:-1].numel()
     if t.is_contiguous():
         return t, d, rows, d
-    if len(shape) == 2 and t.stride(1) == 1 and t.stride(0) >= d:
-        return t, t.stride(0), rows, d
+    strides = t.stride()
+    if strides[-1] == 1:
+        # the leading dimensions of more than one entry, from the last one on: each has to step over all of the one after it
+        ld = step = None
+        for n, s in zip(shape[-2::-1], strides[-2::-1]):
+            if n == 1:
+                continue
+            if step is None:
+                ld = s
+            elif s != step:
+                ld = 0
+                break
+            step = s * n
+        if ld is not None and ld >= d:
+            return t, ld, rows, d
     return t.contiguous(), d, rows, d
 
 

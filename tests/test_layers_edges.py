@@ -268,3 +268,46 @@ def test_rows_that_overflow_have_no_scale(gpu, d):
             y = x[row].double() / x[row].double().square().mean().sqrt() * w.double()
             want = float(y.abs().max()) / q
             assert abs(float(s[row]) - want) <= (64 + d / 2048 + 4) * u * want, (row, d)
+
+
+# ------------------------------------------------------------------ evenly spaced rows of more than two dimensions
+
+def evenly_spaced():
+    """(tensor on the CPU, whether its rows are evenly spaced and at least their length apart)."""
+    t = randn(1, 4, 6, 96, dtype=torch.bfloat16)
+    return [(t, True), (t[..., 32:64], True), (t[..., :1], True), (t[1:3, :, 5:50], True), (t[:, 2:3, 1:95], True), (t[0:1, :, :40], True),
+            (t.view(2, 2, 6, 96)[..., 8:], True), (t[:, ::2], True), (t[::2, 0], True), (t[0, 0, 3:90], True), (t[:, :5], False),
+            (t[::2, ::2, :8], False), (t.view(2, 2, 6, 96)[:, :1, :, :9], False), (t.transpose(0, 1), False), (t.transpose(1, 2), False), (t[..., ::2], False), (t[:, :1].expand(4, 6, 96), False),
+            (t[:1].expand(4, 6, 96), False), (t[:, 0, None].expand(4, 3, 96), False), (t.as_strided((3, 5, 8), (40, 8, 1)), True),
+            (t.as_strided((3, 5, 8), (20, 4, 1)), False), (t.as_strided((3, 5, 8), (60, 12, 1)), True)]
+
+
+@pytest.mark.parametrize("i", range(len(evenly_spaced())))
+def test_evenly_spaced_rows_are_not_copied(i):
+    from dense_tiled_gemm_amd.layers import _rows
+
+    t, even = evenly_spaced()[i]
+    got, ld, rows, d = _rows(t, "t")
+    assert (rows, d) == (math.prod(t.shape[:-1]), t.shape[-1])
+    assert torch.equal(got.as_strided((rows, d), (ld, 1)), t.reshape(rows, d)) and ld >= d
+    assert (got is t) == even
+
+
+@pytest.mark.gpu
+def test_norm_of_evenly_spaced_rows(gpu):
+    """Norm, quantisation and gradient of slices of three and four dimensions: the bits of their contiguous copies."""
+    for i, (t, _) in enumerate(evenly_spaced()):
+        say("rows of", tuple(t.shape), t.stride())
+        base = torch.zeros(4 * 6 * 96, dtype=t.dtype, device="cuda")
+        base.copy_(torch.as_strided(t, (base.numel(),), (1,), 0))
+        x = base.as_strided(t.shape, t.stride(), t.storage_offset())
+        c = x.contiguous()
+        w = (1 + randn(2, t.shape[-1], std=0.2)).cuda()
+        a, b = (gpu.add_rms_norm(v, w, residual=v, out_dtype=torch.float32, save_rstd=True) for v in (x, c))
+        assert a.y.shape == t.shape and torch.equal(a.y, b.y) and torch.equal(a.h, b.h) and torch.equal(a.rstd, b.rstd)
+        a, b = gpu.quantize_rows(x, torch.int8), gpu.quantize_rows(c, torch.int8)
+        assert torch.equal(a.q, b.q) and torch.equal(a.scale, b.scale)
+        rstd = torch.ones(t.shape[:-1], device="cuda")
+        a, b = (gpu.add_rms_norm_backward(v, v, w, rstd, dh=v) for v in (x, c))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(base.cpu(), torch.as_strided(t, (base.numel(),), (1,), 0))
