@@ -314,7 +314,10 @@ def linear(x, weight, bias=None, activation="none", residual=None, x_scale=None,
     wide = dtype if in_code == BF16 or in_code == F16 else torch.bfloat16
     y_dtype = wide if out_dtype is None else out_dtype
     out_code = _float_code(y_dtype, "out_dtype")
-    x, weight = _dense(x), _dense(weight)
+    if in_code == BF16 or in_code == F16:
+        x, weight = _dense(x), _dense(weight)
+    else:  # 8-bit products read whole 16-byte chunks
+        x, weight = _chunked(x), _chunked(weight)
     if bias is not None:
         bias = _term(bias, w_shape[:1], "bias")
         e.bias, e.bias_dtype = bias.data_ptr(), _float_code(bias.dtype, "bias")

@@ -311,3 +311,25 @@ def test_norm_of_evenly_spaced_rows(gpu):
         a, b = (gpu.add_rms_norm_backward(v, v, w, rstd, dh=v) for v in (x, c))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert torch.equal(base.cpu(), torch.as_strided(t, (base.numel(),), (1,), 0))
+
+
+# ------------------------------------------------------------------ 8-bit operands off a 16-byte boundary
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.int8, torch.float8_e4m3fn, torch.float8_e5m2])
+def test_linear_of_eight_bits_from_any_start(gpu, dt):
+    """x and the weight as views that start off a 16-byte boundary: the bits of the aligned ones."""
+    for M, N, K in ((3, 40, 64), (16, 8192, 512), (100, 300, 1024), (64, 512, 8192)):
+        x, w = randn(1, M, K, std=3.0).to(dt).cuda(), randn(2, N, K, std=3.0).to(dt).cuda()
+        b = randn(3, N).cuda()
+        want = gpu.linear(x, w, bias=b, activation="relu")
+        for off_x, off_w in ((1, 0), (0, 8), (5, 15)):
+            say("eight bits", M, N, K, dt, off_x, off_w)
+            moved = []
+            for t, off in ((x, off_x), (w, off_w)):
+                buf = torch.zeros(t.numel() + 16, dtype=torch.uint8, device="cuda").view(dt)
+                v = buf[off:off + t.numel()].view(t.shape)
+                v.copy_(t)
+                assert v.data_ptr() % 16 == off
+                moved.append(v)
+            assert torch.equal(gpu.linear(*moved, bias=b, activation="relu"), want)
