@@ -215,6 +215,8 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, save_rstd=F
         _same(residual, x, "residual")
         rr, ldr, _, _ = _rows(residual, "residual")
         h = _output(h_out, xr, shape, dtype, "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual: without one h is x itself")
     weight = _dense(weight)
     with _on(device):
         st = load().gemm_bt_rms_norm(xr.data_ptr(), ldx, _ptr(rr), ldr, weight.data_ptr(), y.data_ptr(), _ptr(h), _ptr(scale),

@@ -333,3 +333,15 @@ def test_linear_of_eight_bits_from_any_start(gpu, dt):
                 assert v.data_ptr() % 16 == off
                 moved.append(v)
             assert torch.equal(gpu.linear(*moved, bias=b, activation="relu"), want)
+
+
+# ------------------------------------------------------------------ refusals of the wrappers
+
+@pytest.mark.gpu
+def test_h_out_needs_a_residual(gpu):
+    x, w = randn(1, 3, 16).cuda(), torch.ones(16, device="cuda")
+    h = torch.full_like(x, 7.0)
+    with pytest.raises(ValueError, match="residual"):
+        gpu.add_rms_norm(x, w, h_out=h)
+    assert bool((h == 7.0).all())
+    assert gpu.add_rms_norm(x, w, residual=x, h_out=h).h is h and torch.equal(h, x + x)
