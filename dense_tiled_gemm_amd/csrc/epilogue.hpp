@@ -170,9 +170,14 @@ __device__ inline void store1(void* p, int t, size_t i, float v) {
 
 // ---- activations -------------------------------------------------------------
 
-// exp(x) and 1/x of the hardware (1 ulp each of their argument's rounding):
-// the epilogue runs these per output while the matrix cores idle, and its
-// results are rounded to 16 bits, or compared at fp32's own accuracy, after.
+// exp(x) and 1/x of the hardware, which are within 1 ulp; x log2(e) is rounded
+// before the exponential, so exp(x) is off by up to 1.25 |x| + 2 units of 2^-24,
+// relative.  Carried to the results (units of 2^-24, relative): silu 8 + 1.5 |z|,
+// gelu 24 + 1.25 z^2, gelu_tanh 8 + 6 |argument of its exponential|.  z is a
+// rounded fp32 value itself, which moves a tail by half as much or so, and
+// 16-bit results are rounded at 2^-9 or 2^-12; two or more operations per output
+// for the low part of the product would lie open in the epilogue, which nothing
+// covers.
 __device__ inline float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 __device__ inline float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
@@ -180,8 +185,9 @@ __device__ inline float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ inline float sigmoid_f(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
 // Phi(-x) = exp(-x^2/2) t p(t), t = 1 / (1 + x/4), for x >= 0: p is a least
-// largest relative error fit (3.4e-8) of exp(x^2/2) Phi(-x) / t on 0 < t <= 1,
-// highest power first, so the tail keeps its relative accuracy.
+// largest relative error fit (4.7e-8 with these fp32 coefficients) of exp(x^2/2)
+// Phi(-x) / t on 0 < t <= 1, highest power first, so the tail keeps the relative
+// accuracy that the exponential has.
 constexpr int kPhiTerms = 10;
 __device__ constexpr float kPhi[kPhiTerms] = {1.978199370e-02f, -8.087722957e-02f, 9.559692442e-02f, -3.171735257e-02f,
                                               6.369900703e-02f, 5.897518620e-02f,  8.160310239e-02f, 9.346635640e-02f,

@@ -345,3 +345,55 @@ def test_h_out_needs_a_residual(gpu):
         gpu.add_rms_norm(x, w, h_out=h)
     assert bool((h == 7.0).all())
     assert gpu.add_rms_norm(x, w, residual=x, h_out=h).h is h and torch.equal(h, x + x)
+
+
+# ------------------------------------------------------------------ tails of the activations
+
+def tail_points():
+    """Zeros, both signs, steps of 1/16 in the middle and the largest arguments whose results are normal fp32 numbers."""
+    z = torch.cat([torch.linspace(-87, 87, 2785), torch.linspace(-13, 13, 6657), randn(1, 2000, std=3.0), randn(2, 200, std=1e-3)])
+    return z.float()
+
+
+def act_and_units(z, act):
+    """act(z) in 64 bits, its derivative, and the relative error the header allows in units of 2^-24."""
+    if act == "silu":
+        p = torch.sigmoid(z)
+        return z * p, p + z * p * (1 - p), 8 + 1.5 * z.abs()
+    if act == "gelu":
+        # ndtr below -5 from the asymptotic continued fraction of Mills' ratio, whose error there is below 1e-12
+        x = z.abs().clamp_min(5.0)
+        f = x
+        for k in range(60, 0, -1):
+            f = x + k / f
+        density = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        phi = torch.where(z < -5, density / f, torch.special.ndtr(z))
+        return z * phi, phi + z * density, 24 + 1.25 * z * z
+    a = math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3)
+    p = torch.sigmoid(a)
+    return z * p, p + z * p * (1 - p) * math.sqrt(8 / math.pi) * (1 + 3 * 0.044715 * z * z), 8 + 6 * a.abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_tails_of_the_activations(gpu, act):
+    """fp32 results, relative to themselves.  The units: the exponential's argument carries one rounding of z (silu), two of
+    z z / 2 or five of gelu_tanh's cubic, times log2(e) rounded twice more, each as large as the argument; the exponential,
+    the reciprocal, the sum and the product are 8 more at most; Phi's polynomial of t = 1 / (1 + |z| / 4) 16 more (t's 3 by
+    the polynomial's condition of 3.2, its steps 3.4, its fit 0.8).  Below 2^-126 |z| a result may be 0."""
+    z = tail_points()
+    want, slope, units = act_and_units(z.double(), act)
+    bound = units * u * want.abs() + 2.0 ** -125 * z.double().abs()
+    assert bool((want[z < -4].abs() > 4 * bound[z < -4])[z[z < -4] > (-80 if act == "silu" else -6)].all())  # 0 would not pass
+    n, gz = z.numel(), z.cuda()
+    for M, K in ((1, 0), (3, 64), (300, 64)):  # the empty sum, the streaming kernel, tiles
+        say("tails", act, M, K)
+        x, w = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.ones(n, K, dtype=torch.bfloat16, device="cuda")
+        y = gpu.linear(x, w, bias=gz, activation=act, out_dtype=torch.float32).cpu().double()
+        bad = ((y - want).abs() > bound).any(0)
+        assert not bool(bad.any()), (act, z[bad][:5], y[0, bad][:5], want[bad][:5])
+    dz, dy = torch.empty(1, n, device="cuda"), torch.ones(1, n, device="cuda")
+    assert gpu.load().gemm_bt_act_backward(dy.data_ptr(), gz.data_ptr(), dz.data_ptr(), None, 1, n, {"silu": 4, "gelu": 2, "gelu_tanh": 3}[act],
+                                           gpu.F32, gpu.F32, gpu.F32, None, 0, handle()) == gpu.OK
+    off = (dz[0].cpu().double() - slope).abs() - (2.0 ** -19 * (1 + z.double().abs()))
+    assert bool((off <= 0).all()), (act, z[off > 0][:5])
