@@ -434,12 +434,13 @@ static bool plan_split_rule(int64_t M, int64_t N, int64_t K, int num_cu, int64_t
 // Split plan of an 8-bit product with an epilogue (whose scales make it a
 // serving product, often of few rows): where 64 x 64 tiles leave half the CUs
 // idle, each is cut along K into pieces of at least 8 steps of 256 (256-byte
-// tile rows), as many as fill the CUs.  Measured (us, int8, weights from HBM,
-// uncut vs cut; 128-byte rows in pieces of 16 steps in brackets): 64x8192x8192
-// 24.6 vs 20.1 (20.8), 16x1024x8192 17.1 vs 9.7 (10.4), 128x1024x8192 17.5 vs
-// 10.6 (11.2), 64x64x8192 17.1 vs 9.4, 256x512x4096 10.7 vs 9.2, 64x4096x4096
-// 10.8 vs 9.7; pieces of 4 steps lose (16x1024x8192 10.6, 64x512x2048 7.6 vs
-// 7.3).
+// tile rows), as many as fill the CUs.  Measured (us, int8, uncut vs cut,
+// weights that no cache holds): 64x8192x8192 27.4 vs 22.7, 16x1024x8192 20.9 vs
+// 10.7, 128x1024x8192 22.3 vs 12.2, 64x64x8192 17.2 vs 9.7, 256x512x4096 13.1 vs
+// 10.9, 64x4096x4096 14.1 vs 11.9; from the caches, with 128-byte rows in pieces
+// of 16 steps in brackets: 64x8192x8192 24.6 vs 20.1 (20.8), 16x1024x8192 17.1
+// vs 9.7 (10.4), 128x1024x8192 17.5 vs 10.6 (11.2); pieces of 4 steps lose
+// (16x1024x8192 10.6, 64x512x2048 7.6 vs 7.3).
 constexpr int64_t kSk8MinSteps = 8;
 static void plan_split8(int64_t K, int num_cu, gemm_bt_plan_t* p) {
     int n = 0;
@@ -459,7 +460,8 @@ static void plan_split8(int64_t K, int num_cu, gemm_bt_plan_t* p) {
 // Split plan of a 16-bit product with an epilogue and M > 64 whose 64 x 64
 // tiles leave half the CUs idle: cut along K from 24 steps of 128 on, into
 // pieces of at least 8 (the thin products' tile).  Measured (us, bf16, uncut vs
-// cut): 1213x91x4279 21.4 vs 15.3, 128x128x8192 22.5 vs 11.4, 512x512x4096 13.5
+// cut, operands from the caches; from HBM the cut gains more, 512x512x4096 17.8 vs
+// 12.4, 500x500x3000 16.2 vs 12.6): 1213x91x4279 21.4 vs 15.3, 128x128x8192 22.5 vs 11.4, 512x512x4096 13.5
 // vs 11.4, 128x2048x4096 13.4 vs 11.4, 500x500x3000 12.2 vs 11.4, 256x256x16384
 // 40.9 vs 20.0; with 16 steps it loses (512x512x2048 8.6 vs 9.6, 256x256x2048
 // 7.9 vs 8.7), and pieces of 4 steps do (128x128x8192 13.2).

@@ -3,8 +3,11 @@
 //   dX = dz W        (M x K, summed over N)
 //   dW = dz^T X      (N x K, summed over M)
 //   db = sum over rows of dz.
-// dz is made once, in the inputs' 16-bit type, by one pass over dy and z that
-// also leaves partial sums of db (act_back_kernel).  Both products then run in
+// dz is made once by one pass over dy and z that also leaves partial sums of db
+// (act_back_kernel).  It is rounded into the inputs' 16-bit type, since the
+// matrix instructions take 16-bit operands at the rate counted on here: in
+// bf16 the relative error of dX and dW is 0.0024 with it, 0.0017 without (their
+// own rounding).  db is summed before that rounding.  Both products then run in
 // ONE launch on the transpose-read tiles of trans_kernel.hpp, operands as they
 // lie in memory: the tiles of one fill the compute units that the other leaves
 // idle, the last block of each column of db is folded by a few more

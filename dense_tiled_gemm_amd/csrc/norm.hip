@@ -82,7 +82,7 @@ __device__ __forceinline__ u32 quant4(float a, float b, float c, float d) {
         int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
         return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     } else {
-        // NaN becomes 0 in the conversion to an integer
+        // (a NaN becomes -127 in the comparisons: a code without a value, whose row's scale is NaN)
         auto code = [](float v) { return (u32)(int)__builtin_fminf(__builtin_fmaxf(__builtin_rintf(v), -127.0f), 127.0f) & 255u; };
         return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
     }

@@ -7,7 +7,8 @@ leading dimensions.  The inputs of the norm and of the quantisation may have eve
 apart (a slice of a wider tensor's last dimension, say); other layouts, and every strided input of the product, are made
 contiguous first.  Calls are asynchronous on torch's current stream, or on ``stream`` (a handle or torch's object), on
 which their results are then allocated; inputs that another stream still writes have to be waited for by the caller, as
-with torch's own operators.
+with torch's own operators.  The calls stand outside torch's autograd: results never require gradients, whatever the
+inputs do, and a training step calls the backward functions itself.
 """
 from __future__ import annotations
 
@@ -356,7 +357,8 @@ def linear_backward(dy, x, weight, preact=None, activation="none", bias_grad=Tru
     """The gradients of linear's x, weight and bias for 16-bit x and weight: LinearGrads(dx, dweight, dbias).
 
     dy (..., N): the gradient of the result, of x's type; preact: what linear returned with save_preact (not needed
-    for the activation "none").  The gradient of the residual is dy itself.
+    for the activation "none").  All three are of x's type, a float32 bias's too.  The gradient of the residual is dy
+    itself, and relu's slope at 0 is 0.
     """
     if stream is not None:
         return _on_stream(stream, dy, lambda: linear_backward(dy, x, weight, preact, activation, bias_grad, need_dx, need_dweight))

@@ -354,7 +354,8 @@ int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes);
  *              aligned, any contents
  * N and K up to 2^21 - 1, dx and dw up to 2^21 tiles of 128 x 128 each.  x, w and (for GEMM_BT_ACT_NONE with N % 8 == 0) dy
  * need 16-byte alignment where K % 8 == 0 (else UNSUPPORTED); the rest needs
- * the alignment of its elements.  A gradient whose sum has no terms is zeros.
+ * the alignment of its elements.  dx, dw and dbias must not overlap an input or
+ * each other.  A gradient whose sum has no terms is zeros.
  * The gradient of an epilogue's residual is dy itself.
  */
 int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw,

@@ -397,3 +397,34 @@ def test_tails_of_the_activations(gpu, act):
                                            gpu.F32, gpu.F32, gpu.F32, None, 0, handle()) == gpu.OK
     off = (dz[0].cpu().double() - slope).abs() - (2.0 ** -19 * (1 + z.double().abs()))
     assert bool((off <= 0).all()), (act, z[off > 0][:5])
+
+
+# ------------------------------------------------------------------ results in an input's place, rows of odd length
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(5, 9), (700, 63), (1200, 513), (3, 1031), (700, 1031), (600, 4097), (300, 16383), (3, 20001)])
+def test_odd_rows_in_place(gpu, rows, d):
+    """The last load of a row of odd length begins inside the chunk before, which another thread may already have replaced:
+    what it holds of that chunk is not used.  The bits are those of results of their own."""
+    lib = gpu.load()
+    x, r, dy = (randn(i, rows, d, dtype=torch.bfloat16).cuda() for i in range(3))
+    w = (1 + randn(4, d, std=0.3)).bfloat16().cuda()
+    want = gpu.add_rms_norm(x, w, residual=r, save_rstd=True)
+    for into in (0, 1):
+        say("odd rows in place", rows, d, into)
+        pair = [x.clone(), r.clone()]
+        got = gpu.add_rms_norm(pair[0], w, residual=pair[1], h_out=pair[into], save_rstd=True)
+        assert torch.equal(pair[into], want.h) and torch.equal(got.y, want.y) and torch.equal(got.rstd, want.rstd)
+    dx, dw = gpu.add_rms_norm_backward(dy, want.h, w, want.rstd, dh=r)
+    need = ctypes.c_size_t()
+    assert lib.gemm_bt_rms_norm_backward_workspace(rows, d, ctypes.byref(need)) == gpu.OK
+    ws, dh, dw2 = torch.empty(need.value + 16, dtype=torch.uint8, device="cuda"), r.clone(), torch.empty_like(dw)
+    assert lib.gemm_bt_rms_norm_backward(dy.data_ptr(), d, want.h.data_ptr(), d, w.data_ptr(), want.rstd.data_ptr(), dh.data_ptr(), d,
+                                         dh.data_ptr(), dw2.data_ptr(), rows, d, gpu.BF16, gpu.BF16, ws.data_ptr(), need.value,
+                                         handle()) == gpu.OK
+    assert torch.equal(dh, dx) and torch.equal(dw2, dw)
+    dz, place = torch.empty_like(dy), dy.clone()
+    for out, src in ((dz, dy), (place, place)):
+        assert lib.gemm_bt_act_backward(src.data_ptr(), x.data_ptr(), out.data_ptr(), None, rows, d, 4, gpu.BF16, gpu.BF16, gpu.BF16, None, 0,
+                                        handle()) == gpu.OK
+    assert torch.equal(dz, place)
