@@ -23,7 +23,8 @@ and torch convenience wrappers ``mm_bt(a, b, out_dtype)`` (2-D or batched 3-D op
 ``mm_layout(a, b, a_layout, b_layout, out_dtype)`` and ``mm(a, b, out_dtype)`` (= a @ b).  The operators around the
 product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_backward, gemm_bt_act_backward,
 gemm_bt_linear_backward) are called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
-``add_rms_norm_backward`` and ``quantize_rows``, which need torch and are imported when first used.
+``add_rms_norm_backward`` and ``quantize_rows``; the layer norm's (gemm_bt_layer_norm and its backward pass) are
+``add_layer_norm`` and ``add_layer_norm_backward``.  They need torch and are imported when first used.
 """
 from __future__ import annotations
 
@@ -44,7 +45,8 @@ EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layo
            "gemm_bt_plan_ws", "gemm_bt_noalloc", "gemm_bt_epi", "gemm_bt_rms_norm", "gemm_bt_rms_norm_backward",
            "gemm_bt_rms_norm_backward_workspace", "gemm_bt_quantize_rows", "gemm_bt_act_backward",
            "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace",
-           "gemm_bt_epi_workspace_size", "gemm_bt_plan_epi")
+           "gemm_bt_epi_workspace_size", "gemm_bt_plan_epi", "gemm_bt_layer_norm", "gemm_bt_layer_norm_backward",
+           "gemm_bt_layer_norm_backward_workspace")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -125,7 +127,11 @@ def load():
             lib.gemm_bt_linear_backward_workspace.argtypes = [i64, i64, i64, ci, szp]
             lib.gemm_bt_epi_workspace_size.argtypes = [i64, i64, i64, ci, ci, szp]
             lib.gemm_bt_plan_epi.argtypes = [i64, i64, i64, ci, ci, ci, ci, ci, ctypes.POINTER(Plan)]
-            for f in (lib.gemm_bt_epi, lib.gemm_bt_epi_workspace_size, lib.gemm_bt_plan_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
+            lib.gemm_bt_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ci, ci, ci, vp]
+            lib.gemm_bt_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64, i64, ci, ci, vp, sz, vp]
+            lib.gemm_bt_layer_norm_backward_workspace.argtypes = [i64, i64, szp]
+            for f in (lib.gemm_bt_layer_norm, lib.gemm_bt_layer_norm_backward, lib.gemm_bt_layer_norm_backward_workspace,
+                      lib.gemm_bt_epi, lib.gemm_bt_epi_workspace_size, lib.gemm_bt_plan_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
                       lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
                       lib.gemm_bt_act_backward_workspace, lib.gemm_bt_linear_backward,
                       lib.gemm_bt_linear_backward_workspace):
@@ -440,7 +446,8 @@ def mm(a, b, out_dtype=None, out=None, stream=None):
     return mm_layout(a, b, K_INNER, K_OUTER, out_dtype, out, stream)
 
 
-_LAYERS = ("linear", "linear_backward", "add_rms_norm", "add_rms_norm_backward", "quantize_rows")
+_LAYERS = ("linear", "linear_backward", "add_rms_norm", "add_rms_norm_backward", "quantize_rows", "add_layer_norm",
+           "add_layer_norm_backward")
 
 
 def __getattr__(name):

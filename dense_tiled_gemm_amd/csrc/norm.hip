@@ -1,7 +1,8 @@
-// norm.hip -- the row operators next to the product: root-mean-square norm
-// with the residual's addition, out in 16 or 32 bits or in 8 bits with one
-// scale per row; 8-bit rows with scales of a matrix as it is; the norm's
-// backward pass; and the backward pass of an epilogue's activation and bias.
+// norm.hip -- the row operators next to the product: root-mean-square norm and
+// layer norm with the residual's addition, out in 16 or 32 bits or in 8 bits
+// with one scale per row; 8-bit rows with scales of a matrix as it is; the
+// norms' backward passes; and the backward pass of an epilogue's activation and
+// bias.
 //
 // All of them are bound by HBM: each reads its inputs once and writes its
 // outputs once.  A row is read into registers (8 elements per thread and
@@ -45,16 +46,57 @@ __device__ __forceinline__ float row_join(float v, float* part) {
     return v;
 }
 
+// Layer norm's sums.  Lanes are joined by data-parallel moves of the vector unit
+// (a row of 16 lanes, then the rows), a few cycles each where a shuffle goes
+// through the LDS unit.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float add_moved(float v) {
+    return v + as_f32((u32)__builtin_amdgcn_update_dpp(0, (int)as_u32(v), CTRL, ROWS, 0xF, false));
+}
+// Lane 15 of each row of 16: the row's sum.
+__device__ __forceinline__ float sum16(float v) {
+    return add_moved<0x118>(add_moved<0x114>(add_moved<0x112>(add_moved<0x111>(v))));
+}
+// The sum over a wave, in every lane.
+__device__ __forceinline__ float sum64(float v) {
+    v = add_moved<0x143, 0xC>(add_moved<0x142, 0xA>(sum16(v)));
+    return as_f32((u32)__builtin_amdgcn_readlane((int)as_u32(v), 63));
+}
+// N sums over the threads of a row at one barrier (at most 16 waves), through N
+// rows of `part`, `gap` apart.
+template <bool WAVE, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[16], int gap) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = sum64(v[i]);
+    if constexpr (!WAVE) {
+        const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[i * gap][threadIdx.x >> 6] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = as_f32((u32)__builtin_amdgcn_readlane((int)as_u32(sum16(lane < waves ? part[i * gap][lane & 15] : 0.0f)), 15));
+    }
+}
+template <bool WAVE>
+__device__ __forceinline__ float row_sum(float v, float (*part)[16]) {
+    float one[1] = {v};
+    row_sums<WAVE, 1>(one, part, 0);
+    return one[0];
+}
+
 // ---- rows in chunks of 8 ---------------------------------------------------------
 
 // Elements i .. i+7 of a row of d that starts at element `base` of p.  RAGGED
 // (d >= 8, no multiple of 8): the last chunk is loaded from element d - 8 on and
-// moved into place when it is decoded.  A load is then one instruction for
+// moved into place when it is decoded.  WHOLE: every chunk is known to be 8 elements.  A load is then one instruction for
 // every lane, and nothing waits for it before its use, where a branch that put
 // single elements together waits for everything in flight.  Rows of whole
 // chunks have kernels without the moves.
-template <bool RAGGED>
+template <bool RAGGED, bool WHOLE = false>
 __device__ __forceinline__ Raw8 load_chunk(const void* p, int t, long long base, int i, int d, bool nt = false) {
+    if constexpr (WHOLE) return load_raw8(p, t, (size_t)base + i, 8, nt);
     if constexpr (RAGGED) return load_raw8(p, t, (size_t)(base + min(i, d - 8)), 8, nt);
     return load_raw8(p, t, (size_t)base + i, min(8, d - i), nt);
 }
@@ -165,9 +207,24 @@ struct NormArgs {
     int d;
     float eps;
     int y_type;
+    const void* bias;      // layer norm alone, in weight's type; nullptr: none
+    float* mean;           // layer norm alone; nullptr: not kept
 };
 
 __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
+
+// The mean of a row of d values whose sum in fp32 is `sum`.  Where that left
+// fp32's range the values are summed once more, 2^-27 of each (d <= 2^26).
+template <bool WAVE, class Each>
+__device__ __forceinline__ float mean_of(float sum, int d, float* part, Each&& each) {
+    float mean = sum / (float)d;
+    if (__builtin_expect(!(__builtin_fabsf(mean) < __builtin_inff()), 0)) {
+        float s = 0.0f;
+        each([&](float v) __attribute__((always_inline)) { s = __builtin_fmaf(v, 0x1p-27f, s); });
+        mean = row_join<SumOp, WAVE>(s, part) / (float)d * 0x1p27f;
+    }
+    return mean;
+}
 
 // h = x + residual; y = h rstd w: one pass over x and the residual, whose row
 // stays in registers between its statistics and its results.  Bound by HBM:
@@ -178,23 +235,37 @@ __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t =
 // The T threads that hold a row, U chunks of 8 elements each (T * U * 8 >= d),
 // are a wave (WAVE; a workgroup is up to 4 of them, each with rows of its own) or
 // the whole workgroup, of as many waves as the row fills.
-template <int XT, int WT, int U, bool WAVE, bool RAGGED>
+// CENTER: layer norm, y = (h - mean) rstd w + b.  The sum of h gives m0; then off,
+// the mean of h - m0, which is what the rounding of m0 left out, comes with the
+// squares of h - m0, d off^2 above those of h - m0 - off.  So the centred values do
+// not depend on how well the first sum came out, and rows of nearly equal entries
+// keep what distinguishes them.  Bound by HBM: 8192 x 8192 bf16 with residual 98 us
+// (5.5 TB/s), 8192 x 4096 49, 16384 x 1024 24.  Two joins over the row's threads where
+// the other norm has one: with shuffles and three barriers they cost 113 us, with
+// two 108, with moves in the vector unit (row_sums) 98.
+template <int XT, int WT, int U, bool WAVE, bool RAGGED, bool CENTER = false>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs a) {
-    __shared__ float part[8][16];
+    constexpr bool WHOLE = !RAGGED && !WAVE;  // every chunk is 8 elements of the row (rows below 8 have a wave each)
+    // layer norm of two chunks per thread fetches w and b after the statistics: held
+    // through them they cost a third workgroup's registers
+    constexpr bool LATE = CENTER && U > 1;
+    __shared__ float part[CENTER ? 14 : 8][16];
     const int T = WAVE ? 64 : blockDim.x, RB = WAVE ? blockDim.x >> 6 : 1;
     const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int d = a.d;
     int flip = 0;
     for (long long row = (long long)blockIdx.x * RB + (WAVE ? threadIdx.x >> 6 : 0); row < a.rows;
          row += (long long)gridDim.x * RB) {
-        Raw8 xr[U], rr[U], wr[U];
+        Raw8 xr[U], rr[U], wr[U], br[CENTER ? U : 1];
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                xr[u] = load_chunk<RAGGED>(a.x, XT, row * a.ldx, i, d);
-                if (a.residual) rr[u] = load_chunk<RAGGED>(a.residual, XT, row * a.ldr, i, d);
-                if (a.weight) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
+                xr[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.x, XT, row * a.ldx, i, d);
+                if (a.residual) rr[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.residual, XT, row * a.ldr, i, d);
+                if (!LATE && a.weight) wr[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.weight, WT, 0, i, d);
+                if constexpr (CENTER && !LATE)
+                    if (a.bias) br[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.bias, WT, 0, i, d);
             }
         });
         float h[U][8], ss = 0.0f;
@@ -209,41 +280,79 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] += v[e];
                 }
-                if (a.h) store8(a.h, XT, (size_t)(row * d) + i, min(8, d - i), h[u]);
+                if (a.h) store8(a.h, XT, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), h[u]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[u][e] = 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[u][e], h[u][e], ss);
+            for (int e = 0; e < 8; ++e) ss = CENTER ? ss + h[u][e] : __builtin_fmaf(h[u][e], h[u][e], ss);
         });
+        auto each = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f(h[u][e]);
+        };
+        if constexpr (CENTER) {
+            float sums[2] = {0.0f, 0.0f};
+            const float m0 = mean_of<WAVE>(row_sum<WAVE>(ss, part + 8 + flip), d, part[10 + flip], each);
+            // (elements past the row's end stay 0)
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int n = d - (u * T + renew(t)) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if ((WHOLE ? 0 : e) < n) h[u][e] -= m0;
+                    sums[0] += h[u][e];
+                    sums[1] = __builtin_fmaf(h[u][e], h[u][e], sums[1]);
+                }
+            });
+            row_sums<WAVE, 2>(sums, part + flip, 12);
+            const float off = sums[0] / (float)d;
+            if (a.mean && t == 0) a.mean[row] = m0 + off;
+            ss = __builtin_fmaxf(__builtin_fmaf(-off * off, (float)d, sums[1]), 0.0f);
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int n = d - (u * T + renew(t)) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((WHOLE ? 0 : e) < n) h[u][e] -= off;
+            });
+        }
         float rstd = 1.0f;
         if (a.weight) {
-            ss = row_join<SumOp, WAVE>(ss, part[flip]);
-            rstd = rstd_of<WAVE>(ss, d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f(h[u][e]);
-            });
+            if constexpr (!CENTER) ss = row_join<SumOp, WAVE>(ss, part[flip]);
+            rstd = rstd_of<WAVE>(ss, d, a.eps, part + 4, flip, each);
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
         const bool codes = is_code_type(a.y_type);
-        const float factor = codes && a.weight ? power_below(rstd) : rstd;
+        const float factor = codes && a.weight && !CENTER ? power_below(rstd) : rstd;
         float amax = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
+                if constexpr (LATE) {
+                    wr[u] = load_chunk<RAGGED, WHOLE>(a.weight, WT, 0, i, d);
+                    if (a.bias) br[u] = load_chunk<RAGGED, WHOLE>(a.bias, WT, 0, i, d);
+                }
                 if (a.weight) {
                     float w[8];
                     decode_chunk<RAGGED>(wr[u], WT, i, d, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * factor * w[e];
                 }
+                if constexpr (CENTER)
+                    if (a.bias) {
+                        float b[8];
+                        decode_chunk<RAGGED>(br[u], WT, i, d, b);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[u][e] += b[e];
+                    }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[u][e]));
-                if (!codes) store8(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
+                if (!codes) store8(a.y, a.y_type, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), h[u]);
             }
         });
         if (codes) {
@@ -256,7 +365,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
                 if (i < d) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] *= s.code;
-                    store_codes(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
+                    store_codes(a.y, a.y_type, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), h[u]);
                 }
             });
         }
@@ -266,10 +375,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
 
 // Rows too long for a workgroup's registers: read once per statistic.  h is
 // written in the last pass, so that it may replace x or the residual.
-template <int XT, int WT>
+template <int XT, int WT, bool CENTER = false>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
     constexpr int T = 1024;
-    __shared__ float part[8][16];
+    __shared__ float part[CENTER ? 14 : 8][16];
     const int t = threadIdx.x;
     int flip = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -282,35 +391,59 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
                 for (int e = 0; e < 8; ++e) h[e] += v[e];
             }
         };
-        auto load_y = [&](int i, int n, float factor, float (&h)[8]) __attribute__((always_inline)) {
+        float m0 = 0.0f, off = 0.0f;
+        // h, and without its mean
+        auto load_c = [&](int i, int n, float (&h)[8]) __attribute__((always_inline)) {
             load_h(i, n, h);
+            if constexpr (CENTER) {
+                const int m = renew(n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = e < m ? h[e] - m0 - off : 0.0f;
+            }
+        };
+        auto load_y = [&](int i, int n, float factor, float (&h)[8]) __attribute__((always_inline)) {
+            load_c(i, n, h);
             if (a.weight) {
                 float w[8];
                 decode8(load_raw8(a.weight, WT, (size_t)i, n), WT, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = h[e] * factor * w[e];
             }
+            if constexpr (CENTER)
+                if (a.bias) {
+                    float b[8];
+                    decode8(load_raw8(a.bias, WT, (size_t)i, n), WT, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[e] += b[e];
+                }
         };
         const bool codes = is_code_type(a.y_type);
         float rstd = 1.0f, code = 1.0f, h[8];
+        auto each = [&](auto&& f) __attribute__((always_inline)) {
+            for (long long i = t * 8; i < a.d; i += T * 8) {
+                load_c((int)i, min(8, a.d - (int)i), h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f(h[e]);
+            }
+        };
+        if constexpr (CENTER) {
+            float sum = 0.0f;
+            each([&](float v) __attribute__((always_inline)) { sum += v; });
+            // (m0 is still 0 while the mean is taken, off while its rest is)
+            m0 = mean_of<false>(row_join<SumOp, false>(sum, part[8 + flip]), a.d, part[10 + flip], each);
+            sum = 0.0f;
+            each([&](float v) __attribute__((always_inline)) { sum += v; });
+            off = row_join<SumOp, false>(sum, part[12 + flip]) / (float)a.d;
+            if (a.mean && t == 0) a.mean[row] = m0 + off;
+        }
         if (a.weight) {
             float ss = 0.0f;
-            for (long long i = t * 8; i < a.d; i += T * 8) {
-                load_h((int)i, min(8, a.d - (int)i), h);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
-            }
+            each([&](float v) __attribute__((always_inline)) { ss = __builtin_fmaf(v, v, ss); });
             ss = row_join<SumOp, false>(ss, part[flip]);
-            rstd = rstd_of<false>(ss, a.d, a.eps, part + 4, flip, [&](auto&& f) __attribute__((always_inline)) {
-                for (long long i = t * 8; i < a.d; i += T * 8) {
-                    load_h((int)i, min(8, a.d - (int)i), h);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f(h[e]);
-                }
-            });
+            rstd = rstd_of<false>(ss, a.d, a.eps, part + 4, flip, each);
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
-        const float factor = codes && a.weight ? power_below(rstd) : rstd;
+        const float factor = codes && a.weight && !CENTER ? power_below(rstd) : rstd;
         if (codes) {
             float amax = 0.0f;
             for (long long i = t * 8; i < a.d; i += T * 8) {
@@ -350,11 +483,12 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
 
 // Rows of no elements: their squares' mean is 0, and so is their largest
 // magnitude.
-__global__ __launch_bounds__(256) void empty_rows_kernel(float* scale, float* rstd, long long rows, float eps) {
+__global__ __launch_bounds__(256) void empty_rows_kernel(float* scale, float* rstd, float* mean, long long rows, float eps) {
     const long long step = (long long)gridDim.x * 256;
     for (long long row = (long long)blockIdx.x * 256 + threadIdx.x; row < rows; row += step) {
         if (scale) scale[row] = 0x1p-100f;
         if (rstd) rstd[row] = 1.0f / __builtin_sqrtf(eps);
+        if (mean) mean[row] = 0.0f;
     }
 }
 
@@ -370,6 +504,8 @@ struct NormBackArgs {
     float* partials;  // gridDim.x rows of d sums of dy * xhat
     long long rows, ld_dy, ldh, ld_dh;
     int d;
+    const float* mean;    // layer norm alone
+    float* bias_parts;    // layer norm alone: gridDim.x rows of d sums of dy, nullptr: not wanted
     // rows of whole 16-byte chunks: dy, h and dh are read past the caches (8192
     // x 8192 bf16 100.3 -> 93.6 us).  Elsewhere neighbouring chunks share lines, and
     // it makes no difference (8191 x 4097 80.5 against 80.9).
@@ -384,41 +520,47 @@ struct NormBackArgs {
 // workgroup leaves one row of partial sums.  AHEAD: the next row is fetched
 // while this one is worked on, and the weight stays in registers; without it
 // (rows that fill the registers) both are read when they are needed.
-template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST, bool RAGGED>
+// CENTER: layer norm (8192 x 4096 bf16 with dh and db 50 us in all, 5.4 TB/s; joins by
+// shuffles 53).  xhat = (h - mean) rstd, dx = rstd (g - mean(g) - xhat mean(g
+// xhat)) + dh, and db = sum over rows of dy, summed and left like dw.
+template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST, bool RAGGED, bool CENTER = false>
 __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
     constexpr int RB = WAVE ? MOST / 64 : 1;
-    __shared__ float part[2][16];
+    constexpr int S = CENTER ? 2 : 1;  // sums over rows: dw, db
+    constexpr bool WHOLE = !RAGGED && !WAVE;  // every chunk is 8 elements of the row (rows below 8 have a wave each)
+    __shared__ float part[2 * S][16];
     __shared__ float joined[WAVE ? MOST * U * 8 : 1];
     const int T = WAVE ? 64 : blockDim.x;
     const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int d = a.d;
-    float dw[U][8];
+    float dw[S * U][8];  // with db after it
     Raw8 wr[U];
     if constexpr (AHEAD)
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
-            if (i < d) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
+            if (i < d) wr[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.weight, WT, 0, i, d);
         });
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < S * U; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[u][e] = 0.0f;
     const long long step = (long long)gridDim.x * RB;
     struct Row {
         Raw8 dy[U], h[U], dh[U];
-        float rstd;
+        float rstd, mean;
     };
     auto fetch = [&](long long row, Row& r) __attribute__((always_inline)) {
         if (row >= a.rows) return;
         r.rstd = a.rstd[row];
+        if constexpr (CENTER) r.mean = a.mean[row];
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
-                r.dy[u] = load_chunk<RAGGED>(a.dy, XT, row * a.ld_dy, i, d, a.nt);
-                r.h[u] = load_chunk<RAGGED>(a.h, XT, row * a.ldh, i, d, a.nt);
-                if (AHEAD && a.dh) r.dh[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d, a.nt);
+                r.dy[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.dy, XT, row * a.ld_dy, i, d, a.nt);
+                r.h[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.h, XT, row * a.ldh, i, d, a.nt);
+                if (AHEAD && a.dh) r.dh[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.dh, XT, row * a.ld_dh, i, d, a.nt);
             }
         });
     };
@@ -433,41 +575,56 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
         } else {
             fetch(row, now);
         }
-        float xhat[U][8], g[U][8], c = 0.0f;
+        float xhat[U][8], g[U][8], c = 0.0f, m = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 float w[8];
-                if constexpr (!AHEAD) wr[u] = load_chunk<RAGGED>(a.weight, WT, 0, i, d);
+                if constexpr (!AHEAD) wr[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.weight, WT, 0, i, d);
                 decode_chunk<RAGGED>(now.h[u], XT, i, d, xhat[u]);
                 decode_chunk<RAGGED>(now.dy[u], XT, i, d, g[u]);
                 decode_chunk<RAGGED>(wr[u], WT, i, d, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    xhat[u][e] *= now.rstd;
+                    if constexpr (CENTER) {
+                        // (0 past the row's end: 0 g stays 0 however far the mean is)
+                        xhat[u][e] = WHOLE || i + e < d ? (xhat[u][e] - now.mean) * now.rstd : 0.0f;
+                        dw[U + u][e] += g[u][e];
+                    } else {
+                        xhat[u][e] *= now.rstd;
+                    }
                     dw[u][e] = __builtin_fmaf(g[u][e], xhat[u][e], dw[u][e]);
                     g[u][e] *= w[e];
                     c = __builtin_fmaf(g[u][e], xhat[u][e], c);
+                    if constexpr (CENTER) m += g[u][e];
                 }
             }
         });
-        c = row_join<SumOp, WAVE>(c, part[flip]) / (float)d;
+        if constexpr (CENTER) {
+            float sums[2] = {c, m};
+            row_sums<WAVE, 2>(sums, part + flip, 2);
+            c = sums[0];
+            m = sums[1] / (float)d;
+        } else {
+            c = row_join<SumOp, WAVE>(c, part[flip]);
+        }
+        c /= (float)d;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = now.rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
+                for (int e = 0; e < 8; ++e) o[e] = now.rstd * __builtin_fmaf(-xhat[u][e], c, CENTER ? g[u][e] - m : g[u][e]);
                 if (a.dh) {
                     float v[8];
-                    if constexpr (!AHEAD) now.dh[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d);
+                    if constexpr (!AHEAD) now.dh[u] = load_chunk<RAGGED, CENTER && WHOLE>(a.dh, XT, row * a.ld_dh, i, d);
                     decode_chunk<RAGGED>(now.dh[u], XT, i, d, v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] += v[e];
                 }
-                store8(a.dx, XT, (size_t)(row * d) + i, min(8, d - i), o);
+                store8(a.dx, XT, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), o);
             }
         });
         if constexpr (AHEAD) now = next;
@@ -476,26 +633,32 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
     if constexpr (RB > 1) {
         // join the waves' sums, in wave order
         const int wave = threadIdx.x >> 6;
-        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
-            constexpr int u = decltype(uc)::value;
+        static_for<0, S>([&](auto sc) __attribute__((always_inline)) {
+            constexpr int s = decltype(sc)::value;
+            if constexpr (s > 0) __syncthreads();
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) joined[(wave * U * 8 + u * 8 + e) * 64 + t] = dw[u][e];
+                for (int e = 0; e < 8; ++e) joined[(wave * U * 8 + u * 8 + e) * 64 + t] = dw[s * U + u][e];
+            });
+            __syncthreads();
+            if (wave == 0)
+                static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                    constexpr int u = decltype(uc)::value;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+#pragma unroll
+                        for (int w = 1; w < RB; ++w) dw[s * U + u][e] += joined[(w * U * 8 + u * 8 + e) * 64 + t];
+                });
         });
-        __syncthreads();
         if (wave != 0) return;
-        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
-            constexpr int u = decltype(uc)::value;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int w = 1; w < RB; ++w) dw[u][e] += joined[(w * U * 8 + u * 8 + e) * 64 + t];
-        });
     }
-    static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+    static_for<0, S * U>([&](auto uc) __attribute__((always_inline)) {
         constexpr int u = decltype(uc)::value;
-        const int i = (u * T + t) * 8;
-        if (i < d) {
-            float* p = a.partials + (size_t)blockIdx.x * d + i;
+        const int i = (u % U * T + t) * 8;
+        float* const sums = u < U ? a.partials : a.bias_parts;
+        if (i < d && (u < U || sums)) {
+            float* p = sums + (size_t)blockIdx.x * d + i;
             if (i + 8 <= d) {
                 *(u32x4_any*)p = u32x4{as_u32(dw[u][0]), as_u32(dw[u][1]), as_u32(dw[u][2]), as_u32(dw[u][3])};
                 *(u32x4_any*)(p + 4) = u32x4{as_u32(dw[u][4]), as_u32(dw[u][5]), as_u32(dw[u][6]), as_u32(dw[u][7])};
@@ -511,10 +674,13 @@ __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {
 // Few rows: the first a.rows workgroups (WAVE: a wave each) make dx, one row
 // each; the others make dw itself, 64 columns each over all rows, from dy and
 // h as the caches hold them.  One launch, no partial sums.
-template <int XT, int WT, int U, bool WAVE, bool RAGGED>
-__global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs a, int row_blocks, void* dweight) {
-    __shared__ float part[16];
-    __shared__ float joined[128][65];
+// CENTER: layer norm, with db (dbias, nullptr: not wanted) beside dw.
+template <int XT, int WT, int U, bool WAVE, bool RAGGED, bool CENTER = false>
+__global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs a, int row_blocks, void* dweight, void* dbias) {
+    constexpr int S = CENTER ? 2 : 1;
+    constexpr bool WHOLE = !RAGGED && !WAVE;
+    __shared__ float part[S][16];
+    __shared__ float joined[S][128][65];
     const int d = a.d;
     if ((int)blockIdx.x < row_blocks) {
         const int T = WAVE ? 64 : blockDim.x;
@@ -522,7 +688,7 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
         const long long row = WAVE ? (long long)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
         if (row >= a.rows) return;
         Raw8 dyr[U], hr[U], dhr[U], wr[U];
-        const float rstd = a.rstd[row];
+        const float rstd = a.rstd[row], mean = CENTER ? a.mean[row] : 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
@@ -533,7 +699,7 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
                 if (a.dh) dhr[u] = load_chunk<RAGGED>(a.dh, XT, row * a.ld_dh, i, d);
             }
         });
-        float xhat[U][8], g[U][8], c = 0.0f;
+        float xhat[U][8], g[U][8], c = 0.0f, m = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
@@ -544,20 +710,32 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
                 decode_chunk<RAGGED>(dyr[u], XT, i, d, g[u]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    xhat[u][e] *= rstd;
+                    if constexpr (CENTER)
+                        xhat[u][e] = WHOLE || i + e < d ? (xhat[u][e] - mean) * rstd : 0.0f;
+                    else
+                        xhat[u][e] *= rstd;
                     g[u][e] *= w[e];
                     c = __builtin_fmaf(g[u][e], xhat[u][e], c);
+                    if constexpr (CENTER) m += g[u][e];
                 }
             }
         });
-        c = row_join<SumOp, WAVE>(c, part) / (float)d;
+        if constexpr (CENTER) {
+            float sums[2] = {c, m};
+            row_sums<WAVE, 2>(sums, part, 1);
+            c = sums[0];
+            m = sums[1] / (float)d;
+        } else {
+            c = row_join<SumOp, WAVE>(c, part[0]);
+        }
+        c /= (float)d;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = rstd * __builtin_fmaf(-xhat[u][e], c, g[u][e]);
+                for (int e = 0; e < 8; ++e) o[e] = rstd * __builtin_fmaf(-xhat[u][e], c, CENTER ? g[u][e] - m : g[u][e]);
                 if (a.dh) {
                     float v[8];
                     decode_chunk<RAGGED>(dhr[u], XT, i, d, v);
@@ -572,18 +750,21 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
     // dw of 64 columns: 8 lanes of 8 columns, blockDim / 8 groups of them over the rows
     const int G = blockDim.x >> 3, l = threadIdx.x & 7, k = threadIdx.x >> 3;
     const int j = ((int)blockIdx.x - row_blocks) * 64 + l * 8;
-    float sum[8];
+    float sum[S][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[s][e] = 0.0f;
     if (j < d) {
         for (int r = k; r < a.rows; r += 4 * G) {
             Raw8 dyr[4], hr[4];
-            float rs[4];
+            float rs[4], mean[4];
             static_for<0, 4>([&](auto uc) __attribute__((always_inline)) {
                 constexpr int u = decltype(uc)::value;
                 const long long row = r + u * G;
                 if (row < a.rows) {
                     rs[u] = a.rstd[row];
+                    if constexpr (CENTER) mean[u] = a.mean[row];
                     dyr[u] = load_chunk<RAGGED>(a.dy, XT, row * a.ld_dy, j, d);
                     hr[u] = load_chunk<RAGGED>(a.h, XT, row * a.ldh, j, d);
                 }
@@ -595,46 +776,66 @@ __global__ __launch_bounds__(1024) void norm_back_few_kernel(const NormBackArgs 
                     decode_chunk<RAGGED>(dyr[u], XT, j, d, y);
                     decode_chunk<RAGGED>(hr[u], XT, j, d, h);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(y[e], h[e] * rs[u], sum[e]);
+                    for (int e = 0; e < 8; ++e) {
+                        sum[0][e] = __builtin_fmaf(y[e], CENTER ? (h[e] - mean[u]) * rs[u] : h[e] * rs[u], sum[0][e]);
+                        if constexpr (CENTER) sum[S - 1][e] += y[e];
+                    }
                 }
             });
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) joined[k][l * 8 + e] = sum[e];
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) joined[s][k][l * 8 + e] = sum[s][e];
     __syncthreads();
     // the groups' sums, halved in number until one is left
     for (int half = G >> 1; half > 0; half >>= 1) {
-        for (int i = threadIdx.x; i < half * 64; i += blockDim.x) joined[i >> 6][i & 63] += joined[(i >> 6) + half][i & 63];
+        for (int i = threadIdx.x; i < half * 64; i += blockDim.x)
+#pragma unroll
+            for (int s = 0; s < S; ++s) joined[s][i >> 6][i & 63] += joined[s][(i >> 6) + half][i & 63];
         __syncthreads();
     }
     const int col = ((int)blockIdx.x - row_blocks) * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && col < d) store1(dweight, WT, (size_t)col, joined[0][threadIdx.x]);
+    if (threadIdx.x < 64 && col < d) {
+        store1(dweight, WT, (size_t)col, joined[0][0][threadIdx.x]);
+        if (CENTER && dbias) store1(dbias, WT, (size_t)col, joined[S - 1][0][threadIdx.x]);
+    }
 }
 
 // Rows too long for a workgroup's registers: dw is summed in the workgroup's
 // row of partial sums itself, each word by one thread.
-template <int XT, int WT>
+template <int XT, int WT, bool CENTER = false>
 __global__ __launch_bounds__(1024) void norm_back_long_kernel(const NormBackArgs a) {
     constexpr int T = 1024;
-    __shared__ float part[2][16];
+    __shared__ float part[CENTER ? 4 : 2][16];
     const int t = threadIdx.x;
     float* sums = a.partials + (size_t)blockIdx.x * a.d;
-    for (long long i = t; i < a.d; i += T) sums[i] = 0.0f;
+    float* bsums = CENTER && a.bias_parts ? a.bias_parts + (size_t)blockIdx.x * a.d : nullptr;
+    for (long long i = t; i < a.d; i += T) {
+        sums[i] = 0.0f;
+        if (bsums) bsums[i] = 0.0f;
+    }
     int flip = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const float rstd = a.rstd[row];
+        const float rstd = a.rstd[row], mean = CENTER ? a.mean[row] : 0.0f;
         auto load1x = [&](const void* p, long long ld, long long i) { return load1(p, XT, (size_t)(row * ld + i)); };
-        float c = 0.0f;
-        for (long long i = t; i < a.d; i += T)
-            c = __builtin_fmaf(load1x(a.dy, a.ld_dy, i) * load1(a.weight, WT, i), load1x(a.h, a.ldh, i) * rstd, c);
-        c = row_join<SumOp, false>(c, part[flip]) / (float)a.d;
+        auto load_xhat = [&](long long i) { return (CENTER ? load1x(a.h, a.ldh, i) - mean : load1x(a.h, a.ldh, i)) * rstd; };
+        float c = 0.0f, m = 0.0f;
         for (long long i = t; i < a.d; i += T) {
-            const float dy = load1x(a.dy, a.ld_dy, i), xhat = load1x(a.h, a.ldh, i) * rstd;
-            float o = rstd * __builtin_fmaf(-xhat, c, dy * load1(a.weight, WT, i));
+            const float g = load1x(a.dy, a.ld_dy, i) * load1(a.weight, WT, i);
+            c = __builtin_fmaf(g, load_xhat(i), c);
+            if constexpr (CENTER) m += g;
+        }
+        c = row_join<SumOp, false>(c, part[flip]) / (float)a.d;
+        if constexpr (CENTER) m = row_join<SumOp, false>(m, part[2 + flip]) / (float)a.d;
+        for (long long i = t; i < a.d; i += T) {
+            const float dy = load1x(a.dy, a.ld_dy, i), xhat = load_xhat(i), g = dy * load1(a.weight, WT, i);
+            float o = rstd * __builtin_fmaf(-xhat, c, CENTER ? g - m : g);
             if (a.dh) o += load1x(a.dh, a.ld_dh, i);
             store1(a.dx, XT, (size_t)(row * a.d + i), o);
             sums[i] = __builtin_fmaf(dy, xhat, sums[i]);
+            if (bsums) bsums[i] += dy;
         }
         flip ^= 1;
     }
@@ -645,6 +846,11 @@ __global__ __launch_bounds__(1024) void norm_back_long_kernel(const NormBackArgs
 __global__ __launch_bounds__(512) void fold_kernel(const FoldArgs a) {
     __shared__ float sums[512 / 16][17];
     fold_columns<512>(a, blockIdx.x, sums);
+}
+// Two at once, the grid's second axis.
+__global__ __launch_bounds__(512) void fold2_kernel(const FoldArgs a, const FoldArgs b) {
+    __shared__ float sums[512 / 16][17];
+    fold_columns<512>(blockIdx.y ? b : a, blockIdx.x, sums);
 }
 
 // ---- activation and bias, backward -------------------------------------------------
@@ -731,31 +937,31 @@ struct RowPlan {
 // Whole waves that hold `chunks` groups of 8 elements, U of them per thread.
 static int threads_for(int64_t chunks, int U) { return (int)((chunks + 64 * U - 1) / (64 * U) * 64); }
 
-template <int XT, int WT, bool R>
+template <int XT, int WT, bool R, bool C>
 static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
     const int64_t chunks = (d + 7) / 8;
     // Few rows (at most two per CU): one chunk per thread, so that one load's
     // latency is all that is waited for.
     const bool few = rows <= 2 * num_cu;
     if (chunks <= 64)
-        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R>, 64, 1}
-                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R>, 256, 4};
-    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true, R>, 256, 4};
+        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R, C>, 64, 1}
+                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R, C>, 256, 4};
+    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true, R, C>, 256, 4};
     if (chunks <= 256 || (few && chunks <= 1024))
-        return {(const void*)&norm_kernel<XT, WT, 1, false, R>, threads_for(chunks, 1), 1};
-    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false, R>, threads_for(chunks, 2), 1};
-    return {(const void*)&norm_long_kernel<XT, WT>, 1024, 1};
+        return {(const void*)&norm_kernel<XT, WT, 1, false, R, C>, threads_for(chunks, 1), 1};
+    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false, R, C>, threads_for(chunks, 2), 1};
+    return {(const void*)&norm_long_kernel<XT, WT, C>, 1024, 1};
 }
 
-template <int XT, int WT, bool R>
+template <int XT, int WT, bool R, bool C>
 static RowPlan norm_back_plan(int64_t d) {
     const int64_t chunks = (d + 7) / 8;
-    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 1, true, true, 256, R>, 256, 4};
-    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 2, true, true, 256, R>, 256, 4};
-    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 1, false, true, 256, R>, threads_for(chunks, 1), 1};
-    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 2, false, true, 512, R>, threads_for(chunks, 2), 1};
-    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 2, false, false, 1024, R>, threads_for(chunks, 2), 1};
-    return {(const void*)&norm_back_long_kernel<XT, WT>, 1024, 1};
+    if (chunks <= 64) return {(const void*)&norm_back_kernel<XT, WT, 1, true, true, 256, R, C>, 256, 4};
+    if (chunks <= 128) return {(const void*)&norm_back_kernel<XT, WT, 2, true, true, 256, R, C>, 256, 4};
+    if (chunks <= 256) return {(const void*)&norm_back_kernel<XT, WT, 1, false, true, 256, R, C>, threads_for(chunks, 1), 1};
+    if (chunks <= 1024) return {(const void*)&norm_back_kernel<XT, WT, 2, false, true, 512, R, C>, threads_for(chunks, 2), 1};
+    if (chunks <= 2048) return {(const void*)&norm_back_kernel<XT, WT, 2, false, false, 1024, R, C>, threads_for(chunks, 2), 1};
+    return {(const void*)&norm_back_long_kernel<XT, WT, C>, 1024, 1};
 }
 
 // Rows that end inside a chunk of 8 (those below 8 have no chunk to load from).
@@ -780,31 +986,33 @@ static RowPlan with_types(int x_type, int w_type, int64_t d, F&& f) {
     return w_type == GEMM_BT_F32 ? g(BF16{}, F32{}) : g(BF16{}, BF16{});
 }
 
+template <bool C = false>
 static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
     int num_cu = 0;
     const int st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
     const RowPlan p = with_types(
-        x_type, w_type, a.d, [&](auto x, auto w, auto r) { return norm_plan<x(), w(), r()>(a.rows, a.d, num_cu); });
+        x_type, w_type, a.d, [&](auto x, auto w, auto r) { return norm_plan<x(), w(), r(), C>(a.rows, a.d, num_cu); });
     const int64_t grid = std::min<int64_t>((a.rows + p.rows_per_block - 1) / p.rows_per_block, 1 << 20);
     void* args[] = {&a};
     return launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
 }
 
 // Rows of no elements leave their scales and rstd, where there are any.
-static int empty_rows(float* scale, float* rstd, long long rows, float eps, void* stream) {
-    if (!aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
-    if (!scale && !rstd) return GEMM_BT_OK;
+static int empty_rows(float* scale, float* rstd, float* mean, long long rows, float eps, void* stream) {
+    if (!aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32) || !aligned(mean, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!scale && !rstd && !mean) return GEMM_BT_OK;
     int num_cu = 0;
     const int st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
-    void* args[] = {&scale, &rstd, &rows, &eps};
+    void* args[] = {&scale, &rstd, &mean, &rows, &eps};
     return launch((const void*)&empty_rows_kernel, dim3((unsigned)std::min<int64_t>((rows + 255) / 256, 8 * num_cu)), 256, args,
                   stream);
 }
 
+template <bool C = false>
 static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
-    return with_types(x_type, w_type, d, [&](auto x, auto w, auto r) { return norm_back_plan<x(), w(), r()>(d); });
+    return with_types(x_type, w_type, d, [&](auto x, auto w, auto r) { return norm_back_plan<x(), w(), r(), C>(d); });
 }
 // The kernel for few rows, or none: while dy and h stay in the caches, reading
 // them twice costs less than a second launch and its partial sums, as long as
@@ -813,7 +1021,7 @@ static RowPlan norm_back_plan_of(int x_type, int w_type, int64_t d) {
 // 8192 17.5 vs 13.7; with 16 rows to a group 1000 x 2050 fp32 13.1 vs 14.3, 400 x
 // 1023 bf16 7.0 vs 9.2, with 32 1000 x 2048 11.3 vs 19.8, 2048 x 4096 22.5 vs 27.0).  Threads in a power of two: the
 // last step halves their groups.
-template <int XT, int WT, bool R>
+template <int XT, int WT, bool R, bool C>
 static RowPlan norm_back_few(int64_t rows, int64_t d) {
     const int64_t chunks = (d + 7) / 8;
     auto pow2 = [](int64_t n) {
@@ -823,9 +1031,9 @@ static RowPlan norm_back_few(int64_t rows, int64_t d) {
     };
     if (chunks > 2048 || rows * d > (4 << 20)) return {nullptr, 0, 0};
     RowPlan p;
-    if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true, R>, 256, 4};
-    else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false, R>, pow2(chunks), 1};
-    else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false, R>, 1024, 1};
+    if (chunks <= 64) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, true, R, C>, 256, 4};
+    else if (chunks <= 1024) p = {(const void*)&norm_back_few_kernel<XT, WT, 1, false, R, C>, pow2(chunks), 1};
+    else p = {(const void*)&norm_back_few_kernel<XT, WT, 2, false, R, C>, 1024, 1};
     if (rows > p.threads) return {nullptr, 0, 0};
     return p;
 }
@@ -898,6 +1106,69 @@ int launch_act_back(ActBackArgs a, int num_cu, void* stream) {
     return launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
 }
 
+// ---- the norms' backward passes: checks and launches ---------------------------------
+
+// Layer norm (C) leaves the partial sums of dbias after those of dweight.
+template <bool C>
+static int norm_back_workspace(int64_t rows, int64_t d, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    // (the plans' grids do not depend on the types, nor on whole chunks)
+    if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16, false, C>(rows, d).fn) return GEMM_BT_OK;
+    *bytes = (size_t)(norm_back_grid(norm_back_plan_of<C>(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * (C ? 8 : 4));
+    return GEMM_BT_OK;
+}
+
+template <bool C>
+static int norm_backward(NormBackArgs a, int64_t d, void* dweight, void* dbias, int x_dtype, int w_dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    const int64_t rows = a.rows;
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d == 0) return GEMM_BT_OK;
+    if (!dweight || !aligned(dweight, w_dtype) || !aligned(dbias, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (rows > 0) {
+        // (the few-rows kernel's sums for dweight read dy and h while dx is written)
+        if (!a.dy || !a.h || !a.weight || !a.rstd || (C && !a.mean) || !a.dx || a.dx == a.dy || a.dx == a.h)
+            return GEMM_BT_ERR_INVALID_VALUE;
+        if (!stride_ok(a.ld_dy, d) || !stride_ok(a.ldh, d) || (a.dh && !stride_ok(a.ld_dh, d))) return GEMM_BT_ERR_INVALID_VALUE;
+        if (!aligned(a.dy, x_dtype) || !aligned(a.h, x_dtype) || !aligned(a.dh, x_dtype) || !aligned(a.dx, x_dtype) ||
+            !aligned(a.weight, w_dtype) || !aligned(a.rstd, GEMM_BT_F32) || !aligned(a.mean, GEMM_BT_F32) ||
+            !aligned(workspace, GEMM_BT_F32))
+            return GEMM_BT_ERR_INVALID_VALUE;
+    }
+    int num_cu = 0;
+    int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    a.d = (int)d;
+    int64_t grid = 0;
+    if (rows > 0) {
+        const RowPlan few = with_types(
+            x_dtype, w_dtype, d, [&](auto x, auto w, auto r) { return norm_back_few<x(), w(), r(), C>(rows, d); });
+        if (few.fn) {
+            int row_blocks = (int)((rows + few.rows_per_block - 1) / few.rows_per_block);
+            void* args[] = {&a, &row_blocks, &dweight, &dbias};
+            return launch(few.fn, dim3((unsigned)(row_blocks + (d + 63) / 64)), few.threads, args, stream);
+        }
+        const RowPlan p = norm_back_plan_of<C>(x_dtype, w_dtype, d);
+        grid = norm_back_grid(p, rows, num_cu);
+        if (!workspace || workspace_bytes < (size_t)(grid * d * (C ? 8 : 4))) return GEMM_BT_ERR_INVALID_VALUE;
+        a.partials = (float*)workspace;
+        if (dbias) a.bias_parts = a.partials + grid * d;
+        a.nt = whole_chunks(a.dy, a.ld_dy, x_dtype) && whole_chunks(a.h, a.ldh, x_dtype) && whole_chunks(a.dh, a.ld_dh, x_dtype);
+        void* args[] = {&a};
+        st = launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
+        if (st != GEMM_BT_OK) return st;
+    }
+    if (!dbias) return fold((const float*)workspace, dweight, w_dtype, grid, d, stream);
+    FoldArgs fw = {(const float*)workspace, dweight, d, (int)grid, w_dtype}, fb = {fw.partials + grid * d, dbias, d, (int)grid, w_dtype};
+    void* args[] = {&fw, &fb};
+    return launch((const void*)&fold2_kernel, dim3(fold_blocks(d), 2), 512, args, stream);
+}
+
 }  // namespace gbt
 
 using namespace gbt;
@@ -913,14 +1184,34 @@ int gemm_bt_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t l
     if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (rows == 0) return GEMM_BT_OK;
     if (codes && !scale) return GEMM_BT_ERR_INVALID_VALUE;
-    if (d == 0) return empty_rows(codes ? scale : nullptr, rstd, rows, eps, stream);
+    if (d == 0) return empty_rows(codes ? scale : nullptr, rstd, nullptr, rows, eps, stream);
     if (!x || !weight || !y) return GEMM_BT_ERR_INVALID_VALUE;
     if (!stride_ok(ldx, d) || (residual && !stride_ok(ldr, d))) return GEMM_BT_ERR_INVALID_VALUE;
     if (!aligned(x, x_dtype) || !aligned(residual, x_dtype) || !aligned(h, x_dtype) || !aligned(weight, w_dtype) ||
         (!codes && !aligned(y, y_dtype)) || !aligned(scale, GEMM_BT_F32) || !aligned(rstd, GEMM_BT_F32))
         return GEMM_BT_ERR_INVALID_VALUE;
-    NormArgs a = {x, residual, weight, y, h, scale, rstd, rows, ldx, ldr, (int)d, eps, y_dtype};
+    NormArgs a = {x, residual, weight, y, h, scale, rstd, rows, ldx, ldr, (int)d, eps, y_dtype, nullptr, nullptr};
     return launch_norm(a, x_dtype, w_dtype, stream);
+}
+
+int gemm_bt_layer_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, const void* bias,
+                       void* y, void* h, float* scale, float* mean, float* rstd, int64_t rows, int64_t d, float eps, int x_dtype,
+                       int w_dtype, int y_dtype, void* stream) {
+    if (rows < 0 || d < 0 || !(eps >= 0.0f)) return GEMM_BT_ERR_INVALID_VALUE;
+    const bool codes = y_dtype == GEMM_BT_FP8_E4M3 || y_dtype == GEMM_BT_INT8;
+    if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype) || !(codes || float_type(y_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (rows == 0) return GEMM_BT_OK;
+    if (codes && !scale) return GEMM_BT_ERR_INVALID_VALUE;
+    if (d == 0) return empty_rows(codes ? scale : nullptr, rstd, mean, rows, eps, stream);
+    if (!x || !weight || !y) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!stride_ok(ldx, d) || (residual && !stride_ok(ldr, d))) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!aligned(x, x_dtype) || !aligned(residual, x_dtype) || !aligned(h, x_dtype) || !aligned(weight, w_dtype) ||
+        !aligned(bias, w_dtype) || (!codes && !aligned(y, y_dtype)) || !aligned(scale, GEMM_BT_F32) || !aligned(mean, GEMM_BT_F32) ||
+        !aligned(rstd, GEMM_BT_F32))
+        return GEMM_BT_ERR_INVALID_VALUE;
+    NormArgs a = {x, residual, weight, y, h, scale, rstd, rows, ldx, ldr, (int)d, eps, y_dtype, bias, mean};
+    return launch_norm<true>(a, x_dtype, w_dtype, stream);
 }
 
 int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int64_t rows, int64_t d, int x_dtype,
@@ -930,63 +1221,34 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
     if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
     if (rows == 0) return GEMM_BT_OK;
     if (!scale) return GEMM_BT_ERR_INVALID_VALUE;
-    if (d == 0) return empty_rows(scale, nullptr, rows, 0.0f, stream);
+    if (d == 0) return empty_rows(scale, nullptr, nullptr, rows, 0.0f, stream);
     if (!x || !q || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
     if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
-    NormArgs a = {x, nullptr, nullptr, q, nullptr, scale, nullptr, rows, ldx, 0, (int)d, 0.0f, q_dtype};
+    NormArgs a = {x, nullptr, nullptr, q, nullptr, scale, nullptr, rows, ldx, 0, (int)d, 0.0f, q_dtype, nullptr, nullptr};
     return launch_norm(a, x_dtype, x_dtype, stream);
 }
 
 int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) {
-    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
-    *bytes = 0;
-    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
-    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
-    // (the plans' grids do not depend on the types, nor on whole chunks)
-    if (norm_back_few<GEMM_BT_BF16, GEMM_BT_BF16, false>(rows, d).fn) return GEMM_BT_OK;
-    *bytes = (size_t)(norm_back_grid(norm_back_plan_of(GEMM_BT_BF16, GEMM_BT_BF16, d), rows, plan_cus()) * d * 4);
-    return GEMM_BT_OK;
+    return norm_back_workspace<false>(rows, d, bytes);
 }
 
 int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight,
                               const float* rstd, const void* dh, int64_t ld_dh, void* dx, void* dweight, int64_t rows,
                               int64_t d, int x_dtype, int w_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
-    if (!float_type(x_dtype) || !weight_type_ok(x_dtype, w_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (d == 0) return GEMM_BT_OK;
-    if (!dweight || !aligned(dweight, w_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
-    if (rows > 0) {
-        // (the few-rows kernel's sums for dweight read dy and h while dx is written)
-        if (!dy || !h || !weight || !rstd || !dx || dx == dy || dx == h) return GEMM_BT_ERR_INVALID_VALUE;
-        if (!stride_ok(ld_dy, d) || !stride_ok(ldh, d) || (dh && !stride_ok(ld_dh, d))) return GEMM_BT_ERR_INVALID_VALUE;
-        if (!aligned(dy, x_dtype) || !aligned(h, x_dtype) || !aligned(dh, x_dtype) || !aligned(dx, x_dtype) ||
-            !aligned(weight, w_dtype) || !aligned(rstd, GEMM_BT_F32) || !aligned(workspace, GEMM_BT_F32))
-            return GEMM_BT_ERR_INVALID_VALUE;
-    }
-    int num_cu = 0;
-    int st = check_device(&num_cu);
-    if (st != GEMM_BT_OK) return st;
-    int64_t grid = 0;
-    if (rows > 0) {
-        const RowPlan few = with_types(
-            x_dtype, w_dtype, d, [&](auto x, auto w, auto r) { return norm_back_few<x(), w(), r()>(rows, d); });
-        if (few.fn) {
-            NormBackArgs a = {dy, h, weight, rstd, dh, dx, nullptr, rows, ld_dy, ldh, ld_dh, (int)d, 0};
-            int row_blocks = (int)((rows + few.rows_per_block - 1) / few.rows_per_block);
-            void* args[] = {&a, &row_blocks, &dweight};
-            return launch(few.fn, dim3((unsigned)(row_blocks + (d + 63) / 64)), few.threads, args, stream);
-        }
-        const RowPlan p = norm_back_plan_of(x_dtype, w_dtype, d);
-        grid = norm_back_grid(p, rows, num_cu);
-        if (!workspace || workspace_bytes < (size_t)(grid * d * 4)) return GEMM_BT_ERR_INVALID_VALUE;
-        NormBackArgs a = {dy, h, weight, rstd, dh, dx, (float*)workspace, rows, ld_dy, ldh, ld_dh, (int)d,
-                          whole_chunks(dy, ld_dy, x_dtype) && whole_chunks(h, ldh, x_dtype) && whole_chunks(dh, ld_dh, x_dtype)};
-        void* args[] = {&a};
-        st = launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
-        if (st != GEMM_BT_OK) return st;
-    }
-    return fold((const float*)workspace, dweight, w_dtype, grid, d, stream);
+    NormBackArgs a = {dy, h, weight, rstd, dh, dx, nullptr, rows, ld_dy, ldh, ld_dh, 0, nullptr, nullptr, 0};
+    return norm_backward<false>(a, d, dweight, nullptr, x_dtype, w_dtype, workspace, workspace_bytes, stream);
+}
+
+int gemm_bt_layer_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) {
+    return norm_back_workspace<true>(rows, d, bytes);
+}
+
+int gemm_bt_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight, const float* mean,
+                                const float* rstd, const void* dh, int64_t ld_dh, void* dx, void* dweight, void* dbias,
+                                int64_t rows, int64_t d, int x_dtype, int w_dtype, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    NormBackArgs a = {dy, h, weight, rstd, dh, dx, nullptr, rows, ld_dy, ldh, ld_dh, 0, mean, nullptr, 0};
+    return norm_backward<true>(a, d, dweight, dbias, x_dtype, w_dtype, workspace, workspace_bytes, stream);
 }
 
 int gemm_bt_act_backward_workspace(int64_t rows, int64_t n, size_t* bytes) {

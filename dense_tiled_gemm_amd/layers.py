@@ -45,6 +45,22 @@ class Normed(NamedTuple):
     rstd: Optional[torch.Tensor]    # fp32, one per row
 
 
+class LayerNormed(NamedTuple):
+    """What add_layer_norm returns; None for what was not asked for."""
+
+    y: torch.Tensor                 # the normalised rows
+    scale: Optional[torch.Tensor]   # fp32, one per row, of 8-bit rows
+    h: Optional[torch.Tensor]       # x + residual
+    mean: Optional[torch.Tensor]    # fp32, one per row
+    rstd: Optional[torch.Tensor]    # fp32, one per row
+
+
+class LayerNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: Optional[torch.Tensor]
+
+
 class Quantized(NamedTuple):
     q: torch.Tensor
     scale: torch.Tensor
@@ -180,6 +196,7 @@ def _workspace_query(name):
 
 _epi_bytes = _workspace_query("gemm_bt_epi_workspace_size")
 _norm_back_bytes = _workspace_query("gemm_bt_rms_norm_backward_workspace")
+_layer_norm_back_bytes = _workspace_query("gemm_bt_layer_norm_backward_workspace")
 _linear_back_bytes = _workspace_query("gemm_bt_linear_backward_workspace")
 
 
@@ -281,6 +298,96 @@ def add_rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     if st:
         raise GemmBtError(st, "gemm_bt_rms_norm_backward")
     return dx, dw
+
+
+def _affine(t, x, what):
+    """A norm's weight or bias: (d,) of x's type or float32, contiguous."""
+    if t.shape != x.shape[-1:]:
+        raise ValueError("%s must have the shape of the last dimension, got %s and %s" % (what, tuple(t.shape), tuple(x.shape)))
+    if t.dtype != x.dtype and t.dtype != torch.float32:
+        raise TypeError("%s must be %s or float32, got %s" % (what, x.dtype, t.dtype))
+    return _dense(t)
+
+
+def add_layer_norm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None, save_stats=False, out=None, h_out=None,
+                   stream=None):
+    """h = x + residual; y = (h - mean(h)) / sqrt(mean((h - mean(h))²) + eps) * weight + bias, over the last dimension.
+
+    x: float32, float16 or bfloat16; residual: as x, or None; weight and bias: (d,) of x's type or float32, both of one
+    type, bias None for none.  ``out_dtype``, ``out`` and ``h_out`` as for add_rms_norm.  Returns LayerNormed(y, scale, h,
+    mean, rstd): scale for 8-bit rows, h where a residual is given, mean and rstd with ``save_stats``.  h is used unrounded
+    and returned rounded to x's type.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, lambda: add_layer_norm(x, weight, bias, residual, eps, out_dtype, save_stats, out, h_out))
+    device = _on_gpu(x, weight, bias, residual)
+    dtype, shape = x.dtype, x.shape
+    x_code = _float_code(dtype, "x")
+    xr, ldx, rows, d = _rows(x, "x")
+    weight = _affine(weight, x, "weight")
+    if bias is not None:
+        bias = _affine(bias, x, "bias")
+        if bias.dtype != weight.dtype:
+            raise TypeError("weight and bias must share one dtype, got %s and %s" % (weight.dtype, bias.dtype))
+    y_dtype = dtype if out_dtype is None else out_dtype
+    y_code = _CODES.get(y_dtype)
+    if y_code is None or y_code == FP8_E5M2:
+        raise TypeError("out_dtype must be a float type, float8_e4m3fn or int8, got %s" % y_dtype)
+    y = _output(out, xr, shape, y_dtype)
+    scale = x.new_empty(shape[:-1], dtype=torch.float32) if y_code in _EIGHT else None
+    mean = rstd = None
+    if save_stats:
+        mean, rstd = (x.new_empty(shape[:-1], dtype=torch.float32) for _ in range(2))
+    rr, ldr, h = None, 0, None
+    if residual is not None:
+        _same(residual, x, "residual")
+        rr, ldr, _, _ = _rows(residual, "residual")
+        h = _output(h_out, xr, shape, dtype, "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual: without one h is x itself")
+    with _on(device):
+        st = load().gemm_bt_layer_norm(xr.data_ptr(), ldx, _ptr(rr), ldr, weight.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(h),
+                                       _ptr(scale), _ptr(mean), _ptr(rstd), rows, d, eps, x_code, _CODES[weight.dtype], y_code,
+                                       _stream(device.index))
+    if st:
+        raise GemmBtError(st, "gemm_bt_layer_norm")
+    return LayerNormed(y, scale, h, mean, rstd)
+
+
+def add_layer_norm_backward(dy, h, weight, mean, rstd, dh=None, bias_grad=True, stream=None):
+    """LayerNormGrads(dx, dweight, dbias) of add_layer_norm: h, mean and rstd as it returned them (h is x where there was no
+    residual), dy the gradient of y, dh the gradient that reaches h from elsewhere.  dx is the gradient of x and of residual
+    alike; dbias, of weight's type, is None without ``bias_grad``."""
+    if stream is not None:
+        return _on_stream(stream, dy, lambda: add_layer_norm_backward(dy, h, weight, mean, rstd, dh, bias_grad))
+    device = _on_gpu(dy, h, weight, mean, rstd, dh)
+    dtype, shape = dy.dtype, dy.shape
+    code = _float_code(dtype, "dy")
+    _same(h, dy, "h")
+    dyr, ld_dy, rows, d = _rows(dy, "dy")
+    weight = _affine(weight, dy, "weight")
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or t.shape != shape[:-1]:
+            raise ValueError("%s must be a float32 tensor of shape %s" % (what, tuple(shape[:-1])))
+    hr, ldh, _, _ = _rows(h, "h")
+    dhr, ld_dh = None, 0
+    if dh is not None:
+        _same(dh, dy, "dh")
+        dhr, ld_dh, _, _ = _rows(dh, "dh")
+    mean, rstd = _dense(mean), _dense(rstd)
+    dx = _output(None, dyr, shape, dtype)
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(weight) if bias_grad else None
+    with _on(device):
+        s = _stream(device.index)
+        need = _layer_norm_back_bytes(rows, d, device.index)
+        ws = dyr.new_empty(need, dtype=torch.uint8) if need else None
+        st = load().gemm_bt_layer_norm_backward(dyr.data_ptr(), ld_dy, hr.data_ptr(), ldh, weight.data_ptr(), mean.data_ptr(),
+                                                rstd.data_ptr(), _ptr(dhr), ld_dh, dx.data_ptr(), dw.data_ptr(), _ptr(db), rows, d,
+                                                code, _CODES[weight.dtype], _ptr(ws), need, s)
+    if st:
+        raise GemmBtError(st, "gemm_bt_layer_norm_backward")
+    return LayerNormGrads(dx, dw, db)
 
 
 # ---------------------------------------------------------------- the product with its epilogue

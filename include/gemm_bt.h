@@ -324,6 +324,38 @@ int gemm_bt_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int6
 int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
 
 /*
+ * Layer norm with the residual's addition:
+ *   h = x + residual        (h = x where residual is NULL)
+ *   mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *   y = (h - mean) * rstd * weight + bias
+ * As gemm_bt_rms_norm in everything else: types, strides, 8-bit y with one
+ * scale per row, what may be what.  The squares are those of h - mean (never
+ * mean(h^2) - mean^2), and the mean's own rounding is taken out of h - mean.
+ * A row with an infinity or a NaN, or whose h - mean leaves fp32's range, is NaN.
+ *   bias   d elements of w_dtype, or NULL
+ *   mean   rows fp32, or NULL: receives mean for the backward pass
+ * A row of no elements has mean 0.
+ */
+int gemm_bt_layer_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                       const void* bias, void* y, void* h, float* scale, float* mean, float* rstd, int64_t rows,
+                       int64_t d, float eps, int x_dtype, int w_dtype, int y_dtype, void* stream);
+
+/*
+ * Layer norm's backward pass.  With xhat = (h - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dh
+ *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy
+ * As gemm_bt_rms_norm_backward in everything else.
+ *   mean, rstd  as gemm_bt_layer_norm left them
+ *   dbias       d elements of w_dtype, or NULL: not wanted
+ *   workspace   at least gemm_bt_layer_norm_backward_workspace bytes
+ */
+int gemm_bt_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ldh, const void* weight,
+                                const float* mean, const float* rstd, const void* dh, int64_t ld_dh, void* dx,
+                                void* dweight, void* dbias, int64_t rows, int64_t d, int x_dtype, int w_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+int gemm_bt_layer_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
+
+/*
  * The backward pass of gemm_bt_epi's activation and bias:
  *   dz = dy * act'(preact),   dbias = sum over rows of dz
  * (gemm_bt_linear_backward is this with the gradients of A and B).
