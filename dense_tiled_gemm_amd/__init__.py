@@ -24,7 +24,8 @@ and torch convenience wrappers ``mm_bt(a, b, out_dtype)`` (2-D or batched 3-D op
 product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_backward, gemm_bt_act_backward,
 gemm_bt_linear_backward) are called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
 ``add_rms_norm_backward`` and ``quantize_rows``; the layer norm's (gemm_bt_layer_norm and its backward pass) are
-``add_layer_norm`` and ``add_layer_norm_backward``.  They need torch and are imported when first used.
+``add_layer_norm`` and ``add_layer_norm_backward``, the gated product's (gemm_bt_gated and its backward pass)
+``gated_linear`` and ``gated_linear_backward``.  They need torch and are imported when first used.
 """
 from __future__ import annotations
 
@@ -46,7 +47,8 @@ EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layo
            "gemm_bt_rms_norm_backward_workspace", "gemm_bt_quantize_rows", "gemm_bt_act_backward",
            "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace",
            "gemm_bt_epi_workspace_size", "gemm_bt_plan_epi", "gemm_bt_layer_norm", "gemm_bt_layer_norm_backward",
-           "gemm_bt_layer_norm_backward_workspace")
+           "gemm_bt_layer_norm_backward_workspace", "gemm_bt_gated", "gemm_bt_gated_workspace_size",
+           "gemm_bt_gated_backward", "gemm_bt_gated_backward_workspace")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -130,7 +132,12 @@ def load():
             lib.gemm_bt_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, ci, ci, ci, vp]
             lib.gemm_bt_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64, i64, ci, ci, vp, sz, vp]
             lib.gemm_bt_layer_norm_backward_workspace.argtypes = [i64, i64, szp]
-            for f in (lib.gemm_bt_layer_norm, lib.gemm_bt_layer_norm_backward, lib.gemm_bt_layer_norm_backward_workspace,
+            lib.gemm_bt_gated.argtypes = lib.gemm_bt_epi.argtypes
+            lib.gemm_bt_gated_workspace_size.argtypes = lib.gemm_bt_epi_workspace_size.argtypes
+            lib.gemm_bt_gated_backward.argtypes = lib.gemm_bt_linear_backward.argtypes
+            lib.gemm_bt_gated_backward_workspace.argtypes = lib.gemm_bt_linear_backward_workspace.argtypes
+            for f in (lib.gemm_bt_gated, lib.gemm_bt_gated_workspace_size, lib.gemm_bt_gated_backward,
+                      lib.gemm_bt_gated_backward_workspace, lib.gemm_bt_layer_norm, lib.gemm_bt_layer_norm_backward, lib.gemm_bt_layer_norm_backward_workspace,
                       lib.gemm_bt_epi, lib.gemm_bt_epi_workspace_size, lib.gemm_bt_plan_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
                       lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
                       lib.gemm_bt_act_backward_workspace, lib.gemm_bt_linear_backward,
@@ -447,7 +454,7 @@ def mm(a, b, out_dtype=None, out=None, stream=None):
 
 
 _LAYERS = ("linear", "linear_backward", "add_rms_norm", "add_rms_norm_backward", "quantize_rows", "add_layer_norm",
-           "add_layer_norm_backward")
+           "add_layer_norm_backward", "gated_linear", "gated_linear_backward")
 
 
 def __getattr__(name):

@@ -174,7 +174,11 @@ struct SkArgs {
     float* partials;     // one slot of BM * BN floats per workgroup
 };
 // EPI = 1: the same kernel with an epilogue (epilogue.hpp) between the sums
-// and C; its arguments travel with the split's.
+// and C; its arguments travel with the split's.  EPI = 2: the gated epilogue.  B
+// has 2 N rows, and a tile of BN rows of B holds rows n0 .. n0 + BN / 2 - 1 of its
+// first half and the same rows of its second half, so both products of an
+// output are finished by one workgroup and meet in its LDS; everything up to the
+// sums is the product with 2 N columns.
 struct SkEpiArgs : SkArgs {
     EpiArgs epi;
 };
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                                                           int tiles_m, int tiles_n, int group_m,
                                                           int vec_store, int item_tiles_m, long long sa, long long sb,
                                                           long long sc,
-                                                          const std::conditional_t<EPI, SkEpiArgs, SkArgs> sk) {
+                                                          const std::conditional_t<(EPI != 0), SkEpiArgs, SkArgs> sk) {
     constexpr int W = WM * WN;
     constexpr int ESZ = in_size(IN);     // bytes per input element (2, or 1 for 8-bit floats)
     constexpr int EPC = 16 / ESZ;        // elements per 16-byte chunk
@@ -196,6 +200,9 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     constexpr int LA = BM / (RPI * W);   // A load instructions per wave per stage
     constexpr int LB = BN / (RPI * W);
     constexpr int TM = BM / WM, TN = BN / WN;
+    constexpr bool GATE = EPI == 2;
+    constexpr int BNR = GATE ? BN / 2 : BN;  // columns of C per tile
+    static_assert(!GATE || (SCHED >= 2 && BNR % RPI == 0 && WN % 2 == 0), "a load, and a wave, lies in one half of B");
     constexpr int FM = TM / MF, FN = TN / MF;
     // K per MFMA: 16-bit inputs 16 (32x32x16) or 32 (16x16x32); 8-bit inputs 64 (32x32x64)
     constexpr int KSUB = (512 / MF) * (ESZ == 2 ? 1 : 4);
@@ -297,11 +304,25 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     const int carry_a = PH ? (lchunk + phase(Ap, (int64_t)m0 + ld_row)) >> 3 : 0;
     const int carry_b = PH ? (lchunk + phase(Bp, (int64_t)n0 + ld_row)) >> 3 : 0;
     const int ph_fa = PH ? phase(Ap, (int64_t)m0 + wm * TM + fr) : 0;
-    const int ph_fb = PH ? phase(Bp, (int64_t)n0 + wn * TN + fr) : 0;
+    const int ph_fb = !PH ? 0
+                      : GATE && wn >= WN / 2 ? phase(Bp, (int64_t)N + n0 + wn * TN - BNR + fr)
+                                             : phase(Bp, (int64_t)n0 + wn * TN + fr);
+    const int carry_b2 = PH && GATE ? (lchunk + phase(Bp, (int64_t)N + n0 + ld_row)) >> 3 : 0;  // of B's second half
 
-    const int rows_a = min(BM, M - m0), rows_b = min(BN, N - n0);
+    const int rows_a = min(BM, M - m0), rows_b = min(BNR, N - n0);
     const i32x4 ra = rsrc_words((const unsigned char*)Ap + (size_t)m0 * row_bytes, (u32)rows_a * row_bytes);
     const i32x4 rb = rsrc_words((const unsigned char*)Bp + (size_t)n0 * row_bytes, (u32)rows_b * row_bytes);
+    const i32x4 rb2 = GATE ? rsrc_words((const unsigned char*)Bp + (size_t)(N + (int64_t)n0) * row_bytes, (u32)rows_b * row_bytes) : rb;
+    // whether load i of B (of `lw` waves) lies in its second half, whose rows start BNR tile rows on
+    auto second = [&](int i, int lw) {
+        constexpr int H = BNR / RPI;
+        return GATE && ((i + 1) * lw <= H ? false : (i * lw >= H ? true : wave + i * lw >= H));
+    };
+    auto load_rows_b = [&](unsigned char* dst, bool up, u32 off, u32 soff) {
+        // (2 BNR rows are less than 2^31 bytes: what was out of range stays so)
+        if (GATE && up) dma16(rb2, dst, off - (u32)BNR * row_bytes, soff);
+        else dma16(rb, dst, off, soff);
+    };
     // k < Ke: the whole chunks of this K range (loads past it come back as zeros)
     const int Ke = min(Kf, ke * BK);
     const bool with_tail = ESZ == 2 && Kf != K && ke == nk_all;
@@ -314,9 +335,11 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     if (with_tail) {
         const int r = threadIdx.x;
         const bool in_a = r < BM;
-        const bool valid = in_a ? r < rows_a : (r < BM + BN && r - BM < rows_b);
+        const bool up = GATE && r >= BM + BNR;
+        const bool valid = in_a ? r < rows_a : (r < BM + BN && r - BM - (up ? BNR : 0) < rows_b);
         if (valid) {
-            const u16* src = in_a ? Ap + (size_t)(m0 + r) * K + Kf : Bp + (size_t)(n0 + r - BM) * K + Kf;
+            const u16* src = in_a ? Ap + (size_t)(m0 + r) * K + Kf
+                                  : Bp + (size_t)(n0 + (int64_t)(r - BM) + (up ? (int64_t)N - BNR : 0)) * K + Kf;
             const int t = K - Kf;
 #pragma unroll
             for (int e = 0; e < 7; ++e)
@@ -473,14 +496,14 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             if constexpr (PH) {
                 // K segment (kb + kt - carry) of the lane's row; its full byte
                 // offset in the per-lane operand (none before the first segment)
-                const int carry = d < LAW ? carry_a : carry_b;
+                const int carry = d < LAW ? carry_a : (second(d - LAW, LW) ? carry_b2 : carry_b);
                 const int seg = kb + kt - carry;
                 const u32 base = l_off + (u32)(d < LAW ? d : d - LAW) * lw_stride;
                 const u32 off = seg >= 0 && seg * BK + l_kc < Ke ? base + (u32)seg * (u32)ROWB : kOutOfRange;
                 if (d < LAW)
                     dma16(ra, sbase + (wave + d * LW) * 1024, off, 0u);
                 else
-                    dma16(rb, sbase + BM * ROWB + (wave + (d - LAW) * LW) * 1024, off, 0u);
+                    load_rows_b(sbase + BM * ROWB + (wave + (d - LAW) * LW) * 1024, second(d - LAW, LW), off, 0u);
                 return;
             }
             const u32 kbytes = (u32)(kb + kt) * (u32)ROWB;
@@ -489,8 +512,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                 dma16(ra, sbase + (wave + d * LW) * 1024, l_kc < kleft ? l_off + (u32)d * lw_stride : kOutOfRange,
                       kbytes);
             else
-                dma16(rb, sbase + BM * ROWB + (wave + (d - LAW) * LW) * 1024,
-                      l_kc < kleft ? l_off + (u32)(d - LAW) * lw_stride : kOutOfRange, kbytes);
+                load_rows_b(sbase + BM * ROWB + (wave + (d - LAW) * LW) * 1024, second(d - LAW, LW),
+                            l_kc < kleft ? l_off + (u32)(d - LAW) * lw_stride : kOutOfRange, kbytes);
         };
         // fragment r of substep ks in consumption order: b0, a0 .. a[FM-1], b1 ..
         // (sta, stb: the A and B tiles)
@@ -561,8 +584,8 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         auto load_b = [&](int sl, int kt, int d) {
             if (!loader) return;
             const int kleft = Ke - (kb + kt) * BK;
-            dma16(rb, slot(sl) + (wave + d * LW) * 1024, l_kc < kleft ? l_off + (u32)d * lw_stride : kOutOfRange,
-                  (u32)(kb + kt) * (u32)ROWB);
+            load_rows_b(slot(sl) + (wave + d * LW) * 1024, second(d, LW),
+                        l_kc < kleft ? l_off + (u32)d * lw_stride : kOutOfRange, (u32)(kb + kt) * (u32)ROWB);
         };
         static_assert(SPREAD == 1 && FD == 1 && CH == LAW + LBW, "one refill burst per step");
         // RING5 == 2: A(kt + 2) goes out during the first substep of step kt
@@ -788,7 +811,11 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     auto store_c = [&](void* Cp, int m0, int n0, Acc& acc) {
         int tid_r = threadIdx.x;
         asm volatile("" : "+v"(tid_r));
-        if constexpr (EPI) {
+        if constexpr (GATE) {
+            barrier_no_fence();
+            store_tile_gated<IN == GEMM_BT_INT8, FN, FM, BM, BN, WM, 64 * W, STAGES * STAGE_BYTES, MF>(
+                acc, lds, Cp, M, N, m0, n0, wm * TM, wn * TN, wm, tid_r, sk.epi);
+        } else if constexpr (EPI != 0) {
             // every wave is past its last LDS read and its loads have landed
             barrier_no_fence();
             store_tile_epi<IN == GEMM_BT_INT8, FN, FM, BM, BN, WM, 64 * W, STAGES * STAGE_BYTES, MF>(
@@ -813,7 +840,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             tm64 -= (int64_t)z * item_tiles_m;
             batch_item(z, A, B, C, sa, sb, sc);
         }
-        const int m0 = (int)tm64 * BM, n0 = (int)tn64 * BN;
+        const int m0 = (int)tm64 * BM, n0 = (int)tn64 * BNR;
         Acc acc;
         zero(acc);
         run(A, B, m0, n0, 0, nk_all, acc);
@@ -883,7 +910,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         };
         int64_t tm, tn;
         band_coord(s, tiles_m, tiles_n, group_m, &tm, &tn);
-        const int m0 = uni((int)tm * BM), n0 = uni((int)tn * BN);
+        const int m0 = uni((int)tm * BM), n0 = uni((int)tn * BNR);
         Acc acc;
         zero(acc);
         run(A, B, m0, n0, kb, ke, acc);

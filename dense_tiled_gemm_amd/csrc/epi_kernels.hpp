@@ -6,15 +6,17 @@
 
 namespace gbt {
 
-// The twin of dma_variants()[variant] for inputs of in_dtype with an epilogue,
-// or of its split form; nullptr where there is none.  Any output type.
-const void* epi_dma_fn(int variant, int in_dtype, bool split);
+// The twin of dma_variants()[variant] for inputs of in_dtype with an epilogue
+// (the gated one), or of its split form; nullptr where there is none.  Any output
+// type.
+const void* epi_dma_fn(int variant, int in_dtype, bool split, bool gated);
 // The streaming kernel for M <= 16 (the first of skinny_variants()).
-const void* epi_skinny_fn(int in_dtype);
+const void* epi_skinny_fn(int in_dtype, bool gated);
 // K == 0: (void* C, int M, int N, EpiArgs), a grid of any size.
-const void* epi_fill_fn();
+const void* epi_fill_fn(bool gated);
 
-// The same epilogue for the rows from m1 on of a product with N columns.
+// The same epilogue for the rows from m1 on, N columns each (of the kept
+// pre-activation, where it is gated).
 inline EpiArgs epi_rows(EpiArgs e, int64_t m1, int64_t N) {
     if (e.row_scale) e.row_scale += m1;
     if (e.residual) e.residual = (const char*)e.residual + m1 * N * elem_size(epi_type(e.mode, EPI_RESIDUAL_TYPE));

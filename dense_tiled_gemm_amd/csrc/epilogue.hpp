@@ -392,6 +392,106 @@ __device__ __forceinline__ void store_tile_epi(const typename AccBlock<MF>::type
     }
 }
 
+// The gated epilogue: sums of the tile's first BN / 2 columns and of its second
+// ones belong to the same BN / 2 columns of C,
+//   Zg = row_scale[i] col_scale[j] sum + bias[j],  Zu the same with j + N,
+//   C[i][j] = act(Zg) Zu,
+// and preact holds rows of 2 N elements, Zg and then Zu.  As store_tile_epi in
+// everything else; both halves meet in LDS, so an output costs one pass.
+template <bool INT, int FN, int FM, int BM, int BN, int WM, int NT, int LDS_BYTES, int MF>
+__device__ __forceinline__ void store_tile_gated(const typename AccBlock<MF>::type (&acc)[FN][FM], unsigned char* lds, void* C,
+                                                 int M, int N, int m0, int n0, int mw, int nw, int wm, int tid, const EpiArgs& e) {
+    typedef AccBlock<MF> AB;
+    constexpr int ROWB = BN * 4, CPR = ROWB / 16;
+    constexpr int P = BM * ROWB <= LDS_BYTES ? 1 : WM;
+    constexpr int RP = BM / P;       // tile rows per pass
+    constexpr int GPR = BN / 16;     // groups of 8 columns of C per row
+    constexpr int IT = (RP * GPR + NT - 1) / NT;
+    constexpr bool FIXED = NT % GPR == 0;  // every group of a thread has the same columns
+    static_assert(CPR == 24 || (CPR >= 8 && (CPR & (CPR - 1)) == 0), "row chunks");
+    static_assert(RP * ROWB <= LDS_BYTES, "a pass must fit in LDS");
+    const int mlim = M - m0, nlim = N - n0;
+    const int lane = tid & 63;
+    auto mode = [&]() __attribute__((always_inline)) {
+        int m = e.mode;
+        asm volatile("" : "+s"(m));
+        return m;
+    };
+    float cs[2][8], cb[2][8];
+    auto columns = [&](int g) __attribute__((always_inline)) {
+        const int n = min(8, nlim - 8 * g), md = mode();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                cs[s][x] = 1.0f;
+                cb[s][x] = 0.0f;
+            }
+            if (n <= 0) continue;
+            const size_t j = (size_t)n0 + 8 * g + (s ? (size_t)N : 0);
+            if (md & EPI_COL_SCALE) decode8(load_raw8(e.col_scale, GEMM_BT_F32, j, n), GEMM_BT_F32, cs[s]);
+            if (md & EPI_BIAS) {
+                const int t = epi_type(md, EPI_BIAS_TYPE);
+                decode8(load_raw8(e.bias, t, j, n), t, cb[s]);
+            }
+        }
+    };
+    if constexpr (FIXED) columns(tid % GPR);
+#pragma unroll 1
+    for (int p = 0; p < P; ++p) {
+        if (P == 1 || wm == p) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const int r = (mw + MF * j + AB::row(lane)) % RP;  // tile row within the pass
+#pragma unroll
+                    for (int g = 0; g < AB::regs / 4; ++g) {
+                        const int c = (nw + MF * i + AB::col(lane, g)) / 4;
+                        float v[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float s = acc[i][j][4 * g + x];
+                            v[x] = INT ? (float)(int)as_u32(s) : s;
+                        }
+                        *(u32x4*)(lds + r * ROWB + epi_chunk(c, r, CPR) * 16) =
+                            u32x4{as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+                    }
+                }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int it = 0; it < IT; ++it) {
+            const int q = it * NT + renew(tid);
+            const int g = q % GPR, r = q / GPR, row = p * RP + r;
+            if (q < RP * GPR && row < mlim && 8 * g < nlim) {
+                if constexpr (!FIXED) columns(g);
+                const int n = min(8, nlim - 8 * g), md = mode();
+                const float rs = md & EPI_ROW_SCALE ? e.row_scale[(size_t)m0 + row] : 1.0f;
+                const size_t line = (size_t)(m0 + row) * N + n0 + 8 * g;  // in C
+                float z[2][8];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int c = 2 * (g + s * GPR);
+                    const u32x4 lo = *(const u32x4*)(lds + r * ROWB + epi_chunk(c, r, CPR) * 16);
+                    const u32x4 hi = *(const u32x4*)(lds + r * ROWB + epi_chunk(c + 1, r, CPR) * 16);
+                    decode8(Raw8{lo, hi}, GEMM_BT_F32, z[s]);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) z[s][x] = __builtin_fmaf(z[s][x] * rs, cs[s][x], cb[s][x]);
+                    if (md & EPI_PREACT)
+                        store8(e.preact, epi_type(md, EPI_PREACT_TYPE), line + (size_t)(m0 + row + s) * N, n, z[s]);
+                }
+                with_act(md >> EPI_ACT, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) z[0][x] = act_value<decltype(act)::value>(z[0][x]) * z[1][x];
+                });
+                store8(C, epi_type(md, EPI_OUT_TYPE), line, n, z[0]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // What an epilogue adds to outputs j .. j+n-1 (n in 0..4) of row i: fetched
 // ahead of the sums, so that its latency passes behind them.
 struct Epi4 {

@@ -1098,10 +1098,12 @@ static SkArgs sk_args(const gemm_bt_plan_t& p, int64_t K, void* ws) {
 
 // Every K-inner call: argument checks, the plan for the current device and
 // the launch.  `ws` (with `ws_bytes`) enables the stream-K plan; NULL plans
-// the data-parallel grid as gemm_bt does.
+// the data-parallel grid as gemm_bt does.  `gated`: B has 2 N rows, and the plan is
+// that of 2 N columns (its tiles_n and the streaming kernel's grid then count
+// blocks of half as many columns of C).
 static int launch_inner(const void* A, const void* B, void* C, int64_t batch, int64_t M, int64_t N, int64_t K,
                         int64_t stride_a, int64_t stride_b, int64_t stride_c, int in_dtype, int out_dtype, void* ws,
-                        size_t ws_bytes, void* stream, const EpiArgs* epi = nullptr) {
+                        size_t ws_bytes, void* stream, const EpiArgs* epi = nullptr, bool gated = false) {
     gemm_bt_plan_t p;
     if (stride_a < 0 || stride_b < 0 || stride_c < 0) return GEMM_BT_ERR_INVALID_VALUE;
     const bool multi = batch > 1;
@@ -1110,9 +1112,11 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
     const int a_al = item_align(A, batch, stride_a, isz), b_al = item_align(B, batch, stride_b, isz),
               c_al = item_align(C, batch, stride_c, osz);
     const bool allow_sk = ws != nullptr;
+    if (gated && N > 0x3FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
+    const int64_t Np = gated ? 2 * N : N;
     // Plan against the default CU count first: it validates the arguments
     // without touching the device.
-    int st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, 256, allow_sk, &p, epi != nullptr);
+    int st = plan_impl(batch, M, Np, K, in_dtype, out_dtype, a_al, b_al, c_al, 256, allow_sk, &p, epi != nullptr);
     if (st != GEMM_BT_OK) return st;
     if (p.kernel == KIND_NONE) return GEMM_BT_OK;
     st = check_items(A, B, C, p.kernel, batch, M, N, stride_a, stride_b, stride_c, isz, osz);
@@ -1122,7 +1126,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
     st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
     if (num_cu != 256) {
-        st = plan_impl(batch, M, N, K, in_dtype, out_dtype, a_al, b_al, c_al, num_cu, allow_sk, &p, epi != nullptr);
+        st = plan_impl(batch, M, Np, K, in_dtype, out_dtype, a_al, b_al, c_al, num_cu, allow_sk, &p, epi != nullptr);
         if (st != GEMM_BT_OK) return st;
     }
     if ((p.split_tiles > 0 || p.split_rows > 0 || p.split_items > 0) && p.workspace_bytes > 0 &&
@@ -1132,12 +1136,12 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         // two launches in stream order: rows [0, m1), then the rest (each
         // with its own plan; the second may use the workspace)
         const int64_t m1 = p.split_rows;
-        st = launch_inner(A, B, C, 1, m1, N, K, 0, 0, 0, in_dtype, out_dtype, ws, ws_bytes, stream, epi);
+        st = launch_inner(A, B, C, 1, m1, N, K, 0, 0, 0, in_dtype, out_dtype, ws, ws_bytes, stream, epi, gated);
         if (st != GEMM_BT_OK) return st;
         EpiArgs rest;
-        if (epi) rest = epi_rows(*epi, m1, N);
+        if (epi) rest = epi_rows(*epi, m1, Np);
         return launch_inner((const char*)A + m1 * K * isz, B, (char*)C + m1 * N * osz, 1, M - m1, N, K, 0, 0, 0,
-                            in_dtype, out_dtype, ws, ws_bytes, stream, epi ? &rest : nullptr);
+                            in_dtype, out_dtype, ws, ws_bytes, stream, epi ? &rest : nullptr, gated);
     }
     if (p.split_items > 0) {
         // items [0, z1), then the rest, in stream order (a stride of 0
@@ -1164,7 +1168,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         if (epi) {
             EpiArgs ea = *epi;
             void* eargs[] = {&C, &Mi, &Ni, &ea};
-            e = hipLaunchKernel(epi_fill_fn(), dim3((unsigned)p.grid), dim3(p.threads), eargs, 0, s);
+            e = hipLaunchKernel(epi_fill_fn(gated), dim3((unsigned)p.grid), dim3(p.threads), eargs, 0, s);
         } else
             e = hipLaunchKernel((const void*)&zero_fill_kernel, dim3((unsigned)p.grid, gy), dim3(p.threads), args, 0, s);
     } else {
@@ -1177,7 +1181,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         if (vec_store && (N * osz) % 16 == 0 && c_al >= 16) vec_store = 2;
         if (p.kernel == KIND_DMA) {
             int n = 0;
-            const void* fn = epi ? epi_dma_fn(p.variant, in_dtype, p.split_tiles > 0)
+            const void* fn = epi ? epi_dma_fn(p.variant, in_dtype, p.split_tiles > 0, gated)
                              : p.split_tiles > 0 ? sk_fn(p.variant, in_dtype, out_dtype)
                                                  : dma_variants(&n)[p.variant].fn[in_index(in_dtype)][out_index(out_dtype)];
             if (!fn) return GEMM_BT_ERR_UNSUPPORTED;  // no kernel of this plan in this build
@@ -1200,7 +1204,7 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         } else {
             const void* fn = nullptr;
             if (epi) {
-                fn = epi_skinny_fn(in_dtype);
+                fn = epi_skinny_fn(in_dtype, gated);
             } else if (p.variant >= 1) {
                 int n = 0;
                 fn = skinny_variants(&n)[p.variant - 1].fn[in_index(in_dtype)][out_index(out_dtype)];
@@ -1384,34 +1388,56 @@ int gemm_bt_epi_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, in
     return st;
 }
 
+// The arguments of an epilogue (NULL: none of its terms); false for ones that
+// are not valid.
+static bool epi_args(const gemm_bt_epilogue_t* epilogue, int out_dtype, EpiArgs* out) {
+    EpiArgs& e = *out;
+    e = {nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype << EPI_OUT_TYPE};
+    if (!epilogue) return true;
+    const gemm_bt_epilogue_t& g = *epilogue;
+    if (g.activation < GEMM_BT_ACT_NONE || g.activation > GEMM_BT_ACT_SILU) return false;
+    e.row_scale = g.row_scale;
+    e.col_scale = g.col_scale;
+    e.bias = g.bias;
+    e.residual = g.residual;
+    e.preact = g.preact;
+    e.mode |= g.activation << EPI_ACT;
+    // a term that is there: its bit and its type
+    auto term = [&](const void* ptr, int bit, int type, int shift) {
+        if (!ptr) return true;
+        if (!float_type(type) || (uintptr_t)ptr % elem_size(type)) return false;
+        e.mode |= bit | type << shift;
+        return true;
+    };
+    static_assert(GEMM_BT_F32 == 0, "the scales' type adds no bits");
+    return term(g.row_scale, EPI_ROW_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) &&
+           term(g.col_scale, EPI_COL_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) &&
+           term(g.bias, EPI_BIAS, g.bias_dtype, EPI_BIAS_TYPE) &&
+           term(g.residual, EPI_RESIDUAL, g.residual_dtype, EPI_RESIDUAL_TYPE) &&
+           term(g.preact, EPI_PREACT, g.preact_dtype, EPI_PREACT_TYPE);
+}
+
+int gemm_bt_gated_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    if (N > 0x3FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
+    return gemm_bt_epi_workspace_size(M, 2 * N, K, in_dtype, out_dtype, bytes);
+}
+
+int gemm_bt_gated(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype,
+                  const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    EpiArgs e;
+    if (!epi_args(epilogue, out_dtype, &e) || e.residual) return GEMM_BT_ERR_INVALID_VALUE;
+    return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, epi_plan_type(in_dtype, out_dtype), workspace, workspace_bytes, stream,
+                        &e, true);
+}
+
 int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype,
                 const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream) {
     if (!float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
-    EpiArgs e = {nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype << EPI_OUT_TYPE};
-    if (epilogue) {
-        const gemm_bt_epilogue_t& g = *epilogue;
-        if (g.activation < GEMM_BT_ACT_NONE || g.activation > GEMM_BT_ACT_SILU) return GEMM_BT_ERR_INVALID_VALUE;
-        e.row_scale = g.row_scale;
-        e.col_scale = g.col_scale;
-        e.bias = g.bias;
-        e.residual = g.residual;
-        e.preact = g.preact;
-        e.mode |= g.activation << EPI_ACT;
-        // a term that is there: its bit and its type
-        auto term = [&](const void* ptr, int bit, int type, int shift) {
-            if (!ptr) return true;
-            if (!float_type(type) || (uintptr_t)ptr % elem_size(type)) return false;
-            e.mode |= bit | type << shift;
-            return true;
-        };
-        if (!term(g.row_scale, EPI_ROW_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) ||
-            !term(g.col_scale, EPI_COL_SCALE, GEMM_BT_F32, EPI_BIAS_TYPE) ||
-            !term(g.bias, EPI_BIAS, g.bias_dtype, EPI_BIAS_TYPE) ||
-            !term(g.residual, EPI_RESIDUAL, g.residual_dtype, EPI_RESIDUAL_TYPE) ||
-            !term(g.preact, EPI_PREACT, g.preact_dtype, EPI_PREACT_TYPE))
-            return GEMM_BT_ERR_INVALID_VALUE;
-    }
-    static_assert(GEMM_BT_F32 == 0, "the scales' type adds no bits");
+    EpiArgs e;
+    if (!epi_args(epilogue, out_dtype, &e)) return GEMM_BT_ERR_INVALID_VALUE;
     // nothing to do to the sums of a 16-bit product that is planned as the plain
     // one: its kernel (4096^3 bf16 94 us, through the epilogue 102)
     if (e.mode == out_dtype << EPI_OUT_TYPE && (in_dtype == GEMM_BT_BF16 || in_dtype == GEMM_BT_F16)) {

@@ -12,6 +12,8 @@
 // lie in memory: the tiles of one fill the compute units that the other leaves
 // idle, the last block of each column of db is folded by a few more
 // workgroups, and a backward pass costs two launches.
+// The gated product's backward pass is the same with 2 N columns, a pass of its own
+// making dz.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -190,7 +192,7 @@ constexpr BackTile kBackTiles[] = {{128, 128, 0.60, 0.69}, {128, 256, 1.05, 1.15
 // 55.8, 62.0; 8192x1024x4096 167.7, 159.8, 152.9; 4096^3 302.6, 284.1, 236.8.
 // The longer runs first, instead of dW always: 2048x4096x4096 147.8 -> 129.5,
 // 1024x4096x4096 92.4 -> 79.8, 528x1728x7040 50.8 -> 45.8.
-static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu) {
+static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, bool gated, int num_cu) {
     BackPlan p = {};
     p.make_dz = act || N % 8 != 0;
     p.pad = K % 8 != 0;
@@ -225,7 +227,7 @@ static BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool act, int num_cu)
         p.pieces_x = pieces_x;
         p.per_x = per_x;
     }
-    p.sums_parts = M > 0 && N > 0 ? act_back_parts(M, N, num_cu) : 0;
+    p.sums_parts = M > 0 && N > 0 ? (gated ? gated_back_parts(M, N / 2, num_cu) : act_back_parts(M, N, num_cu)) : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -259,16 +261,17 @@ static int fill_zero(void* out, int64_t n, void* stream) {
 }
 
 static int linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
-                           int64_t M, int64_t N, int64_t K, int act, int type, int preact_type, char* ws, const BackPlan& p,
-                           int num_cu, void* stream) {
+                           int64_t M, int64_t N, int64_t K, int act, bool gated, int type, int preact_type, char* ws,
+                           const BackPlan& p, int num_cu, void* stream) {
     int st;
     // dz, and the partial sums of its columns
     const void* dz = dy;
     if (p.make_dz || dbias) {
         if (p.make_dz) dz = ws + p.off_dz;
-        st = launch_act_back({dy, act != GEMM_BT_ACT_NONE ? preact : nullptr, p.make_dz && (dx || dw) ? (void*)dz : nullptr,
-                              dbias ? (float*)(ws + p.off_sums) : nullptr, M, (int)N, (int)p.ldz, 0, type, preact_type, act},
-                             num_cu, stream);
+        const ActBackArgs a = {dy, gated || act != GEMM_BT_ACT_NONE ? preact : nullptr, p.make_dz && (dx || dw) ? (void*)dz : nullptr,
+                               dbias ? (float*)(ws + p.off_sums) : nullptr, M, (int)(gated ? N / 2 : N), (int)p.ldz, 0, type,
+                               preact_type, act};
+        st = gated ? launch_gated_back(a, num_cu, stream) : launch_act_back(a, num_cu, stream);
         if (st != GEMM_BT_OK) return st;
     }
     if (p.pad && (dx || dw)) {
@@ -350,28 +353,25 @@ static int linear_backward(const void* dy, const void* x, const void* w, const v
                   stream);
 }
 
-}  // namespace gbt
-
-using namespace gbt;
-
-extern "C" {
-
-int gemm_bt_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes) {
+// The workspace of a pass, N columns of dz.
+static int back_workspace(int64_t M, int64_t N, int64_t K, int activation, bool gated, size_t* bytes) {
     if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
     *bytes = 0;
     if (M < 0 || N < 0 || K < 0 || activation < GEMM_BT_ACT_NONE || activation > GEMM_BT_ACT_SILU)
         return GEMM_BT_ERR_INVALID_VALUE;
     if (!sizes_ok(M, N, K)) return GEMM_BT_ERR_UNSUPPORTED;
-    if (M > 0 && N > 0) *bytes = (size_t)back_plan(M, N, K, activation != GEMM_BT_ACT_NONE, plan_cus()).bytes;
+    if (M > 0 && N > 0)
+        *bytes = (size_t)back_plan(M, N, K, gated || activation != GEMM_BT_ACT_NONE, gated, plan_cus()).bytes;
     return GEMM_BT_OK;
 }
 
-int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
-                            int64_t M, int64_t N, int64_t K, int activation, int dtype, int preact_dtype, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+// Checks and launches, N columns of dz (gated: dy has half as many).
+static int backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias, int64_t M,
+                    int64_t N, int64_t K, int activation, bool gated, int dtype, int preact_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream) {
     if (M < 0 || N < 0 || K < 0 || activation < GEMM_BT_ACT_NONE || activation > GEMM_BT_ACT_SILU)
         return GEMM_BT_ERR_INVALID_VALUE;
-    const bool act = activation != GEMM_BT_ACT_NONE;
+    const bool act = gated || activation != GEMM_BT_ACT_NONE;
     if ((dtype != GEMM_BT_F16 && dtype != GEMM_BT_BF16) || (act && !float_type(preact_dtype))) return GEMM_BT_ERR_UNSUPPORTED;
     if (!sizes_ok(M, N, K)) return GEMM_BT_ERR_UNSUPPORTED;
     if (K == 0) dx = dw = nullptr;  // nothing to write
@@ -394,15 +394,46 @@ int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const 
         if (st == GEMM_BT_OK && dbias) st = fill_zero(dbias, N, stream);
         return st;
     }
-    const BackPlan p = back_plan(M, N, K, act, num_cu);
+    const BackPlan p = back_plan(M, N, K, act, gated, num_cu);
     if (p.bytes > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < (size_t)p.bytes))
         return GEMM_BT_ERR_INVALID_VALUE;
     // the products read whole 16-byte chunks of their operands where they lie
     auto chunks = [](const void* q) { return (uintptr_t)q % 16 == 0; };
     if ((dx || dw) && ((!p.make_dz && !chunks(dy)) || (!p.pad && ((dw && !chunks(x)) || (dx && !chunks(w))))))
         return GEMM_BT_ERR_UNSUPPORTED;
-    return linear_backward(dy, x, w, preact, dx, dw, dbias, M, N, K, activation, dtype, preact_dtype,
-                           (char*)workspace, p, num_cu, stream);
+    return linear_backward(dy, x, w, preact, dx, dw, dbias, M, N, K, activation, gated, dtype, preact_dtype, (char*)workspace, p,
+                           num_cu, stream);
+}
+
+}  // namespace gbt
+
+using namespace gbt;
+
+extern "C" {
+
+int gemm_bt_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes) {
+    return back_workspace(M, N, K, activation, false, bytes);
+}
+
+int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
+                            int64_t M, int64_t N, int64_t K, int activation, int dtype, int preact_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    return backward(dy, x, w, preact, dx, dw, dbias, M, N, K, activation, false, dtype, preact_dtype, workspace, workspace_bytes,
+                    stream);
+}
+
+int gemm_bt_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes) {
+    if (bytes) *bytes = 0;
+    if (N > 0x3FFFFFFF) return bytes ? GEMM_BT_ERR_UNSUPPORTED : GEMM_BT_ERR_INVALID_VALUE;
+    return back_workspace(M, 2 * N, K, activation, true, bytes);
+}
+
+int gemm_bt_gated_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw, void* dbias,
+                           int64_t M, int64_t N, int64_t K, int activation, int dtype, int preact_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    if (N > 0x3FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
+    return backward(dy, x, w, preact, dx, dw, dbias, M, 2 * N, K, activation, true, dtype, preact_dtype, workspace, workspace_bytes,
+                    stream);
 }
 
 }  // extern "C"

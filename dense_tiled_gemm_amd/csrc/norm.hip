@@ -920,6 +920,105 @@ __global__ __launch_bounds__(256) void act_back_kernel(const ActBackArgs a) {
     }
 }
 
+// act(z) and act'(z), which share their exponential.
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& value, float& slope) {
+    if constexpr (ACT == GEMM_BT_ACT_GELU) {
+        float gauss;
+        const float p = normal_cdf(z, gauss);
+        value = z * p;
+        slope = __builtin_fmaf(z * 0.3989422804014327f, gauss, p);
+    } else if constexpr (ACT == GEMM_BT_ACT_SILU) {
+        const float p = sigmoid_f(z);
+        value = z * p;
+        slope = p * __builtin_fmaf(z, 1.0f - p, 1.0f);
+    } else {
+        value = act_value<ACT>(z);
+        slope = act_slope<ACT>(z);
+    }
+}
+
+// Bound by HBM: reads dy and both halves of z, writes both halves of dz.  Layout
+// as in act_back_kernel, two rows in flight (each is three chunks).
+template <int L, bool RAGGED>
+__global__ __launch_bounds__(256) void gated_back_kernel(const ActBackArgs a) {
+    constexpr int G = 256 / L;
+    __shared__ float joined[2][G][L * 8];
+    const int l = threadIdx.x % L, g = threadIdx.x / L;
+    const int n = a.n, j = (blockIdx.x * L + l) * 8;
+    float sum[2][8];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[s][e] = 0.0f;
+    const long long first = (long long)blockIdx.y * a.rows_per_block;
+    const long long last = min(a.rows, first + a.rows_per_block);
+    if (j < n)
+        with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+            struct Row {
+                Raw8 dy, gate, up;
+            };
+            auto load = [&](long long row, Row& r) __attribute__((always_inline)) {
+                r.dy = load_chunk<RAGGED>(a.dy, a.type, row * n, j, n, a.nt);
+                r.gate = load_chunk<RAGGED>(a.preact, a.preact_type, row * 2 * n, j, n, a.nt);
+                r.up = load_chunk<RAGGED>(a.preact, a.preact_type, (row * 2 + 1) * n, j, n, a.nt);
+            };
+            auto one = [&](const Row& r, long long row) __attribute__((always_inline)) {
+                float dy[8], dg[8], du[8];
+                decode_chunk<RAGGED>(r.dy, a.type, j, n, dy);
+                decode_chunk<RAGGED>(r.gate, a.preact_type, j, n, dg);
+                decode_chunk<RAGGED>(r.up, a.preact_type, j, n, du);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float value, slope;
+                    act_both<ACT>(dg[e], value, slope);
+                    dg[e] = dy[e] * du[e] * slope;
+                    du[e] = dy[e] * value;
+                    sum[0][e] += dg[e];
+                    sum[1][e] += du[e];
+                }
+                if (a.dz) {
+                    const size_t at = (size_t)(row * a.ldz) + j;
+                    store8(a.dz, a.type, at, min(8, n - j), dg);
+                    store8(a.dz, a.type, at + n, min(8, a.ldz - n - j), du);  // with zeros behind the row, up to ldz:
+                    if (j + 8 >= n)  // at most 3 more, past the last chunk (n = 5, 6 or 7 mod 8)
+                        for (int c = n + j + 8; c < a.ldz; ++c) store1(a.dz, a.type, (size_t)(row * a.ldz) + c, 0.0f);
+                }
+            };
+            Row r[2];
+            long long row = first + g;
+            static_for<0, 2>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                if (row + u * G < last) load(row + u * G, r[u]);
+            });
+            for (; row < last; row += 2 * G)
+                static_for<0, 2>([&](auto uc) __attribute__((always_inline)) {
+                    constexpr int u = decltype(uc)::value;
+                    if (row + u * G < last) {
+                        one(r[u], row + u * G);
+                        if (row + (u + 2) * G < last) load(row + (u + 2) * G, r[u]);
+                    }
+                });
+        });
+    if (!a.partials) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) joined[s][g][l * 8 + e] = sum[s][e];
+    __syncthreads();
+    float* p = a.partials + (size_t)blockIdx.y * 2 * n;
+    for (int c = threadIdx.x; c < 2 * L * 8; c += 256) {
+        const int s = c / (L * 8), k = c % (L * 8);
+        const long long col = (long long)blockIdx.x * L * 8 + k;
+        if (col >= n) continue;
+        float v = joined[s][0][k];
+#pragma unroll
+        for (int i = 1; i < G; ++i) v += joined[s][i][k];
+        p[s * (long long)n + col] = v;
+    }
+}
+
 // ---- host ------------------------------------------------------------------------
 
 // One thread per 16 columns and row group of the fold, in a grid of at most 2^32
@@ -1059,13 +1158,14 @@ struct ActBackPlan {
     int64_t strips, blocks;
     int rows_per_block;
 };
-static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu) {
+static ActBackPlan act_back_plan(int64_t rows, int64_t n, int num_cu, bool gated = false) {
     ActBackPlan p;
     int lanes = 64;
     const bool r = ragged(n);
     auto kernel = [&](auto l) {
         lanes = l();
-        p.fn = r ? (const void*)&act_back_kernel<l(), true> : (const void*)&act_back_kernel<l(), false>;
+        if (gated) p.fn = r ? (const void*)&gated_back_kernel<l(), true> : (const void*)&gated_back_kernel<l(), false>;
+        else p.fn = r ? (const void*)&act_back_kernel<l(), true> : (const void*)&act_back_kernel<l(), false>;
     };
     if (n <= 64) kernel(std::integral_constant<int, 8>{});
     else if (n <= 128) kernel(std::integral_constant<int, 16>{});
@@ -1167,6 +1267,16 @@ static int norm_backward(NormBackArgs a, int64_t d, void* dweight, void* dbias, 
     FoldArgs fw = {(const float*)workspace, dweight, d, (int)grid, w_dtype}, fb = {fw.partials + grid * d, dbias, d, (int)grid, w_dtype};
     void* args[] = {&fw, &fb};
     return launch((const void*)&fold2_kernel, dim3(fold_blocks(d), 2), 512, args, stream);
+}
+
+int64_t gated_back_parts(int64_t rows, int64_t n, int num_cu) { return act_back_plan(rows, n, num_cu, true).blocks; }
+
+int launch_gated_back(ActBackArgs a, int num_cu, void* stream) {
+    const ActBackPlan p = act_back_plan(a.rows, a.n, num_cu, true);
+    a.rows_per_block = p.rows_per_block;
+    a.nt = whole_chunks(a.dy, a.n, a.type) && whole_chunks(a.preact, a.n, a.preact_type);
+    void* args[] = {&a};
+    return launch(p.fn, dim3((unsigned)p.strips, (unsigned)p.blocks), 256, args, stream);
 }
 
 }  // namespace gbt

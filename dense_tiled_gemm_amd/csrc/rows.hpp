@@ -64,6 +64,13 @@ struct ActBackArgs {
 int64_t act_back_parts(int64_t rows, int64_t n, int num_cu);
 int launch_act_back(ActBackArgs a, int num_cu, void* stream);
 
+// The same for a gated pair: z has rows of 2 n elements, the gate's and then the
+// other factor's, and so has dz (pitch ldz >= 2 n):
+//   dz[:n] = dy z[n:] act'(z[:n]),  dz[n:] = dy act(z[:n]);
+// partials hold rows of 2 n sums.
+int64_t gated_back_parts(int64_t rows, int64_t n, int num_cu);
+int launch_gated_back(ActBackArgs a, int num_cu, void* stream);
+
 // ---- host helpers ----------------------------------------------------------------
 
 inline int launch(const void* fn, dim3 grid, int threads, void** args, void* stream) {

@@ -64,9 +64,15 @@ __device__ __forceinline__ f32x4 skinny_mma(u32x4 b, u32x4 a, f32x4 c) {
     }
 }
 
-// The kernel's body.  `epi` is the epilogue's arguments (EpiArgs), or nothing
-// (SkinnyPlain): then the sums are rounded into C as they are.
+// The kernel's body.  `epi` is the epilogue's arguments (EpiArgs, or SkinnyGated
+// for the gated one), or nothing (SkinnyPlain): then the sums are rounded into C
+// as they are.  Gated: the BN rows of B are BN / 2 of its first N rows and the same
+// of its second N rows, so a lane finds the other product of its outputs 16 lanes
+// on.
 struct SkinnyPlain {};
+struct SkinnyGated {
+    EpiArgs e;
+};
 template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT, class Epi>
 __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
                                             int M, int N, int K, int vec_store, const Epi& epi) {
@@ -101,10 +107,14 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * BN;
-    const int rows_a = min(AR, M), rows_b = min(BN, N - n0);
+    constexpr bool GATE = std::is_same_v<Epi, SkinnyGated>;
+    constexpr int BNR = GATE ? BN / 2 : BN;  // columns of C per workgroup
+    static_assert(!GATE || (BN == 8 && BNR % RPI == 0), "4 columns, and a load lies in one half of B");
+    const int n0 = blockIdx.x * BNR;
+    const int rows_a = min(AR, M), rows_b = min(BNR, N - n0);
     const i32x4 ra = rsrc_words(A, (u32)rows_a * (u32)K * (u32)ESZ);
     const i32x4 rb = rsrc_words((const unsigned char*)B + (size_t)n0 * K * ESZ, (u32)rows_b * (u32)K * (u32)ESZ);
+    const i32x4 rb2 = GATE ? rsrc_words((const unsigned char*)B + (size_t)(N + (int64_t)n0) * K * ESZ, (u32)rows_b * (u32)K * (u32)ESZ) : rb;
     const u32 row_bytes = (u32)K * (u32)ESZ;
 
     // Loads: stage rows 0..15 hold A, rows 16..16+BN-1 hold B.  Load
@@ -114,17 +124,19 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     const int lrow = lane / CPR, lphys = lane % CPR;
     u32 off[LOADS];
     int kc[LOADS];
-    bool is_a[LOADS];
+    bool is_a[LOADS], is_up[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int j = wave + i * W;
         const int srow = j * RPI + lrow;  // stage row
         const int c = lphys ^ (srow & 15);
         const bool a = srow < AR;
-        const int grow = a ? srow : srow - AR;  // row within A or within this block of B
+        const bool up = GATE && srow >= AR + BNR;
+        const int grow = a ? srow : srow - AR - (up ? BNR : 0);  // row within A or within this block of B
         off[i] = (u32)grow * row_bytes + (u32)c * 16u;
         kc[i] = c * EPC;
         is_a[i] = a;
+        is_up[i] = up;
     }
     const int Kf = K & ~(EPC - 1);  // whole 16-byte chunks: through the LDS DMA (8-bit inputs: all of K)
     const int nk = (Kf + KB - 1) / KB;
@@ -144,6 +156,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
             // B is read exactly once: non-temporal; A is re-read by every
             // workgroup and should stay in L2
             if (is_a[i]) dma16<false>(ra, sbase + j * 1024, o, kbytes);
+            else if (GATE && is_up[i]) dma16<true>(rb2, sbase + j * 1024, o, kbytes);
             else dma16<true>(rb, sbase + j * 1024, o, kbytes);
         }
     };
@@ -170,16 +183,19 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
 #pragma unroll
         for (int b = 0; b < NBLK; ++b) {
             const int br = 16 * b + (r16 % BR);  // B row of the operand's row r16 within this block
-            if (br < rows_b) tb[b] = fetch(B + (size_t)(n0 + br) * K + Kf);
+            const bool up = GATE && br >= BNR;
+            if (br - (up ? BNR : 0) < rows_b) tb[b] = fetch(B + (size_t)(n0 + (int64_t)br + (up ? (int64_t)N - BNR : 0)) * K + Kf);
         }
     }
     // with an epilogue: what it adds to this lane's outputs, columns n0 + 4 q ..
     // of row lane % 16 (the first block of B rows is the only one there is)
     constexpr bool EPI = !std::is_same_v<Epi, SkinnyPlain>;
     static_assert(!EPI || (NBLK == 1 && W == 1), "one wave stores 4 outputs per lane");
-    const int epi_n = EPI && r16 < M && 4 * q < BN ? min(4, N - n0 - 4 * q) : 0;
+    // (gated: lanes 16 .. 31 hold the second products of lanes 0 .. 15, with terms of their own)
+    const int epi_n = !EPI || r16 >= M || 4 * q >= BN ? 0 : GATE ? min(4, N - n0) : min(4, N - n0 - 4 * q);
     Epi4 terms;
-    if constexpr (EPI) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi);
+    if constexpr (GATE) terms = load_epi4(N, r16, n0 + (q == 1 ? N : 0), epi_n, epi.e);
+    else if constexpr (EPI) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi);
 
     f32x4 acc[NBLK];
 #pragma unroll
@@ -227,7 +243,23 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
             const float x = acc[0][e];
             v[e] = IN == GEMM_BT_INT8 ? (float)(int)as_u32(x) : x;
         }
-        if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi);
+        if constexpr (GATE) {
+            const int md = epi.e.mode;
+            float up[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e] * terms.rs, terms.cs[e], terms.cb[e]);
+            if (epi_n > 0 && (md & EPI_PREACT))
+                store4(epi.e.preact, epi_type(md, EPI_PREACT_TYPE), (size_t)(2 * r16 + q) * N + n0, epi_n, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) up[e] = __shfl(v[e], (lane + 16) & 63);
+            with_act(md >> EPI_ACT, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(act)::value>(v[e]) * up[e];
+            });
+            if (epi_n > 0 && q == 0) store4(C, epi_type(md, EPI_OUT_TYPE), (size_t)r16 * N + n0, epi_n, v);
+        } else {
+            if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi);
+        }
         return;
     }
 #pragma unroll
@@ -289,6 +321,14 @@ __global__ __launch_bounds__(64 * W) void skinny_epi_kernel(const u16* __restric
                                                            void* __restrict__ C, int M, int N, int K,
                                                            const EpiArgs epi) {
     skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, epi);  // (OUT is not used)
+}
+
+// The gated epilogue.
+template <int IN, int BN, int KB, int STAGES, int W>
+__global__ __launch_bounds__(64 * W) void skinny_gated_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
+                                                             void* __restrict__ C, int M, int N, int K,
+                                                             const EpiArgs epi) {
+    skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, SkinnyGated{epi});  // (OUT is not used)
 }
 
 }  // namespace gbt

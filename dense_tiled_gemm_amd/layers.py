@@ -198,6 +198,8 @@ _epi_bytes = _workspace_query("gemm_bt_epi_workspace_size")
 _norm_back_bytes = _workspace_query("gemm_bt_rms_norm_backward_workspace")
 _layer_norm_back_bytes = _workspace_query("gemm_bt_layer_norm_backward_workspace")
 _linear_back_bytes = _workspace_query("gemm_bt_linear_backward_workspace")
+_gated_bytes = _workspace_query("gemm_bt_gated_workspace_size")
+_gated_back_bytes = _workspace_query("gemm_bt_gated_backward_workspace")
 
 
 # ---------------------------------------------------------------- norm and quantisation
@@ -498,4 +500,104 @@ def linear_backward(dy, x, weight, preact=None, activation="none", bias_grad=Tru
                                             _ptr(dx), _ptr(dw), _ptr(db), M, N, K, act, code, z_code, _ptr(ws), need, s)
     if st:
         raise GemmBtError(st, "gemm_bt_linear_backward")
+    return LinearGrads(dx, dw, db)
+
+
+# ---------------------------------------------------------------- the gated product
+
+def gated_linear(x, weight, bias=None, activation="silu", x_scale=None, weight_scale=None, out_dtype=None, save_preact=False,
+                 out=None, stream=None):
+    """act(x @ weight[:N].T + bias[:N]) * (x @ weight[N:].T + bias[N:]) in one kernel: the gated projection of a
+    feed-forward block.
+
+    x (..., K) and weight (2 N, K), the gate's rows and then the other factor's, of one input type as for linear; bias,
+    weight_scale (2 N,) and x_scale (...) as for linear.  The result is (..., N) of ``out_dtype`` (the default is x's type,
+    bfloat16 for 8-bit inputs); ``out``, contiguous, receives it.  Everything between the products and the result is held
+    in fp32.  With ``save_preact`` returns (y, z), z (..., 2 N) both products with their scales and bias (x's type,
+    bfloat16 for 8-bit inputs), for gated_linear_backward.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, lambda: gated_linear(x, weight, bias, activation, x_scale, weight_scale, out_dtype, save_preact, out))
+    device = _on_gpu(x, weight, bias, x_scale, weight_scale)
+    dtype = x.dtype
+    in_code = _CODES.get(dtype)
+    if in_code is None or in_code == F32:
+        raise TypeError("unsupported input dtype %s" % dtype)
+    if weight.dtype != dtype:
+        raise TypeError("x and weight must share one dtype")
+    x_shape, w_shape = x.shape, weight.shape
+    if len(w_shape) != 2 or w_shape[0] % 2 or x_shape[-1:] != w_shape[1:]:
+        raise ValueError("expected x (..., K) and weight (2 N, K), got %s and %s" % (tuple(x_shape), tuple(w_shape)))
+    e = Epilogue()
+    e.activation = _activation(activation)
+    N, K = w_shape[0] // 2, w_shape[1]
+    lead = x_shape[:-1]
+    M = lead.numel()
+    sixteen = in_code == BF16 or in_code == F16
+    wide = dtype if sixteen else torch.bfloat16
+    y_dtype = wide if out_dtype is None else out_dtype
+    out_code = _float_code(y_dtype, "out_dtype")
+    x, weight = (_dense(x), _dense(weight)) if sixteen else (_chunked(x), _chunked(weight))
+    if bias is not None:
+        bias = _term(bias, w_shape[:1], "bias")
+        e.bias, e.bias_dtype = bias.data_ptr(), _float_code(bias.dtype, "bias")
+    if x_scale is not None:
+        x_scale = _term(x_scale, lead, "x_scale", torch.float32)
+        e.row_scale = x_scale.data_ptr()
+    if weight_scale is not None:
+        weight_scale = _term(weight_scale, w_shape[:1], "weight_scale", torch.float32)
+        e.col_scale = weight_scale.data_ptr()
+    y = _output(out, x, lead + (N,), y_dtype)
+    z = None
+    if save_preact:
+        z = x.new_empty(lead + w_shape[:1], dtype=wide)
+        e.preact, e.preact_dtype = z.data_ptr(), _CODES[wide]
+    with _on(device):
+        s = _stream(device.index)
+        need = _gated_bytes(M, N, K, in_code, out_code, device.index)
+        ws, ws_bytes = None, 0  # (as for linear)
+        if need:
+            t = workspace_for(device, s, need)
+            ws, ws_bytes = t.data_ptr(), t.numel()
+        st = load().gemm_bt_gated(x.data_ptr(), weight.data_ptr(), y.data_ptr(), M, N, K, in_code, out_code, ctypes.byref(e), ws,
+                                  ws_bytes, s)
+    if st:
+        raise GemmBtError(st, "gemm_bt_gated")
+    return (y, z) if save_preact else y
+
+
+def gated_linear_backward(dy, x, weight, preact, activation="silu", bias_grad=True, need_dx=True, need_dweight=True, stream=None):
+    """The gradients of gated_linear's x, weight and bias for 16-bit x and weight: LinearGrads(dx, dweight, dbias).
+
+    dy (..., N): the gradient of the result, of x's type; preact (..., 2 N): what gated_linear returned with save_preact.
+    All three are of x's type, a float32 bias's too.  relu's slope at 0 is 0.
+    """
+    if stream is not None:
+        return _on_stream(stream, dy, lambda: gated_linear_backward(dy, x, weight, preact, activation, bias_grad, need_dx, need_dweight))
+    device = _on_gpu(dy, x, weight, preact)
+    dtype = x.dtype
+    if dtype not in (torch.bfloat16, torch.float16) or weight.dtype != dtype or dy.dtype != dtype:
+        raise TypeError("dy, x and weight must share float16 or bfloat16")
+    act = _activation(activation)
+    x_shape, w_shape = x.shape, weight.shape
+    if len(w_shape) != 2 or w_shape[0] % 2 or x_shape[-1:] != w_shape[1:] or dy.shape != x_shape[:-1] + (w_shape[0] // 2,):
+        raise ValueError("expected dy (..., N), x (..., K) and weight (2 N, K), got %s, %s and %s"
+                         % (tuple(dy.shape), tuple(x_shape), tuple(w_shape)))
+    if preact.shape != x_shape[:-1] + w_shape[:1]:
+        raise ValueError("preact must be the pre-activation that gated_linear returned, of shape %s" % (tuple(x_shape[:-1] + w_shape[:1]),))
+    z_code = _float_code(preact.dtype, "preact")
+    N, K = w_shape[0] // 2, w_shape[1]
+    M = x_shape[:-1].numel()
+    dy, preact, x, weight = _dense(dy), _dense(preact), _chunked(x), _chunked(weight)
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = weight.new_empty(2 * N) if bias_grad else None
+    with _on(device):
+        s = _stream(device.index)
+        need = _gated_back_bytes(M, N, K, act, device.index)
+        ws = dy.new_empty(need, dtype=torch.uint8) if need else None
+        st = load().gemm_bt_gated_backward(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), preact.data_ptr(), _ptr(dx), _ptr(dw),
+                                           _ptr(db), M, N, K, act, _CODES[dtype], z_code, _ptr(ws), need, s)
+    if st:
+        raise GemmBtError(st, "gemm_bt_gated_backward")
     return LinearGrads(dx, dw, db)

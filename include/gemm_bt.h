@@ -395,6 +395,39 @@ int gemm_bt_linear_backward(const void* dy, const void* x, const void* w, const 
                             int preact_dtype, void* workspace, size_t workspace_bytes, void* stream);
 int gemm_bt_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes);
 
+/*
+ * The gated product of a feed-forward block, both projections and what follows
+ * them in one kernel.  B has 2 N rows: the gate's N, then the other factor's.
+ *   Zg[i][j] = row_scale[i] * col_scale[j] * sum_k A[i][k] B[j][k] + bias[j]
+ *   Zu[i][j] = row_scale[i] * col_scale[N + j] * sum_k A[i][k] B[N + j][k] + bias[N + j]
+ *   C[i][j] = act(Zg[i][j]) * Zu[i][j]
+ * As gemm_bt_epi in everything else: inputs of 16 or 8 bits, float results, Z and
+ * everything after it in fp32, rounded once.
+ *   C         M x N of out_dtype
+ *   epilogue  col_scale and bias have 2 N elements, preact M x 2 N (receives Zg
+ *             and Zu, row by row); residual must be NULL (else INVALID_VALUE)
+ *   workspace as for gemm_bt_epi, of gemm_bt_gated_workspace_size bytes
+ * The plan is that of gemm_bt_epi with 2 N columns, whose limits apply to 2 N.
+ */
+int gemm_bt_gated(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,
+                  int out_dtype, const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes,
+                  void* stream);
+int gemm_bt_gated_workspace_size(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, size_t* bytes);
+
+/*
+ * Its backward pass for 16-bit X (M x K) and W (2 N x K), dy the gradient of C
+ * (M x N):
+ *   dz = [dy * Zu * act'(Zg), dy * act(Zg)] (M x 2 N), rounded into dtype
+ *   dx = dz W,   dw = dz^T X (2 N x K),   dbias = sums over rows of dz (2 N) before its rounding
+ * As gemm_bt_linear_backward with 2 N columns in everything else; preact (M x 2 N)
+ * is read for every activation, and dy needs the alignment of its elements only.
+ *   workspace  at least gemm_bt_gated_backward_workspace bytes, 16-byte aligned, any contents
+ */
+int gemm_bt_gated_backward(const void* dy, const void* x, const void* w, const void* preact, void* dx, void* dw,
+                           void* dbias, int64_t M, int64_t N, int64_t K, int activation, int dtype,
+                           int preact_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int gemm_bt_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes);
+
 /* Workspace gemm_bt_ws needs for these sizes and types (0 when it runs the
    plain grid), for the current device (256 compute units without one).  At
    most 16 KiB + 256 * 64 KiB (16.02 MiB) on an MI355X, whatever the
