@@ -25,7 +25,8 @@ product (gemm_bt_epi, gemm_bt_rms_norm, gemm_bt_quantize_rows, gemm_bt_rms_norm_
 gemm_bt_linear_backward) are called through the wrappers of ``layers``: ``linear``, ``linear_backward``, ``add_rms_norm``,
 ``add_rms_norm_backward`` and ``quantize_rows``; the layer norm's (gemm_bt_layer_norm and its backward pass) are
 ``add_layer_norm`` and ``add_layer_norm_backward``, the gated product's (gemm_bt_gated and its backward pass)
-``gated_linear`` and ``gated_linear_backward``.  They need torch and are imported when first used.
+``gated_linear`` and ``gated_linear_backward``, and 8-bit matrices with scales per block of 128 (gemm_bt_quantize_blocks,
+gemm_bt_block) ``quantize_blocks`` and ``block_linear``.  They need torch and are imported when first used.
 """
 from __future__ import annotations
 
@@ -48,7 +49,8 @@ EXPORTS = ("gemm_bt", "gemm_bt_batched", "gemm_bt_layout", "gemm_bt_batched_layo
            "gemm_bt_act_backward_workspace", "gemm_bt_linear_backward", "gemm_bt_linear_backward_workspace",
            "gemm_bt_epi_workspace_size", "gemm_bt_plan_epi", "gemm_bt_layer_norm", "gemm_bt_layer_norm_backward",
            "gemm_bt_layer_norm_backward_workspace", "gemm_bt_gated", "gemm_bt_gated_workspace_size",
-           "gemm_bt_gated_backward", "gemm_bt_gated_backward_workspace")
+           "gemm_bt_gated_backward", "gemm_bt_gated_backward_workspace", "gemm_bt_quantize_blocks", "gemm_bt_block",
+           "gemm_bt_block_workspace_size", "gemm_bt_plan_block")
 SK_COUNTER_BYTES = 16384  # leading counter area of a gemm_bt_ws workspace (zero between calls)
 
 _lock = threading.Lock()
@@ -136,7 +138,12 @@ def load():
             lib.gemm_bt_gated_workspace_size.argtypes = lib.gemm_bt_epi_workspace_size.argtypes
             lib.gemm_bt_gated_backward.argtypes = lib.gemm_bt_linear_backward.argtypes
             lib.gemm_bt_gated_backward_workspace.argtypes = lib.gemm_bt_linear_backward_workspace.argtypes
-            for f in (lib.gemm_bt_gated, lib.gemm_bt_gated_workspace_size, lib.gemm_bt_gated_backward,
+            lib.gemm_bt_quantize_blocks.argtypes = [vp, i64, vp, vp, i64, i64, ci, ci, ci, ci, vp]
+            lib.gemm_bt_block.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, ci, ci, ci, vp, vp, sz, vp]
+            lib.gemm_bt_block_workspace_size.argtypes = [i64, i64, i64, ci, szp]
+            lib.gemm_bt_plan_block.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(Plan)]
+            for f in (lib.gemm_bt_quantize_blocks, lib.gemm_bt_block, lib.gemm_bt_block_workspace_size, lib.gemm_bt_plan_block,
+                      lib.gemm_bt_gated, lib.gemm_bt_gated_workspace_size, lib.gemm_bt_gated_backward,
                       lib.gemm_bt_gated_backward_workspace, lib.gemm_bt_layer_norm, lib.gemm_bt_layer_norm_backward, lib.gemm_bt_layer_norm_backward_workspace,
                       lib.gemm_bt_epi, lib.gemm_bt_epi_workspace_size, lib.gemm_bt_plan_epi, lib.gemm_bt_rms_norm, lib.gemm_bt_quantize_rows, lib.gemm_bt_rms_norm_backward,
                       lib.gemm_bt_rms_norm_backward_workspace, lib.gemm_bt_act_backward,
@@ -255,6 +262,14 @@ def gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, a_align=256, b_align=256, c_a
     st = load().gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, a_align, b_align, c_align, ctypes.byref(p))
     if st != OK:
         raise GemmBtError(st, "gemm_bt_plan_epi")
+    return p
+
+
+def gemm_bt_plan_block(M, N, K, out_dtype, a_align=256, b_align=256):
+    p = Plan()
+    st = load().gemm_bt_plan_block(M, N, K, out_dtype, a_align, b_align, ctypes.byref(p))
+    if st != OK:
+        raise GemmBtError(st, "gemm_bt_plan_block")
     return p
 
 
@@ -454,7 +469,8 @@ def mm(a, b, out_dtype=None, out=None, stream=None):
 
 
 _LAYERS = ("linear", "linear_backward", "add_rms_norm", "add_rms_norm_backward", "quantize_rows", "add_layer_norm",
-           "add_layer_norm_backward", "gated_linear", "gated_linear_backward")
+           "add_layer_norm_backward", "gated_linear", "gated_linear_backward", "quantize_blocks",
+           "block_linear")
 
 
 def __getattr__(name):

@@ -118,10 +118,10 @@ __device__ inline void dma16(const i32x4& r, unsigned char* dst, u32 voff, u32 s
             : "memory", "m0");
     }
 }
-// 4 bytes per lane into LDS at m0 + 4 L: used only to pull cache lines into
-// L2 ahead of the 16-byte loads that will need them (the LDS bytes are not
-// read).
-__device__ inline void dma4_touch(const i32x4& r, unsigned char* dst, u32 voff, u32 soff) {
+// 4 bytes per lane into LDS at m0 + 4 L: the scales of a step's rows, and in the
+// tuning build loads that only pull cache lines into L2 ahead of the 16-byte ones
+// that will need them (the LDS bytes are not read).
+__device__ inline void dma4(const i32x4& r, unsigned char* dst, u32 voff, u32 soff) {
     const u32 m0 = (u32)(uintptr_t)(lds_ptr_t)dst;
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -182,15 +182,34 @@ struct SkArgs {
 struct SkEpiArgs : SkArgs {
     EpiArgs epi;
 };
+// BLK > 0 (8-bit floats, K steps of one block of 128, with an epilogue): A and B
+// carry one fp32 scale per block of 128 along K, sum = sum_b sa[i][b] sb[j][b]
+// sum_{k in b} a[i][k] b[j][k].  sb is per row of B (BLK = 2) or per 128 rows (BLK =
+// 1).  The matrix instructions of a block add up in registers of their own that
+// start from zero; while those of the next block's first half run, the sums are
+// multiplied by the block's scales and added to the tile's, 16 multiply-adds in
+// the shadow of an instruction of 64 cycles (BLK = 2: 32).  The scales of a K step
+// travel with its operands: one 4-byte load per wave brings those of its 64 rows
+// into LDS, whatever their strides are.
+struct BlockScales {
+    const float* s;
+    long long row, block;  // strides in floats
+};
+struct BlkArgs {
+    BlockScales a, b;
+};
+struct SkBlkArgs : SkEpiArgs {
+    BlkArgs blk;
+};
 
 template <int IN, int OUT, int BM, int BN, int BK, int STAGES, int WM, int WN, int SWZ, int SCHED = 0, int PF = 0,
-          int MF = 32, int LDW = 0, int RING5 = 0, int SK = 0, int PH = 0, int EPI = 0>
+          int MF = 32, int LDW = 0, int RING5 = 0, int SK = 0, int PH = 0, int EPI = 0, int BLK = 0>
 __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict__ A, const u16* __restrict__ B,
                                                           void* __restrict__ C, int M, int N, int K,
                                                           int tiles_m, int tiles_n, int group_m,
                                                           int vec_store, int item_tiles_m, long long sa, long long sb,
                                                           long long sc,
-                                                          const std::conditional_t<(EPI != 0), SkEpiArgs, SkArgs> sk) {
+                                                          const std::conditional_t<(BLK != 0), SkBlkArgs, std::conditional_t<(EPI != 0), SkEpiArgs, SkArgs>> sk) {
     constexpr int W = WM * WN;
     constexpr int ESZ = in_size(IN);     // bytes per input element (2, or 1 for 8-bit floats)
     constexpr int EPC = 16 / ESZ;        // elements per 16-byte chunk
@@ -231,7 +250,15 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                   "line ring: 16-bit inputs, 128-byte tile rows, an early-barrier ring of 3 or more stages, "
                   "every wave loading");
 
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[RING_BYTES + (PF > 0 ? W * 256 : 0)];
+    // BLK: behind the ring, a stage's scales (fp32, A's BM rows and then B's BN rows; a place per thread, since every
+    // wave issues the same number of loads)
+    constexpr int SCALE_BYTES = BLK ? 64 * W * 4 : 0;
+    static_assert(!BLK || (ESZ == 1 && BK == 128 && !RING5 && SCHED >= 2 && PF == 0 && !PH && LDW == 0 && EPI == 1 && BM % 64 == 0 &&
+                           BN % 64 == 0 && BM + BN <= 64 * W && TN <= 64 && RING_BYTES + STAGES * SCALE_BYTES <= 160 * 1024),
+                  "a K step is one block, a wave's scale load lies in one operand, a wave's columns in one block");
+    constexpr int XL = BLK ? 1 : 0;  // loads per wave and stage besides the tile's
+
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[RING_BYTES + STAGES * SCALE_BYTES + (PF > 0 ? W * 256 : 0)];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -381,9 +408,9 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             for (int p = 0; p < PFI; ++p) {
                 const int row = (wave * PFI + p) * 64 + lane;
                 if (row < BM)
-                    dma4_touch(ra, pbase, live ? (u32)row * row_bytes : kOutOfRange, kbytes);
+                    dma4(ra, pbase, live ? (u32)row * row_bytes : kOutOfRange, kbytes);
                 else
-                    dma4_touch(rb, pbase, live ? (u32)(row - BM) * row_bytes : kOutOfRange, kbytes);
+                    dma4(rb, pbase, live ? (u32)(row - BM) * row_bytes : kOutOfRange, kbytes);
             }
         }
     };
@@ -419,6 +446,28 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         for (int i = 0; i < FN; ++i) fb[i] = ld_frag(s + b_base + MF * ROWB * i, ks, ph_fb, nx);
 #pragma unroll
         for (int j = 0; j < FM; ++j) fa[j] = ld_frag(s + a_base + MF * ROWB * j, ks, ph_fa, nx);
+    };
+    // BLK: this wave's 64 rows of scales, of A or of B
+    [[maybe_unused]] u32 sc_off = kOutOfRange;
+    [[maybe_unused]] u32 sc_bytes = 0;
+    [[maybe_unused]] const float* sc_base = nullptr;
+    [[maybe_unused]] long long sc_step = 0;
+    if constexpr (BLK != 0) {
+        const bool of_a = wave * 64 < BM;
+        const int r = wave * 64 + lane_r - (of_a ? 0 : BM);  // tile row
+        const bool tall = BLK == 1 && !of_a;
+        const BlockScales s = of_a ? sk.blk.a : sk.blk.b;
+        const int first = of_a ? m0 : (tall ? n0 >> 7 : n0), rows = of_a ? rows_a : rows_b;
+        const int i = tall ? ((n0 + r) >> 7) - first : r, last = tall ? ((n0 + rows - 1) >> 7) - first : rows - 1;
+        sc_base = s.s + (long long)first * s.row + (long long)kb * s.block;
+        sc_step = s.block;
+        sc_bytes = wave * 64 < BM + BN ? ((u32)last * (u32)s.row + 1u) * 4u : 0u;
+        if (r < rows && wave * 64 < BM + BN) sc_off = (u32)i * (u32)s.row * 4u;
+    }
+    auto load_scales = [&](int stage, int kt) {
+        if constexpr (BLK != 0)
+            dma4(rsrc_words(sc_base + (long long)kt * sc_step, kb + kt < ke ? sc_bytes : 0u),
+                 lds + RING_BYTES + stage * SCALE_BYTES + wave * 256, sc_off, 0u);
     };
     auto mfma1 = [&](const Frag& b, const Frag& a, typename AB::type& c) {
         if constexpr (ESZ == 1) c = Mfma<IN>::m32x32x64(b, a, c);
@@ -492,6 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         // first), k >= K masked as in issue()
         auto load_one = [&](int stage, int kt, int d) {
             if (!loader) return;
+            if (BLK && d == 0) load_scales(stage, kt);
             unsigned char* sbase = lds + stage * STAGE_BYTES;
             if constexpr (PH) {
                 // K segment (kb + kt - carry) of the lane's row; its full byte
@@ -536,11 +586,66 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         // MFMA waits for the accumulator of the one just before it, and the
         // reads and loads follow every second one, at the same points in time.
         constexpr int NH = IN == GEMM_BT_INT8 ? 2 : 1;
-        auto mma_step = [&](const Frag (&b)[FN], const Frag (&a)[FM], bool do_load, auto&& load_d, auto&& read_r) {
+        // BLK: the sums of the block that is being read, and the scales of the one before until its sums are added
+        typename AB::type part[BLK ? FN : 1][BLK ? FM : 1];
+        float sa[BLK ? FM : 1], sb[BLK == 2 ? FN * AB::regs : 1];
+        if constexpr (BLK != 0) {
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                sa[j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int r = 0; r < AB::regs; ++r) part[i][j][r] = 0.0f;
+            }
+            if constexpr (BLK == 2)
+#pragma unroll
+                for (int r = 0; r < FN * AB::regs; ++r) sb[r] = 0.0f;
+        }
+        auto read_scales = [&](int stage) {
+            if constexpr (BLK != 0) {
+                const float* s = (const float*)(lds + RING_BYTES + stage * SCALE_BYTES);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) sa[j] = s[wm * TM + MF * j + fr];
+                if constexpr (BLK == 1) {
+                    const float b = s[BM + wn * TN];  // a wave's columns lie in one block
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) sa[j] *= b;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+#pragma unroll
+                        for (int g = 0; g < AB::regs / 4; ++g) {
+                            const f32x4 v = *(const f32x4*)(s + BM + wn * TN + MF * i + AB::col(lane_r, g));
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) sb[i * AB::regs + 4 * g + r] = v[r];
+                        }
+                }
+            }
+        };
+        // block (i, j) of the finished sums, scaled, into the tile's
+        auto add_block = [&](int i, int j) {
+            if constexpr (BLK != 0)
+#pragma unroll
+                for (int r = 0; r < AB::regs; ++r) {
+                    const float p = BLK == 1 ? part[i][j][r] : part[i][j][r] * sa[j];
+                    acc[i][j][r] = __builtin_fmaf(p, BLK == 1 ? sa[j] : sb[i * AB::regs + r], acc[i][j][r]);
+                }
+        };
+        auto mma_step = [&](const Frag (&b)[FN], const Frag (&a)[FM], bool do_load, auto&& load_d, auto&& read_r, auto first) {
             static_for<0, NMMA * NH>([&](auto uc) {
                 constexpr int u = decltype(uc)::value;
                 constexpr int t = u % NMMA;
-                if constexpr (NH == 1)
+                if constexpr (BLK != 0) {
+                    if constexpr (decltype(first)::value) {
+                        add_block(t / FM, t % FM);
+                        typename AB::type z;
+#pragma unroll
+                        for (int r = 0; r < AB::regs; ++r) z[r] = 0.0f;
+                        part[t / FM][t % FM] = z;
+                    }
+                    mfma1(b[t / FM], a[t % FM], part[t / FM][t % FM]);
+                } else if constexpr (NH == 1)
                     mfma1(b[t / FM], a[t % FM], acc[t / FM][t % FM]);
                 else
                     acc[t / FM][t % FM] = Mfma<IN>::template half<u / NMMA>(b[t / FM], a[t % FM], acc[t / FM][t % FM]);
@@ -563,10 +668,13 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         // chunk c of the refill of stage `stage` with tile kt, and with ILR
         // the reads of substep rks of stage rst into rfb/rfa
         auto mma_refill = [&](const Frag (&b)[FN], const Frag (&a)[FM], int stage, int kt, int c,
-                              const unsigned char* rst, int rks, Frag (&rfb)[FN], Frag (&rfa)[FM]) {
+                              const unsigned char* rst, int rks, Frag (&rfb)[FN], Frag (&rfa)[FM], auto first) {
             mma_step(b, a, c >= 0, [&](int d) { load_one(stage, kt, c * CH + d); },
-                     [&](auto rc) { read_one(rst, rst + BM * ROWB, rks, rc, rfb, rfa); });
+                     [&](auto rc) { read_one(rst, rst + BM * ROWB, rks, rc, rfb, rfa); }, first);
         };
+        constexpr auto kFirst = std::true_type{};
+        constexpr auto kLater = std::false_type{};
+        static_assert(!BLK || (KS == 2 && FD == 1), "one substep of a block before the barrier, one after it");
         if constexpr (RING5) {
         // Five slots of one operand tile each: A(j) sits in slot 2j mod 5 and
         // B(j) in slot 2j + 1 mod 5.  After the barrier of step kt the slots
@@ -610,7 +718,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             __builtin_amdgcn_sched_barrier(0);
             const int sp = sa == 0 ? 4 : sa - 1;  // slot of B(kt - 1), free since the last barrier
             mma_step(fb[0], fa[0], SPLIT, [&](int d) { if (d < LAW) load_a(sp, kt + 2, d); },
-                     [&](auto rc) { read_one(slot(sa), slot(sb), 1, rc, fb[1], fa[1]); });
+                     [&](auto rc) { read_one(slot(sa), slot(sb), 1, rc, fb[1], fa[1]); }, kLater);
             wait_vmcnt<LAW>();                   // A(kt + 1), B(kt + 1) have landed; A(kt + 2) may not
             __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): done reading A(kt), B(kt)
             barrier_no_fence();
@@ -625,7 +733,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                          if (d < LBW) load_b(sa, kt + 2, d);
                          else if (!SPLIT) load_a(sb, kt + 3, d - LBW);
                      },
-                     [&](auto rc) { read_one(slot(na), slot(nb), 0, rc, fb[0], fa[0]); });
+                     [&](auto rc) { read_one(slot(na), slot(nb), 0, rc, fb[0], fa[0]); }, kLater);
             __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);
             sa = na;
@@ -636,7 +744,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
 #pragma unroll
             for (int d = 0; d < L; ++d) load_one(s, s, d);
         // tile 0 has landed (PH: tiles 0 and 1, the lines K segment 0 spans)
-        wait_vmcnt<(STAGES - 2 - (PH ? 1 : 0)) * L>();
+        wait_vmcnt<(STAGES - 2 - (PH ? 1 : 0)) * (L + XL)>();
         barrier_no_fence();
 #pragma unroll
         for (int d = 0; d < CH * HEADC; ++d) load_one(STAGES - 1, STAGES - 1, d);  // head chunks of tile STAGES - 1
@@ -655,11 +763,12 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
                 if constexpr (!ILR) read_frags(s, ks + FD, fb[(ks + FD) % NSLOT], fa[(ks + FD) % NSLOT]);
                 __builtin_amdgcn_sched_barrier(0);
                 mma_refill(fb[ks % NSLOT], fa[ks % NSLOT], ps, kt + STAGES - 1, ks + FD < SPREAD ? ks + FD : -1,
-                           s, ks + FD, fb[(ks + FD) % NSLOT], fa[(ks + FD) % NSLOT]);
+                           s, ks + FD, fb[(ks + FD) % NSLOT], fa[(ks + FD) % NSLOT], kFirst);
             }
+            if constexpr (BLK != 0) read_scales(cs);
             // this wave's part of tile kt + 1 has landed (PH: of kt + 2 too,
             // the second line of K segment kt + 1)
-            wait_vmcnt<(STAGES - 2 - (PH ? 1 : 0)) * L>();
+            wait_vmcnt<(STAGES - 2 - (PH ? 1 : 0)) * (L + XL)>();
             __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): done reading stage cs
             barrier_no_fence();
             __builtin_amdgcn_sched_barrier(0);
@@ -670,7 +779,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
 #pragma unroll
             for (int j = 0; j < FD; ++j)  // head chunks of the refill of stage cs
                 mma_refill(fb[(KS - FD + j) % NSLOT], fa[(KS - FD + j) % NSLOT], cs, kt + STAGES, j < SPREAD ? j : -1,
-                           lds + ns * STAGE_BYTES, j, fb[j], fa[j]);
+                           lds + ns * STAGE_BYTES, j, fb[j], fa[j], kLater);
             // the next tile's first fragments arrived behind those MFMAs;
             // saying so here keeps the next iteration from waiting on the
             // reads it issues first
@@ -678,6 +787,9 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             ps = cs;
             cs = ns;
         }
+        // BLK: the last block's sums
+        if constexpr (BLK != 0)
+            static_for<0, NMMA>([&](auto tc) { add_block(decltype(tc)::value / FM, decltype(tc)::value % FM); });
         }
     } else if constexpr (SCHED == 1) {
         static_assert(W == 8 && WM == 2, "ping-pong pairs the two wave rows");

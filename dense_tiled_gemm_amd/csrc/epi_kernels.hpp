@@ -15,6 +15,17 @@ const void* epi_skinny_fn(int in_dtype, bool gated);
 // K == 0: (void* C, int M, int N, EpiArgs), a grid of any size.
 const void* epi_fill_fn(bool gated);
 
+// The 8-bit product with scales per block of 128: tiles of blockTile(i) with B's
+// scales per 128 rows (tall) or per row, their split form, and the streaming
+// kernel for M <= 16.
+constexpr int kBlockTiles = 3;
+struct BlockTile {
+    int bm, bn, threads;
+};
+constexpr BlockTile kBlockTile[kBlockTiles] = {{256, 128, 512}, {128, 128, 256}, {64, 64, 256}};
+const void* block_dma_fn(int tile, bool tall, bool split);
+const void* block_skinny_fn(bool tall);
+
 // The same epilogue for the rows from m1 on, N columns each (of the kept
 // pre-activation, where it is gated).
 inline EpiArgs epi_rows(EpiArgs e, int64_t m1, int64_t N) {

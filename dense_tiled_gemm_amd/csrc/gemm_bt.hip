@@ -1229,6 +1229,112 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
     return GEMM_BT_OK;
 }
 
+// ---- the product with scales per block of 128 ------------------------------------------
+
+// Plan: the streaming kernel for M <= 16 where its workgroups of 8 rows of B are
+// more than two per CU (as for 8-bit rows with an epilogue), else the tile shapes
+// of kBlockTile (`variant` is the index), the smallest cut along K where they leave
+// half the CUs idle.
+static int plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, int num_cu, bool allow_sk,
+                      gemm_bt_plan_t* p) {
+    std::memset(p, 0, sizeof(*p));
+    if (M < 0 || N < 0 || K < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    p->batch = 1;
+    if (!float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    // 32-bit buffer offsets inside one 256-row panel of A, B and C
+    if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || 256 * K >= 0x7FFFFFFFLL || 256 * N * (int64_t)out_size(out_dtype) >= 0x7FFFFFFFLL)
+        return GEMM_BT_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GEMM_BT_OK;  // KIND_NONE
+    p->threads = 256;
+    if (K == 0) {
+        p->kernel = KIND_FILL;
+        p->grid = std::min<int64_t>((M * N + 255) / 256, 4096);
+        return GEMM_BT_OK;
+    }
+    if (K % 16 != 0 || a_align % 16 != 0 || b_align % 16 != 0) return GEMM_BT_ERR_UNSUPPORTED;
+    if (M <= 16 && N > 16 * (int64_t)num_cu) {
+        p->kernel = KIND_SKINNY;
+        p->bm = 16;
+        p->bn = 8;
+        p->bk = 512;
+        p->stages = 3;
+        p->threads = 64;
+        p->tiles_m = 1;
+        p->tiles_n = p->grid = (N + 7) / 8;
+        return GEMM_BT_OK;
+    }
+    auto tiles = [&](int i) {
+        const BlockTile& t = kBlockTile[i];
+        return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    };
+    const int use = tiles(0) >= num_cu ? 0 : tiles(1) * 2 > num_cu ? 1 : 2;
+    const BlockTile& t = kBlockTile[use];
+    p->kernel = KIND_DMA;
+    p->variant = use;
+    p->bm = t.bm;
+    p->bn = t.bn;
+    p->bk = 128;
+    p->stages = use == 0 ? 3 : 4;
+    p->threads = t.threads;
+    p->group_m = kGroupM;
+    p->tiles_m = (M + t.bm - 1) / t.bm;
+    p->tiles_n = (N + t.bn - 1) / t.bn;
+    p->grid = p->tiles_m * p->tiles_n;
+    if (p->grid > 0x7FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
+    const int64_t T = p->grid, nk = (K + 127) / 128, S = std::min<int64_t>(num_cu / T, nk / 8);
+    if (allow_sk && use == 2 && T * 2 <= num_cu && S >= 2) {
+        p->grid = T * S;
+        p->split_tiles = T;
+        p->workspace_bytes = kSkCounterBytes + p->grid * (int64_t)t.bm * t.bn * 4;
+    }
+    return GEMM_BT_OK;
+}
+
+static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int out_dtype, const EpiArgs& epi,
+                        const BlkArgs& blk, bool tall, void* ws, size_t ws_bytes, void* stream) {
+    gemm_bt_plan_t p;
+    int st = plan_block(M, N, K, out_dtype, align_of(A), align_of(B), 256, ws != nullptr, &p);
+    if (st != GEMM_BT_OK) return st;
+    if (p.kernel == KIND_NONE) return GEMM_BT_OK;
+    if (!C || (uintptr_t)C % out_size(out_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (p.kernel != KIND_FILL) {
+        if (!A || !B || !blk.a.s || !blk.b.s || !aligned(blk.a.s, GEMM_BT_F32) || !aligned(blk.b.s, GEMM_BT_F32))
+            return GEMM_BT_ERR_INVALID_VALUE;
+        if (blk.a.row < 0 || blk.a.block < 0 || blk.b.row < 0 || blk.b.block < 0) return GEMM_BT_ERR_INVALID_VALUE;
+        // 32-bit offsets over a tile's rows and over a stage's blocks
+        if (std::max(blk.a.row, blk.b.row) >= 1 << 20 || std::max(blk.a.block, blk.b.block) >= 1 << 26) return GEMM_BT_ERR_UNSUPPORTED;
+    }
+    int num_cu = 256;
+    st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    if (num_cu != 256) {
+        st = plan_block(M, N, K, out_dtype, align_of(A), align_of(B), num_cu, ws != nullptr, &p);
+        if (st != GEMM_BT_OK) return st;
+    }
+    if (p.workspace_bytes > 0 && ((uintptr_t)ws % 16 != 0 || ws_bytes < (size_t)p.workspace_bytes)) return GEMM_BT_ERR_INVALID_VALUE;
+    const u16* a = (const u16*)A;
+    const u16* b = (const u16*)B;
+    int Mi = (int)M, Ni = (int)N, Ki = (int)K;
+    EpiArgs ea = epi;
+    if (p.kernel == KIND_FILL) {
+        void* args[] = {&C, &Mi, &Ni, &ea};
+        return launch(epi_fill_fn(false), dim3((unsigned)p.grid), p.threads, args, stream);
+    }
+    if (p.kernel == KIND_SKINNY) {
+        BlkArgs ba = blk;
+        void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &ea, &ba};
+        return launch(block_skinny_fn(tall), dim3((unsigned)p.grid), p.threads, args, stream);
+    }
+    SkBlkArgs s;
+    (SkArgs&)s = sk_args(p, K, ws);
+    s.epi = epi;
+    s.blk = blk;
+    int tm = (int)p.tiles_m, tn = (int)p.tiles_n, gm = p.group_m, vec_store = 0;
+    long long zero = 0;
+    void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &tm, &tn, &gm, &vec_store, &tm, &zero, &zero, &zero, &s};
+    return launch(block_dma_fn(p.variant, tall, p.split_tiles > 0), dim3((unsigned)p.grid), p.threads, args, stream);
+}
+
 }  // namespace gbt
 
 using namespace gbt;
@@ -1449,6 +1555,32 @@ int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int
             return gemm_bt_ws(A, B, C, M, N, K, in_dtype, out_dtype, workspace, workspace_bytes, stream);
     }
     return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, epi_plan_type(in_dtype, out_dtype), workspace, workspace_bytes, stream, &e);
+}
+
+int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int out_dtype, size_t* bytes) {
+    if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
+    *bytes = 0;
+    gemm_bt_plan_t p;
+    const int st = plan_block(M, N, K, out_dtype, 256, 256, plan_cus(), true, &p);
+    if (st == GEMM_BT_OK) *bytes = (size_t)p.workspace_bytes;
+    return st;
+}
+
+int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, gemm_bt_plan_t* plan) {
+    if (!plan) return GEMM_BT_ERR_INVALID_VALUE;
+    return plan_block(M, N, K, out_dtype, a_align, b_align, plan_cus(), true, plan);
+}
+
+int gemm_bt_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, const float* a_scale, int64_t a_row_stride,
+                  int64_t a_block_stride, const float* b_scale, int64_t b_row_stride, int64_t b_block_stride, int b_block_rows,
+                  int in_dtype, int out_dtype, const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+    if (in_dtype != GEMM_BT_FP8_E4M3 || !float_type(out_dtype)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (b_block_rows != 1 && b_block_rows != 128) return GEMM_BT_ERR_INVALID_VALUE;
+    EpiArgs e;
+    if (!epi_args(epilogue, out_dtype, &e)) return GEMM_BT_ERR_INVALID_VALUE;
+    const BlkArgs blk = {{a_scale, a_row_stride, a_block_stride}, {b_scale, b_row_stride, b_block_stride}};
+    return launch_block(A, B, C, M, N, K, out_dtype, e, blk, b_block_rows == 128, workspace, workspace_bytes, stream);
 }
 
 int gemm_bt_noalloc(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int in_dtype,

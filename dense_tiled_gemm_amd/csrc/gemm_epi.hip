@@ -89,6 +89,26 @@ const void* epi_skinny_fn(int in_dtype, bool gated) {
     }
 }
 
+template <int BM, int BN, int S, int WM, int WN, int SCHED, int SK, int BLK>
+static const void* block_fn() {
+    return (const void*)&dma_kernel<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BM, BN, 128, S, WM, WN, 2, SCHED, 0, 32, 0, 0, SK, 0, 1, BLK>;
+}
+template <int BLK>
+static const void* block_fn_of(int tile, bool split) {
+    if (split) return tile == 2 ? block_fn<64, 64, 4, 2, 2, 4, 1, BLK>() : nullptr;
+    switch (tile) {
+        case 0: return block_fn<256, 128, 3, 4, 2, 8, 0, BLK>();
+        case 1: return block_fn<128, 128, 4, 2, 2, 8, 0, BLK>();
+        default: return block_fn<64, 64, 4, 2, 2, 4, 0, BLK>();
+    }
+}
+const void* block_dma_fn(int tile, bool tall, bool split) {
+    return tall ? block_fn_of<1>(tile, split) : block_fn_of<2>(tile, split);
+}
+const void* block_skinny_fn(bool tall) {
+    return tall ? (const void*)&skinny_block_kernel<1, 8, 512, 3> : (const void*)&skinny_block_kernel<0, 8, 512, 3>;
+}
+
 // K == 0: the epilogue of empty sums.
 __global__ void epi_fill_kernel(void* C, int M, int N, const EpiArgs e) {
     const size_t n = (size_t)M * N, stride = (size_t)gridDim.x * blockDim.x;

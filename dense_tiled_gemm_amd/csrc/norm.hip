@@ -116,6 +116,7 @@ __device__ __forceinline__ void decode_chunk(const Raw8& r, int t, int i, int d,
 // ---- 8-bit codes ---------------------------------------------------------------
 
 typedef u32x2 u32x2_byte __attribute__((aligned(1)));
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 
 // Four values (|v| <= 448 or 127 up to rounding, or NaN) in 8 bits, to nearest even.
 template <int QT>
@@ -489,6 +490,146 @@ __global__ __launch_bounds__(256) void empty_rows_kernel(float* scale, float* rs
         if (scale) scale[row] = 0x1p-100f;
         if (rstd) rstd[row] = 1.0f / __builtin_sqrtf(eps);
         if (mean) mean[row] = 0.0f;
+    }
+}
+
+// ---- 8-bit blocks --------------------------------------------------------------------
+
+struct BlockArgs {
+    const void* x;
+    void* q;
+    float* scale;
+    long long rows, ldx, pitch;  // of x; pitch of q's rows in bytes
+    int d;
+    long long tiles_d, tiles;    // 128 x 128 tiles of x: per row of them, and all
+};
+
+// V = x, or x transposed (TRANS), in E4M3 with one scale per 1 x 128 block of V, or
+// per 128 x 128 block (TALL): scale = max(amax / 448, 2^-100), code = RNE(v / scale).
+// Bound by HBM.  A workgroup takes a 128 x 128 tile of x, thread (tr, tc) = (t / 16,
+// t % 16) its rows 8 tr .. 8 tr + 7 and columns 8 tc .. 8 tc + 7: the 16 lanes of a row
+// of x are one row of the vector unit's data moves, a column's rows lie in 8
+// registers, and the 8 x 8 codes of a thread turn in registers for the transposed
+// result, which leaves through LDS as whole 128-byte rows.  Scales lie block by
+// block, those of consecutive rows of V next to each other, as the product's
+// tiles read them.
+template <int XT, bool TALL, bool TRANS>
+__global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a) {
+    __shared__ float part[4][128];
+    __shared__ __attribute__((aligned(16))) unsigned char turned[TRANS ? 128 * 128 : 16];
+    const int t = threadIdx.x, tr = t >> 4, tc = t & 15, wave = t >> 6;
+    for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const long long ti = tile / a.tiles_d, tj = tile - ti * a.tiles_d;
+        const long long row0 = ti * 128 + 8 * tr;
+        const int col0 = (int)(tj * 128) + 8 * tc;
+        const int cols = min(8, a.d - col0), rows = (int)max(0LL, min(8LL, a.rows - row0));
+        Raw8 raw[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            raw[r] = Raw8{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+            if (r < rows && cols > 0) raw[r] = load_raw8(a.x, XT, (size_t)((row0 + r) * a.ldx) + col0, cols);
+        }
+        float v[8][8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) decode8(raw[r], XT, v[r]);
+        auto larger = [](float p, float x) __attribute__((always_inline)) { return MaxBitsOp::join(p, __builtin_fabsf(x)); };
+        // what each row (TRANS: each column; TALL: every one) of the thread's part is multiplied by
+        float code[8];
+        if constexpr (TALL) {
+            float top = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) top = larger(top, v[r][c]);
+#pragma unroll
+            for (int m = 32; m > 0; m >>= 1) top = MaxBitsOp::join(top, __shfl_xor(top, m));
+            if ((t & 63) == 0) part[wave][0] = top;
+            __syncthreads();
+            top = MaxBitsOp::join(MaxBitsOp::join(part[0][0], part[1][0]), MaxBitsOp::join(part[2][0], part[3][0]));
+            const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) code[r] = s.code;
+            if (t == 0) {
+                const long long high = (a.rows + 127) / 128;  // row blocks of x
+                a.scale[TRANS ? ti * a.tiles_d + tj : tj * high + ti] = s.scale;
+            }
+        } else if constexpr (!TRANS) {
+            float scale[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) top = larger(top, v[r][c]);
+                // the largest of 16 lanes, in each of them: rotations by 8, 4, 2 and 1
+                auto moved = [&](auto ctrl) __attribute__((always_inline)) {
+                    top = MaxBitsOp::join(top, as_f32((u32)__builtin_amdgcn_update_dpp(0, (int)as_u32(top), decltype(ctrl)::value, 0xF, 0xF, false)));
+                };
+                moved(std::integral_constant<int, 0x128>{});
+                moved(std::integral_constant<int, 0x124>{});
+                moved(std::integral_constant<int, 0x122>{});
+                moved(std::integral_constant<int, 0x121>{});
+                const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
+                code[r] = s.code;
+                scale[r] = s.scale;
+            }
+            if (tc == 0)
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < rows) a.scale[tj * a.rows + row0 + r] = scale[r];
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                float top = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) top = larger(top, v[r][c]);
+                top = MaxBitsOp::join(top, __shfl_xor(top, 16));
+                code[c] = MaxBitsOp::join(top, __shfl_xor(top, 32));
+            }
+            if ((t & 63) < 16) {
+                *(f32x4*)&part[wave][8 * tc] = f32x4{code[0], code[1], code[2], code[3]};
+                *(f32x4*)&part[wave][8 * tc + 4] = f32x4{code[4], code[5], code[6], code[7]};
+            }
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                float top = part[0][8 * tc + c];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) top = MaxBitsOp::join(top, part[w][8 * tc + c]);
+                const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
+                code[c] = s.code;
+                if (tr == 0 && c < cols) a.scale[ti * a.d + col0 + c] = s.scale;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[r][c] *= code[TRANS ? c : r];
+        if constexpr (!TRANS) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < rows && cols > 0) store_codes(a.q, GEMM_BT_FP8_E4M3, (size_t)((row0 + r) * a.pitch) + col0, cols, v[r]);
+            if constexpr (TALL) __syncthreads();  // `part` is written again
+        } else {
+            // column c of the tile is 128 bytes of `turned`, its 16-byte chunk k at place k ^ (c / 8 % 8)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const u32x2 w = {quant4<GEMM_BT_FP8_E4M3>(v[0][c], v[1][c], v[2][c], v[3][c]),
+                                 quant4<GEMM_BT_FP8_E4M3>(v[4][c], v[5][c], v[6][c], v[7][c])};
+                *(u32x2*)(turned + (8 * tc + c) * 128 + (((tr >> 1) ^ (tc & 7)) * 16) + (tr & 1) * 8) = w;
+            }
+            __syncthreads();
+            const int wide = (int)min(128LL, a.pitch - ti * 128);  // a multiple of 16: zeros behind the last row of x
+            const int high = min(128, a.d - (int)(tj * 128));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = i * 32 + (t >> 3), k = t & 7;
+                if (c < high && 16 * k < wide) {
+                    const u32x4 w = *(const u32x4*)(turned + c * 128 + ((k ^ (c >> 3 & 7)) * 16));
+                    __builtin_nontemporal_store(w, (u32x4_byte*)((unsigned char*)a.q + (size_t)((tj * 128 + c) * a.pitch) + ti * 128 + 16 * k));
+                }
+            }
+            __syncthreads();  // `part` and `turned` are written again
+        }
     }
 }
 
@@ -1336,6 +1477,35 @@ int gemm_bt_quantize_rows(const void* x, int64_t ldx, void* q, float* scale, int
     if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
     NormArgs a = {x, nullptr, nullptr, q, nullptr, scale, nullptr, rows, ldx, 0, (int)d, 0.0f, q_dtype, nullptr, nullptr};
     return launch_norm(a, x_dtype, x_dtype, stream);
+}
+
+int gemm_bt_quantize_blocks(const void* x, int64_t ldx, void* q, float* scale, int64_t rows, int64_t d, int block_rows,
+                            int transpose, int x_dtype, int q_dtype, void* stream) {
+    if (rows < 0 || d < 0) return GEMM_BT_ERR_INVALID_VALUE;
+    if ((block_rows != 1 && block_rows != 128) || (transpose != 0 && transpose != 1)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!float_type(x_dtype) || q_dtype != GEMM_BT_FP8_E4M3) return GEMM_BT_ERR_UNSUPPORTED;
+    if (d > kMaxColumns || rows > (1LL << 31)) return GEMM_BT_ERR_UNSUPPORTED;
+    if (rows == 0 || d == 0) return GEMM_BT_OK;
+    if (!x || !q || !scale || !stride_ok(ldx, d)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (!aligned(x, x_dtype) || !aligned(scale, GEMM_BT_F32)) return GEMM_BT_ERR_INVALID_VALUE;
+    int num_cu = 0;
+    const int st = check_device(&num_cu);
+    if (st != GEMM_BT_OK) return st;
+    const int64_t wide = (d + 127) / 128;
+    BlockArgs a = {x, q, scale, rows, ldx, transpose ? (rows + 15) / 16 * 16 : d, (int)d, wide, (rows + 127) / 128 * wide};
+    const void* fn = nullptr;
+    auto pick = [&](auto t) {
+        constexpr int XT = decltype(t)::value;
+        if (block_rows == 128)
+            fn = transpose ? (const void*)&quantize_blocks_kernel<XT, true, true> : (const void*)&quantize_blocks_kernel<XT, true, false>;
+        else
+            fn = transpose ? (const void*)&quantize_blocks_kernel<XT, false, true> : (const void*)&quantize_blocks_kernel<XT, false, false>;
+    };
+    if (x_dtype == GEMM_BT_F32) pick(std::integral_constant<int, GEMM_BT_F32>{});
+    else if (x_dtype == GEMM_BT_F16) pick(std::integral_constant<int, GEMM_BT_F16>{});
+    else pick(std::integral_constant<int, GEMM_BT_BF16>{});
+    void* args[] = {&a};
+    return launch(fn, dim3((unsigned)std::min<int64_t>(a.tiles, 1 << 20)), 256, args, stream);
 }
 
 int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes) {

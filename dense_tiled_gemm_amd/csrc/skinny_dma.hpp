@@ -73,6 +73,20 @@ struct SkinnyPlain {};
 struct SkinnyGated {
     EpiArgs e;
 };
+// One scale per block of 128 (see BLK in dma_kernel.hpp): a stage holds whole
+// blocks, and the scales of its rows come with it, 4 bytes per lane.  A block's
+// sums start from zero and are added to the others times both scales.
+template <int TALL>
+struct SkinnyBlocks {
+    EpiArgs e;
+    BlkArgs b;
+};
+template <class T>
+struct is_blocks : std::false_type {};
+template <int TALL>
+struct is_blocks<SkinnyBlocks<TALL>> : std::true_type {
+    static constexpr int tall = TALL;
+};
 template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT, class Epi>
 __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
                                             int M, int N, int K, int vec_store, const Epi& epi) {
@@ -104,6 +118,11 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
 
     __shared__ __attribute__((aligned(1024))) unsigned char lds[STAGES * STAGE_BYTES];
     __shared__ f32x4 red[W][NBLK][64];
+    constexpr bool BLOCKS = is_blocks<Epi>::value;
+    constexpr int BPS = KB / 128;  // blocks of 128 per stage
+    static_assert(!BLOCKS || (W == 1 && ESZ == 1 && NBLK == 1 && ROT == 0 && BPS * AR <= 64 && BPS * BN <= 64), "a lane per scale");
+    // a stage's scales: those of A, block by block, in the first 64 places, those of B in the others
+    __shared__ float scales[BLOCKS ? STAGES : 1][BLOCKS ? 128 : 1];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -143,11 +162,36 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     // ROT > 0: workgroup g walks the K steps starting at (g * ROT) mod nk and
     // wraps around, so that concurrent workgroups read different K offsets
     const int k0 = ROT > 0 && nk > 0 ? (int)(((long long)blockIdx.x * ROT) % nk) : 0;
+    // the lane's scales of A and of B: row lane % 16 (B: % BN) of block lane / 16 (/ BN) of the stage
+    [[maybe_unused]] u32 so[2] = {kOutOfRange, kOutOfRange};
+    [[maybe_unused]] int sk_block[2] = {0, 0};
+    [[maybe_unused]] long long s_first = 0;
+    if constexpr (BLOCKS) {
+        constexpr bool tall = is_blocks<Epi>::tall;
+        sk_block[0] = lane / AR;
+        sk_block[1] = lane / BN;
+        s_first = tall ? n0 >> 7 : n0;
+        const int ra_ = lane % AR, rb_ = lane % BN;
+        if (ra_ < rows_a && sk_block[0] < BPS) so[0] = ((u32)ra_ * (u32)epi.b.a.row + (u32)sk_block[0] * (u32)epi.b.a.block) * 4u;
+        if (rb_ < rows_b && sk_block[1] < BPS)
+            so[1] = ((u32)(tall ? ((n0 + rb_) >> 7) - (int)s_first : rb_) * (u32)epi.b.b.row + (u32)sk_block[1] * (u32)epi.b.b.block) * 4u;
+    }
+    auto issue_scales = [&](int stage, int kt) {
+        if constexpr (BLOCKS) {
+            const int left = (K + 127) / 128 - kt * BPS;  // blocks from this stage on
+            const long long at = (long long)kt * BPS;
+            dma4(rsrc_words(epi.b.a.s + at * epi.b.a.block, 0x7FFFFFFFu), (unsigned char*)scales[stage],
+                 sk_block[0] < left ? so[0] : kOutOfRange, 0u);
+            dma4(rsrc_words(epi.b.b.s + s_first * epi.b.b.row + at * epi.b.b.block, 0x7FFFFFFFu), (unsigned char*)(scales[stage] + 64),
+                 sk_block[1] < left ? so[1] : kOutOfRange, 0u);
+        }
+    };
     auto issue = [&](int stage, int kstep) {
         const int kt = ROT > 0 ? (kstep + k0 >= nk ? kstep + k0 - nk : kstep + k0) : kstep;
         unsigned char* sbase = lds + stage * STAGE_BYTES;
         const u32 kbytes = (u32)kt * (u32)ROWB;
         const int kleft = Kf - kt * KB;
+        issue_scales(stage, kt);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int j = wave + i * W;
@@ -195,6 +239,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     const int epi_n = !EPI || r16 >= M || 4 * q >= BN ? 0 : GATE ? min(4, N - n0) : min(4, N - n0 - 4 * q);
     Epi4 terms;
     if constexpr (GATE) terms = load_epi4(N, r16, n0 + (q == 1 ? N : 0), epi_n, epi.e);
+    else if constexpr (BLOCKS) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi.e);
     else if constexpr (EPI) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi);
 
     f32x4 acc[NBLK];
@@ -203,6 +248,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
 
     auto compute = [&](int stage) {
         const unsigned char* s = lds + stage * STAGE_BYTES;
+        f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int t = 0; t < KPW; ++t) {
             const int kb = wave * KPW + t;
@@ -215,7 +261,21 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
                 const int brow = AR + 16 * b + (r16 % BR);
                 const int chb = ((4 * kb + q) ^ (brow & 15)) * 16;
                 const u32x4 fb = *(const u32x4*)(s + brow * ROWB + chb);
-                acc[b] = skinny_mma<IN>(fb, fa, acc[b]);
+                if constexpr (BLOCKS) {
+                    part = skinny_mma<IN>(fb, fa, part);
+                    if (t % 2 == 1) {  // a block is two k-blocks of 64 bytes
+                        const float sa = scales[stage][t / 2 * AR + r16];
+                        const f32x4 sb = *(const f32x4*)&scales[stage][64 + t / 2 * BN + 4 * q % BN];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float p = part[e], w = sb[e], c = acc[b][e];
+                            acc[b][e] = __builtin_fmaf(p * sa, w, c);
+                        }
+                        part = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                } else {
+                    acc[b] = skinny_mma<IN>(fb, fa, acc[b]);
+                }
             }
         }
     };
@@ -224,7 +284,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
     int cs = 0, ls = STAGES - 1;
     for (int kt = 0; kt < nk; ++kt) {
-        wait_vmcnt<PEND>();
+        wait_vmcnt<PEND + (BLOCKS ? 2 * (STAGES - 2) : 0)>();
         barrier_no_fence();
         issue(ls, kt + STAGES - 1);
         compute(cs);
@@ -257,6 +317,8 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
                 for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(act)::value>(v[e]) * up[e];
             });
             if (epi_n > 0 && q == 0) store4(C, epi_type(md, EPI_OUT_TYPE), (size_t)r16 * N + n0, epi_n, v);
+        } else if constexpr (BLOCKS) {
+            if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi.e);
         } else {
             if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi);
         }
@@ -329,6 +391,13 @@ __global__ __launch_bounds__(64 * W) void skinny_gated_kernel(const u16* __restr
                                                              void* __restrict__ C, int M, int N, int K,
                                                              const EpiArgs epi) {
     skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, SkinnyGated{epi});  // (OUT is not used)
+}
+
+// E4M3 with scales per block, B's per 128 rows (TALL) or per row.
+template <int TALL, int BN, int KB, int STAGES>
+__global__ __launch_bounds__(64) void skinny_block_kernel(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
+                                                         int M, int N, int K, const EpiArgs epi, const BlkArgs blk) {
+    skinny_body<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BN, KB, STAGES, 1, 0>(A, B, C, M, N, K, 0, SkinnyBlocks<TALL>{epi, blk});
 }
 
 }  // namespace gbt

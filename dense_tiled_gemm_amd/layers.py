@@ -198,6 +198,7 @@ _epi_bytes = _workspace_query("gemm_bt_epi_workspace_size")
 _norm_back_bytes = _workspace_query("gemm_bt_rms_norm_backward_workspace")
 _layer_norm_back_bytes = _workspace_query("gemm_bt_layer_norm_backward_workspace")
 _linear_back_bytes = _workspace_query("gemm_bt_linear_backward_workspace")
+_block_bytes = _workspace_query("gemm_bt_block_workspace_size")
 _gated_bytes = _workspace_query("gemm_bt_gated_workspace_size")
 _gated_back_bytes = _workspace_query("gemm_bt_gated_backward_workspace")
 
@@ -601,3 +602,109 @@ def gated_linear_backward(dy, x, weight, preact, activation="silu", bias_grad=Tr
     if st:
         raise GemmBtError(st, "gemm_bt_gated_backward")
     return LinearGrads(dx, dw, db)
+
+
+# ---------------------------------------------------------------- 8 bits with scales per block of 128
+
+def quantize_blocks(x, block=(1, 128), transpose=False, dtype=torch.float8_e4m3fn, stream=None):
+    """x (rows, d), or its transpose, in 8 bits with one float32 scale per block: Quantized(q, scale).
+
+    ``block``: (1, 128), blocks along the rows of the result, for activations and gradients, or (128, 128), for weights; the
+    last blocks may be shorter.  Leading dimensions count as rows: without ``transpose`` q has x's shape, and a scale of
+    (1, 128) blocks the shape (..., ceil(d / 128)).  With it q is (d, rows), its rows filled with zeros up to a multiple of
+    16, for products that sum over the rows of x (a weight's gradient), or over a weight's rows (an input's gradient).
+    Scales are strided tensors, consecutive rows next to each other, which is what block_linear reads fastest.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, lambda: quantize_blocks(x, block, transpose, dtype))
+    device = _on_gpu(x)
+    x_code = _float_code(x.dtype, "x")
+    if dtype != torch.float8_e4m3fn:
+        raise TypeError("dtype must be float8_e4m3fn, got %s" % dtype)
+    if tuple(block) not in ((1, 128), (128, 128)):
+        raise ValueError("block must be (1, 128) or (128, 128), got %r" % (block,))
+    xr, ldx, rows, d = _rows(x, "x")
+    high, shape = block[0], x.shape
+    up = lambda n, m: (n + m - 1) // m
+    if transpose:
+        q, lead, cols = x.new_empty((d, up(rows, 16) * 16), dtype=dtype), (d,), rows
+    else:
+        q, lead, cols = x.new_empty(shape, dtype=dtype), shape[:-1], d
+    if high > 1:
+        lead = (up(d if transpose else rows, high),)
+    scale = x.new_empty((up(cols, 128),) + tuple(lead), dtype=torch.float32)
+    with _on(device):
+        st = load().gemm_bt_quantize_blocks(xr.data_ptr(), ldx, q.data_ptr(), scale.data_ptr(), rows, d, high, int(bool(transpose)),
+                                            x_code, FP8_E4M3, _stream(device.index))
+    if st:
+        raise GemmBtError(st, "gemm_bt_quantize_blocks")
+    return Quantized(q, scale.movedim(0, -1))
+
+
+def _block_scale(t, rows, blocks, what):
+    """(tensor, row stride, block stride) of scales seen as (rows, blocks)."""
+    if t.dtype != torch.float32 or t.shape[-1:] != (blocks,) or t.numel() != rows * blocks:
+        raise ValueError("%s must be a float32 tensor of %d rows of %d blocks, got %s %s" % (what, rows, blocks, t.dtype, tuple(t.shape)))
+    if t.dim() != 2:  # (leading dimensions as one: a view where they are evenly spaced)
+        t = t.reshape(rows, blocks)
+    row, block = t.stride()
+    if row >= 1 << 20 or block >= 1 << 26:
+        t = t.t().contiguous().t()
+        row, block = t.stride()
+    return t, row, block
+
+
+def block_linear(x, weight, x_scale, weight_scale, bias=None, activation="none", residual=None, out_dtype=torch.bfloat16,
+                 save_preact=False, out=None, stream=None):
+    """act(x @ weight.T + bias) + residual for 8-bit x and weight with a scale per block of 128, in one kernel.
+
+    x (..., K) and weight (N, K): float8_e4m3fn, K % 16 == 0; x_scale (..., ceil(K / 128)), one per 1 x 128 block of x;
+    weight_scale (ceil(N / 128), ceil(K / 128)), one per 128 x 128 block, or (N, ceil(K / 128)), one per 1 x 128 block, as
+    quantize_blocks makes them; matrices that it transposed go in with the zeros it filled their rows with.  bias, activation, residual, ``out_dtype``, ``save_preact`` (z in bfloat16) and ``out`` as for linear.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, lambda: block_linear(x, weight, x_scale, weight_scale, bias, activation, residual, out_dtype,
+                                                          save_preact, out))
+    device = _on_gpu(x, weight, x_scale, weight_scale, bias, residual)
+    if x.dtype != torch.float8_e4m3fn or weight.dtype != torch.float8_e4m3fn:
+        raise TypeError("x and weight must be float8_e4m3fn, got %s and %s" % (x.dtype, weight.dtype))
+    x_shape, w_shape = x.shape, weight.shape
+    if len(w_shape) != 2 or x_shape[-1:] != w_shape[1:]:
+        raise ValueError("expected x (..., K) and weight (N, K), got %s and %s" % (tuple(x_shape), tuple(w_shape)))
+    e = Epilogue()
+    e.activation = _activation(activation)
+    N, K = w_shape
+    lead = x_shape[:-1]
+    M = lead.numel()
+    shape = lead + w_shape[:1]
+    out_code = _float_code(out_dtype, "out_dtype")
+    blocks = (K + 127) // 128
+    if x_scale.shape[:-1] != lead:
+        raise ValueError("x_scale must have x's leading dimensions, got %s and %s" % (tuple(x_scale.shape), tuple(x_shape)))
+    x_scale, xr, xb = _block_scale(x_scale, M, blocks, "x_scale")
+    high = 1 if weight_scale.dim() == 2 and weight_scale.shape[0] == N else 128
+    weight_scale, wr, wb = _block_scale(weight_scale, N if high == 1 else (N + 127) // 128, blocks, "weight_scale")
+    x, weight = _chunked(x), _chunked(weight)
+    if bias is not None:
+        bias = _term(bias, w_shape[:1], "bias")
+        e.bias, e.bias_dtype = bias.data_ptr(), _float_code(bias.dtype, "bias")
+    if residual is not None:
+        residual = _term(residual, shape, "residual")
+        e.residual, e.residual_dtype = residual.data_ptr(), _float_code(residual.dtype, "residual")
+    y = _output(out, x, shape, out_dtype)
+    z = None
+    if save_preact:
+        z = x.new_empty(shape, dtype=torch.bfloat16)
+        e.preact, e.preact_dtype = z.data_ptr(), BF16
+    with _on(device):
+        s = _stream(device.index)
+        need = _block_bytes(M, N, K, out_code, device.index)
+        ws, ws_bytes = None, 0
+        if need:
+            t = workspace_for(device, s, need)
+            ws, ws_bytes = t.data_ptr(), t.numel()
+        st = load().gemm_bt_block(x.data_ptr(), weight.data_ptr(), y.data_ptr(), M, N, K, x_scale.data_ptr(), xr, xb,
+                                  weight_scale.data_ptr(), wr, wb, high, FP8_E4M3, out_code, ctypes.byref(e), ws, ws_bytes, s)
+    if st:
+        raise GemmBtError(st, "gemm_bt_block")
+    return (y, z) if save_preact else y

@@ -428,6 +428,48 @@ int gemm_bt_gated_backward(const void* dy, const void* x, const void* w, const v
                            int preact_dtype, void* workspace, size_t workspace_bytes, void* stream);
 int gemm_bt_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int activation, size_t* bytes);
 
+/*
+ * A matrix in 8 bits with one scale per block of 128 along its rows.  V is x (rows
+ * x d) or, with transpose = 1, x transposed (d x rows); a block is 1 x 128 entries of
+ * V (block_rows 1) or 128 x 128 (block_rows 128), the last ones of a row or column
+ * shorter.  With amax a block's largest |v|, scale = max(amax / 448, 2^-100) and q
+ * holds v / scale rounded to nearest even; a block with an infinity or a NaN gets
+ * the scale NaN (its codes then hold no value).
+ *   x      as for gemm_bt_quantize_rows
+ *   q      q_dtype GEMM_BT_FP8_E4M3 (else UNSUPPORTED): V row-major, dense; with
+ *          transpose the rows are rows rounded up to a multiple of 16 long, the
+ *          rest zeros (for a product that sums over the rows of x)
+ *   scale  fp32, block by block: scale[b * R + r] belongs to block b of row r of V (of
+ *          rows 128 r .. 128 r + 127 for block_rows 128), R the number of those
+ */
+int gemm_bt_quantize_blocks(const void* x, int64_t ldx, void* q, float* scale, int64_t rows, int64_t d,
+                            int block_rows, int transpose, int x_dtype, int q_dtype, void* stream);
+
+/*
+ * The product of two such matrices, with gemm_bt_epi's epilogue:
+ *   S[i][j] = sum_b sa(i, b) sb(j, b) sum_{k in block b} A[i][k] B[j][k],  b = k / 128
+ *   Z[i][j] = row_scale[i] * col_scale[j] * S[i][j] + bias[j],   C[i][j] = act(Z[i][j]) + residual[i][j]
+ * A (M x K) has blocks of 1 x 128, B (N x K) of 1 x 128 (b_block_rows 1: sb(j, b) is that of
+ * row j) or of 128 x 128 (128: that of row j / 128).  A scale lies at
+ * row * row_stride + b * block_stride floats: strides (1, R) as gemm_bt_quantize_blocks
+ * leaves them (the fastest), or others (0 .. 2^20 - 1 and 0 .. 2^26 - 1, else UNSUPPORTED).
+ * A block's sum and everything after it is held in fp32; sa * sb is rounded to fp32
+ * first where B has blocks of 128 x 128, so it must not leave fp32's range.
+ *   in_dtype   GEMM_BT_FP8_E4M3 (else UNSUPPORTED); K % 16 == 0, A and B 16-byte
+ *              aligned (else UNSUPPORTED), as for 8-bit inputs of gemm_bt
+ *   out_dtype, epilogue, K == 0 as for gemm_bt_epi
+ *   workspace  as for gemm_bt_ws, of gemm_bt_block_workspace_size bytes (NULL: no split along K)
+ * For M <= 16 and N more than 16 per compute unit the streaming kernel; else tiles
+ * of 256 x 128, 128 x 128 or 64 x 64, these cut along K where they leave half the
+ * compute units idle.  gemm_bt_plan_block reports the plan with a workspace (its
+ * variant is the index in that list).
+ */
+int gemm_bt_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, const float* a_scale,
+                  int64_t a_row_stride, int64_t a_block_stride, const float* b_scale, int64_t b_row_stride,
+                  int64_t b_block_stride, int b_block_rows, int in_dtype, int out_dtype,
+                  const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream);
+int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int out_dtype, size_t* bytes);
+
 /* Workspace gemm_bt_ws needs for these sizes and types (0 when it runs the
    plain grid), for the current device (256 compute units without one).  At
    most 16 KiB + 256 * 64 KiB (16.02 MiB) on an MI355X, whatever the
@@ -489,6 +531,9 @@ int gemm_bt_plan_ws(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype
    that is large enough. */
 int gemm_bt_plan_epi(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtype, int a_align, int b_align,
                      int c_align, gemm_bt_plan_t* plan);
+
+/* The plan of gemm_bt_block given a workspace that is large enough. */
+int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, gemm_bt_plan_t* plan);
 
 /* The plan of gemm_bt_layout (for kernel 5 the variant is 0: A K-outer, 1: B
    K-outer, 2: both, on 128 x 128 tiles; 3, 4, 5 the same on 256 x 256 tiles). */
