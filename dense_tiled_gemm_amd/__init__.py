@@ -140,8 +140,8 @@ def load():
             lib.gemm_bt_gated_backward_workspace.argtypes = lib.gemm_bt_linear_backward_workspace.argtypes
             lib.gemm_bt_quantize_blocks.argtypes = [vp, i64, vp, vp, i64, i64, ci, ci, ci, ci, vp]
             lib.gemm_bt_block.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, ci, ci, ci, vp, vp, sz, vp]
-            lib.gemm_bt_block_workspace_size.argtypes = [i64, i64, i64, ci, szp]
-            lib.gemm_bt_plan_block.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(Plan)]
+            lib.gemm_bt_block_workspace_size.argtypes = [i64, i64, i64, ci, ci, szp]
+            lib.gemm_bt_plan_block.argtypes = [i64, i64, i64, ci, ci, ci, ci, ctypes.POINTER(Plan)]
             for f in (lib.gemm_bt_quantize_blocks, lib.gemm_bt_block, lib.gemm_bt_block_workspace_size, lib.gemm_bt_plan_block,
                       lib.gemm_bt_gated, lib.gemm_bt_gated_workspace_size, lib.gemm_bt_gated_backward,
                       lib.gemm_bt_gated_backward_workspace, lib.gemm_bt_layer_norm, lib.gemm_bt_layer_norm_backward, lib.gemm_bt_layer_norm_backward_workspace,
@@ -265,9 +265,9 @@ def gemm_bt_plan_epi(M, N, K, in_dtype, out_dtype, a_align=256, b_align=256, c_a
     return p
 
 
-def gemm_bt_plan_block(M, N, K, out_dtype, a_align=256, b_align=256):
+def gemm_bt_plan_block(M, N, K, b_block_rows, out_dtype, a_align=256, b_align=256):
     p = Plan()
-    st = load().gemm_bt_plan_block(M, N, K, out_dtype, a_align, b_align, ctypes.byref(p))
+    st = load().gemm_bt_plan_block(M, N, K, b_block_rows, out_dtype, a_align, b_align, ctypes.byref(p))
     if st != OK:
         raise GemmBtError(st, "gemm_bt_plan_block")
     return p

@@ -253,9 +253,10 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     // BLK: behind the ring, a stage's scales (fp32, A's BM rows and then B's BN rows; a place per thread, since every
     // wave issues the same number of loads)
     constexpr int SCALE_BYTES = BLK ? 64 * W * 4 : 0;
-    static_assert(!BLK || (ESZ == 1 && BK == 128 && !RING5 && SCHED >= 2 && PF == 0 && !PH && LDW == 0 && EPI == 1 && BM % 64 == 0 &&
-                           BN % 64 == 0 && BM + BN <= 64 * W && TN <= 64 && RING_BYTES + STAGES * SCALE_BYTES <= 160 * 1024),
-                  "a K step is one block, a wave's scale load lies in one operand, a wave's columns in one block");
+    constexpr int BPS = BLK ? BK / 128 : 1;  // blocks per K step
+    static_assert(!BLK || (ESZ == 1 && BK % 128 == 0 && !RING5 && SCHED >= 2 && PF == 0 && !PH && LDW == 0 && EPI == 1 && BM % 64 == 0 &&
+                           BN % 64 == 0 && BPS * (BM + BN) <= 64 * W && TN <= 64 && RING_BYTES + STAGES * SCALE_BYTES <= 160 * 1024),
+                  "K steps of whole blocks, a wave's scale load lies in one operand, a wave's columns in one block");
     constexpr int XL = BLK ? 1 : 0;  // loads per wave and stage besides the tile's
 
     __shared__ __attribute__((aligned(1024))) unsigned char lds[RING_BYTES + STAGES * SCALE_BYTES + (PF > 0 ? W * 256 : 0)];
@@ -452,21 +453,24 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
     [[maybe_unused]] u32 sc_bytes = 0;
     [[maybe_unused]] const float* sc_base = nullptr;
     [[maybe_unused]] long long sc_step = 0;
+    [[maybe_unused]] int sc_left = 0;  // blocks from the wave's first one on
     if constexpr (BLK != 0) {
-        const bool of_a = wave * 64 < BM;
-        const int r = wave * 64 + lane_r - (of_a ? 0 : BM);  // tile row
+        const int nth = wave * 64 / (BM + BN);  // block of the step
+        const bool mine = nth < BPS, of_a = wave * 64 - nth * (BM + BN) < BM;
+        const int r = wave * 64 - nth * (BM + BN) + lane_r - (of_a ? 0 : BM);  // tile row
         const bool tall = BLK == 1 && !of_a;
         const BlockScales s = of_a ? sk.blk.a : sk.blk.b;
         const int first = of_a ? m0 : (tall ? n0 >> 7 : n0), rows = of_a ? rows_a : rows_b;
         const int i = tall ? ((n0 + r) >> 7) - first : r, last = tall ? ((n0 + rows - 1) >> 7) - first : rows - 1;
-        sc_base = s.s + (long long)first * s.row + (long long)kb * s.block;
-        sc_step = s.block;
-        sc_bytes = wave * 64 < BM + BN ? ((u32)last * (u32)s.row + 1u) * 4u : 0u;
-        if (r < rows && wave * 64 < BM + BN) sc_off = (u32)i * (u32)s.row * 4u;
+        sc_base = s.s + (long long)first * s.row + ((long long)kb * BPS + nth) * s.block;
+        sc_step = s.block * BPS;
+        sc_bytes = mine ? ((u32)last * (u32)s.row + 1u) * 4u : 0u;
+        sc_left = (min(Kf, ke * BK) + 127) / 128 - kb * BPS - nth;
+        if (r < rows && mine) sc_off = (u32)i * (u32)s.row * 4u;
     }
     auto load_scales = [&](int stage, int kt) {
         if constexpr (BLK != 0)
-            dma4(rsrc_words(sc_base + (long long)kt * sc_step, kb + kt < ke ? sc_bytes : 0u),
+            dma4(rsrc_words(sc_base + (long long)kt * sc_step, kt * BPS < sc_left ? sc_bytes : 0u),
                  lds + RING_BYTES + stage * SCALE_BYTES + wave * 256, sc_off, 0u);
     };
     auto mfma1 = [&](const Frag& b, const Frag& a, typename AB::type& c) {
@@ -587,9 +591,10 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         // reads and loads follow every second one, at the same points in time.
         constexpr int NH = IN == GEMM_BT_INT8 ? 2 : 1;
         // BLK: the sums of the block that is being read, and the scales of the one before until its sums are added
-        typename AB::type part[BLK ? FN : 1][BLK ? FM : 1];
+        constexpr bool WIDE = BLK == 1 && FM * FN > 4, THIN = BPS == 2, WHOLE = BLK && !WIDE && !THIN;
+        typename AB::type part[WHOLE ? FN : 1][WHOLE ? FM : 1];
         float sa[BLK ? FM : 1], sb[BLK == 2 ? FN * AB::regs : 1];
-        if constexpr (BLK != 0) {
+        if constexpr (WHOLE) {
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
                 sa[j] = 0.0f;
@@ -674,7 +679,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
         };
         constexpr auto kFirst = std::true_type{};
         constexpr auto kLater = std::false_type{};
-        static_assert(!BLK || (KS == 2 && FD == 1), "one substep of a block before the barrier, one after it");
+        static_assert(!WHOLE || (KS == 2 && FD == 1), "one substep of a block before the barrier, one after it");
         if constexpr (RING5) {
         // Five slots of one operand tile each: A(j) sits in slot 2j mod 5 and
         // B(j) in slot 2j + 1 mod 5.  After the barrier of step kt the slots
@@ -737,6 +742,174 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);
             sa = na;
+        }
+        } else if constexpr (THIN) {
+        // BLK on wave tiles of one block: two blocks of 128 per K step, each with
+        // registers of its own, so that the sums of one are added while the
+        // instructions of the other run, and half the barriers (us, against steps of
+        // one block: see plan_block).
+        static_assert(FM == 1 && FN == 1 && KS == 4 && L % 4 == 0, "thin blocks");
+        typename AB::type p2[2];
+        Frag wa[2], wb[2];
+        float s[2] = {0.0f, 0.0f}, sv[2][BLK == 2 ? AB::regs : 1];
+#pragma unroll
+        for (int r = 0; r < AB::regs; ++r) p2[1][r] = 0.0f;
+        if constexpr (BLK == 2)
+#pragma unroll
+            for (int r = 0; r < AB::regs; ++r) sv[1][r] = 0.0f;
+        auto rd = [&](const unsigned char* st, int ks) {
+            wb[ks & 1] = ld_frag(st + b_base, ks & 3);
+            wa[ks & 1] = ld_frag(st + a_base, ks & 3);
+        };
+        auto add_sums = [&](int b) {
+#pragma unroll
+            for (int r = 0; r < AB::regs; ++r) {
+                const float p = BLK == 1 ? p2[b][r] : p2[b][r] * s[b];
+                acc[0][0][r] = __builtin_fmaf(p, BLK == 1 ? s[b] : sv[b][r], acc[0][0][r]);
+            }
+        };
+#pragma unroll
+        for (int st = 0; st < STAGES - 1; ++st)
+#pragma unroll
+            for (int d = 0; d < L; ++d) load_one(st, st, d);
+        wait_vmcnt<(STAGES - 2) * (L + XL)>();
+        barrier_no_fence();
+        rd(lds, 0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        int cs = 0, ps = STAGES - 1;  // the stage of tile kt, and the one that takes tile kt + STAGES - 1
+        for (int kt = 0; kt < nk; ++kt) {
+            const unsigned char* st = lds + cs * STAGE_BYTES;
+            const int ns = cs + 1 == STAGES ? 0 : cs + 1;
+            static_for<0, 4>([&](auto kc) {
+                constexpr int ks = decltype(kc)::value, b = ks / 2;
+                if constexpr (ks == 3) {
+                    wait_vmcnt<(STAGES - 2) * (L + XL)>();  // tile kt + 1 has landed
+                    __builtin_amdgcn_s_waitcnt(0xC07F);     // done reading stage cs
+                    barrier_no_fence();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (ks < 3) rd(st, ks + 1);
+                else rd(lds + ns * STAGE_BYTES, 4);
+                if constexpr (ks % 2 == 0) {
+                    typename AB::type z;
+#pragma unroll
+                    for (int r = 0; r < AB::regs; ++r) z[r] = 0.0f;
+                    p2[b] = z;
+                }
+                mfma1(wb[ks & 1], wa[ks & 1], p2[b]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (ks < 3)  // the refill of the stage before this one, freed at the last barrier
+#pragma unroll
+                    for (int d = ks * L / 4; d < (ks == 2 ? L : (ks + 1) * L / 4); ++d) load_one(ps, kt + STAGES - 1, d);
+                if constexpr (ks % 2 == 0) add_sums(b ^ 1);
+                if constexpr (ks == 0) {
+                    const float* sc = (const float*)(lds + RING_BYTES + cs * SCALE_BYTES);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float* q = sc + y * (BM + BN);
+                        s[y] = q[wm * TM + fr] * (BLK == 1 ? q[BM + wn * TN] : 1.0f);
+                        if constexpr (BLK == 2)
+#pragma unroll
+                            for (int g = 0; g < AB::regs / 4; ++g) {
+                                const f32x4 v = *(const f32x4*)(q + BM + wn * TN + AB::col(lane_r, g));
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) sv[y][4 * g + r] = v[r];
+                            }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            ps = cs;
+            cs = ns;
+        }
+        add_sums(1);
+        } else if constexpr (WIDE) {
+        // BLK with a wave tile whose sums leave no room for a second set: block by
+        // block (j outer), both halves of a K step at once, the sums of two blocks
+        // in registers of their own in turn.  While the two instructions of block n
+        // run, the sums of block n - 1 are added to the tile's.  Fragments: B's FN
+        // rows of both halves for the whole step, A's of block row j + 1 while j is
+        // multiplied.  The barrier comes before the last block row, whose
+        // instructions cover the next tile's first reads; the refill goes out
+        // behind it.
+        static_assert(STAGES == 2 && FN == 2 && FM % 2 == 0 && KS == 2 && LAW == 4 && LBW == 4, "wide blocks");
+        constexpr int NB = FM * FN;
+        typename AB::type p2[2];
+        Frag wb[2][FN], wa[2][2];  // [half][i], [j % 2][half]
+        float s[FM];
+        auto rd_b = [&](const unsigned char* st, int h, int i) { wb[h][i] = ld_frag(st + b_base + MF * ROWB * i, h); };
+        auto rd_a = [&](const unsigned char* st, int h, int j) { wa[j & 1][h] = ld_frag(st + a_base + MF * ROWB * (j % FM), h); };
+        auto add_sums = [&](int n) {
+#pragma unroll
+            for (int r = 0; r < AB::regs; ++r)
+                acc[n % FN][n / FN][r] = __builtin_fmaf(p2[n & 1][r], s[n / FN], acc[n % FN][n / FN][r]);
+        };
+        // loads 2 q and 2 q + 1 of the refill: of A for q = 0, 1, of B for q = 2, 3 (an offset past the end stays so)
+        auto refill = [&](int stage, int kt, int q) {
+            const u32 lo = l_kc < Ke - (kb + kt) * BK ? l_off : kOutOfRange;
+            unsigned char* sbase = lds + stage * STAGE_BYTES + (q < 2 ? 0 : BM * ROWB);
+            if (q == 0) load_scales(stage, kt);
+#pragma unroll
+            for (int d = 2 * (q & 1); d < 2 * (q & 1) + 2; ++d)
+                dma16(q < 2 ? ra : rb, sbase + (wave + d * LW) * 1024, lo + (u32)d * lw_stride, (u32)(kb + kt) * (u32)ROWB);
+        };
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) refill(st, st, q);
+        wait_vmcnt<L + XL>();
+        barrier_no_fence();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) rd_b(lds, h, i);
+            rd_a(lds, h, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        int cs = 0;
+        for (int kt = 0; kt < nk; ++kt) {
+            const unsigned char* st = lds + cs * STAGE_BYTES;
+            const unsigned char* nst = lds + (cs ^ 1) * STAGE_BYTES;
+            static_for<0, NB>([&](auto nc) {
+                constexpr int n = decltype(nc)::value, j = n / FN, i = n % FN;
+                constexpr bool LAST = j == FM - 1;
+                if constexpr (LAST && i == 0) {
+                    wait_vmcnt<0>();                     // tile kt + 1 has landed
+                    __builtin_amdgcn_s_waitcnt(0xC07F);  // done reading stage cs
+                    barrier_no_fence();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                typename AB::type z;
+#pragma unroll
+                for (int r = 0; r < AB::regs; ++r) z[r] = 0.0f;
+                p2[n & 1] = z;
+                mfma1(wb[0][i], wa[j & 1][0], p2[n & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (!LAST) {
+                    rd_a(st, i, j + 1);  // half i of the next block row
+                } else {
+                    rd_b(nst, 0, i);
+                    rd_a(nst, i, FM);  // row 0
+                    refill(cs, kt + 2, 2 * i);
+                }
+                if constexpr (n == 0) {
+                    const float* sc = (const float*)(lds + RING_BYTES + cs * SCALE_BYTES);
+                    const float b = sc[BM + wn * TN];  // a wave's columns lie in one block
+#pragma unroll
+                    for (int y = 0; y < FM; ++y) s[y] = sc[wm * TM + MF * y + fr] * b;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                mfma1(wb[1][i], wa[j & 1][1], p2[n & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (LAST) {
+                    rd_b(nst, 1, i);
+                    refill(cs, kt + 2, 2 * i + 1);
+                }
+                if constexpr (n > 0) add_sums(n - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            add_sums(NB - 1);
+            cs ^= 1;
         }
         } else {
 #pragma unroll

@@ -18,11 +18,12 @@ const void* epi_fill_fn(bool gated);
 // The 8-bit product with scales per block of 128: tiles of blockTile(i) with B's
 // scales per 128 rows (tall) or per row, their split form, and the streaming
 // kernel for M <= 16.
-constexpr int kBlockTiles = 3;
+constexpr int kBlockTiles = 5;
 struct BlockTile {
-    int bm, bn, threads;
+    int bm, bn, bk, threads, stages;
 };
-constexpr BlockTile kBlockTile[kBlockTiles] = {{256, 128, 512}, {128, 128, 256}, {64, 64, 256}};
+constexpr BlockTile kBlockTile[kBlockTiles] = {
+    {256, 128, 128, 512, 3}, {128, 128, 128, 256, 4}, {64, 64, 128, 256, 4}, {256, 256, 128, 512, 2}, {64, 64, 256, 256, 4}};  // (3: tall alone)
 const void* block_dma_fn(int tile, bool tall, bool split);
 const void* block_skinny_fn(bool tall);
 

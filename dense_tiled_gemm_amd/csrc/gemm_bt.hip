@@ -1231,12 +1231,55 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
 
 // ---- the product with scales per block of 128 ------------------------------------------
 
+// What a wave of a tile shape (one workgroup per CU, of 64 x 64 tiles in steps of
+// 128 two) takes in us: `start` for its prologue and epilogue, `step` for each
+// block of 128 along K with B's scales per 128 rows, `step_rows` with one per row.
+// Measured in whole calls, tall and per row (us, 64 x 64 in steps of 256, 64 x 64, 128
+// x 128, 256 x 128, 256 x 256): 256x4096x4096 13.3 13.7, 15.3 16.6, 25.8 29.4, 29.6
+// 35.5, 54.0; 1024x2048x4096 21.4 23.3, 18.6 20.7, 24.8 29.5, 29.8 35.7, 54.0;
+// 1024x4096x4096 46 48, 39 41, 28 32, 32 38, 54; 1536x4096x4096 -, 54 60, 53 61, 35
+// 41, 55; 2048x4352x4096 -, 77 85, 75 89, 68 81, 59; 4096^3 -, 136 147, 106 123, 80 94,
+// 75; 6144x4096x4096 -, 198 218, 157 182, 119 140, 127; 8192x8192x4096 -, 532 584, 423
+// 485, 312 365, 291.
+struct BlockCost {
+    double start, step, step_rows;
+    int per_cu;
+};
+constexpr BlockCost kBlockCost[kBlockTiles] = {
+    {6.0, 0.96, 1.14, 1}, {4.0, 0.67, 0.78, 1}, {2.0, 0.47, 0.52, 2}, {8.0, 1.94, 1e9, 1}, {2.0, 0.235, 0.25, 1}};
+
+static int64_t block_tiles(int tile, int64_t M, int64_t N) {
+    const BlockTile& t = kBlockTile[tile];
+    return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+// A last wave that fills a part f of the CUs takes about 0.7 + 0.3 f of a full one
+// (256 x 128 tiles at K = 4096: 128 tiles 32.4 us, 192 35.1, 256 41.4; 256 x 256 ones:
+// 128 54.4, 160 59.9, 256 74.9): the full chip runs at a lower clock.
+static double block_time(int tile, int64_t M, int64_t N, int64_t K, bool tall, int num_cu) {
+    const BlockCost& c = kBlockCost[tile];
+    const int64_t n = block_tiles(tile, M, N), wave = (int64_t)num_cu * c.per_cu, rest = n % wave;
+    const double waves = (double)(n / wave) + (rest ? 0.7 + 0.3 * (double)rest / (double)wave : 0.0);
+    return waves * (c.start + (double)((K + 127) / 128) * (tall ? c.step : c.step_rows));
+}
+static int block_best(int64_t M, int64_t N, int64_t K, bool tall, int num_cu, double* time) {
+    int best = 0;
+    for (int i = 1; i < kBlockTiles; ++i)
+        if (block_time(i, M, N, K, tall, num_cu) < block_time(best, M, N, K, tall, num_cu)) best = i;
+    if (time) *time = block_time(best, M, N, K, tall, num_cu);
+    return best;
+}
+
 // Plan: the streaming kernel for M <= 16 where its workgroups of 8 rows of B are
-// more than two per CU (as for 8-bit rows with an epilogue), else the tile shapes
-// of kBlockTile (`variant` is the index), the smallest cut along K where they leave
-// half the CUs idle.
-static int plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, int num_cu, bool allow_sk,
-                      gemm_bt_plan_t* p) {
+// more than two per CU (as for 8-bit rows with an epilogue), else the tile shape
+// with the shortest estimate (`variant` is its index in kBlockTile).  Where whole
+// waves of it and another plan for the remaining rows, in a second launch, are
+// estimated shorter, the product is split into those (split_rows).  64 x 64
+// tiles that leave half the CUs idle are cut along K into pieces of at least 16
+// blocks (us, uncut, pieces of 16, of 8: 16x1024x8192 16.6, 11.1, 11.8; 128x1024x8192
+// 17.3, 11.7, 13.2; 64x512x2048 9.6, 9.5, 10.6).
+constexpr int kThinBlocks = 4;
+static int plan_block(int64_t M, int64_t N, int64_t K, bool tall, int out_dtype, int a_align, int b_align, int num_cu, bool allow_sk,
+                      bool allow_rows, gemm_bt_plan_t* p) {
     std::memset(p, 0, sizeof(*p));
     if (M < 0 || N < 0 || K < 0) return GEMM_BT_ERR_INVALID_VALUE;
     p->batch = 1;
@@ -1252,37 +1295,63 @@ static int plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_alig
         return GEMM_BT_OK;
     }
     if (K % 16 != 0 || a_align % 16 != 0 || b_align % 16 != 0) return GEMM_BT_ERR_UNSUPPORTED;
+    p->vec = 16;
     if (M <= 16 && N > 16 * (int64_t)num_cu) {
         p->kernel = KIND_SKINNY;
         p->bm = 16;
         p->bn = 8;
         p->bk = 512;
         p->stages = 3;
+        p->ksplit = 1;
         p->threads = 64;
         p->tiles_m = 1;
         p->tiles_n = p->grid = (N + 7) / 8;
         return GEMM_BT_OK;
     }
-    auto tiles = [&](int i) {
-        const BlockTile& t = kBlockTile[i];
-        return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-    };
-    const int use = tiles(0) >= num_cu ? 0 : tiles(1) * 2 > num_cu ? 1 : 2;
+    double whole = 0.0;
+    const int use = block_best(M, N, K, tall, num_cu, &whole);
+    if (allow_rows) {
+        int64_t rows = 0;
+        double least = whole;
+        for (int i : {0, 3}) {  // the tiles that large products run
+            const int64_t tn = (N + kBlockTile[i].bn - 1) / kBlockTile[i].bn;
+            const int64_t m1 = block_tiles(i, M, N) / num_cu * num_cu / tn * kBlockTile[i].bm;
+            if (m1 <= 0 || m1 >= M) continue;
+            double rest = 0.0;
+            block_best(M - m1, N, K, tall, num_cu, &rest);
+            const double both = block_time(i, m1, N, K, tall, num_cu) + rest + 3.0;  // (a launch)
+            if (both < least) {
+                least = both;
+                rows = m1;
+            }
+        }
+        if (rows > 0 && least < 0.97 * whole) {
+            gemm_bt_plan_t rest;
+            int st = plan_block(M - rows, N, K, tall, out_dtype, a_align, b_align, num_cu, allow_sk, false, &rest);
+            if (st == GEMM_BT_OK) st = plan_block(rows, N, K, tall, out_dtype, a_align, b_align, num_cu, allow_sk, false, p);
+            if (st != GEMM_BT_OK) return st;
+            p->split_rows = rows;
+            p->workspace_bytes = std::max(p->workspace_bytes, rest.workspace_bytes);
+            return GEMM_BT_OK;
+        }
+    }
     const BlockTile& t = kBlockTile[use];
     p->kernel = KIND_DMA;
     p->variant = use;
     p->bm = t.bm;
     p->bn = t.bn;
-    p->bk = 128;
-    p->stages = use == 0 ? 3 : 4;
+    p->bk = t.bk;
+    p->stages = t.stages;
     p->threads = t.threads;
+    p->lds_bytes = t.stages * ((t.bm + t.bn) * t.bk + t.threads * 4);
     p->group_m = kGroupM;
+    p->ksplit = 1;
     p->tiles_m = (M + t.bm - 1) / t.bm;
     p->tiles_n = (N + t.bn - 1) / t.bn;
     p->grid = p->tiles_m * p->tiles_n;
     if (p->grid > 0x7FFFFFFF) return GEMM_BT_ERR_UNSUPPORTED;
-    const int64_t T = p->grid, nk = (K + 127) / 128, S = std::min<int64_t>(num_cu / T, nk / 8);
-    if (allow_sk && use == 2 && T * 2 <= num_cu && S >= 2) {
+    const int64_t T = p->grid, S = std::min<int64_t>(num_cu / T, (K + 127) / 128 / 16);
+    if (allow_sk && use == kThinBlocks && T * 2 <= num_cu && T <= kSkMaxTiles && S >= 2) {
         p->grid = T * S;
         p->split_tiles = T;
         p->workspace_bytes = kSkCounterBytes + p->grid * (int64_t)t.bm * t.bn * 4;
@@ -1291,9 +1360,9 @@ static int plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_alig
 }
 
 static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int out_dtype, const EpiArgs& epi,
-                        const BlkArgs& blk, bool tall, void* ws, size_t ws_bytes, void* stream) {
+                        const BlkArgs& blk, bool tall, void* ws, size_t ws_bytes, void* stream, bool allow_rows = true) {
     gemm_bt_plan_t p;
-    int st = plan_block(M, N, K, out_dtype, align_of(A), align_of(B), 256, ws != nullptr, &p);
+    int st = plan_block(M, N, K, tall, out_dtype, align_of(A), align_of(B), 256, ws != nullptr, allow_rows, &p);
     if (st != GEMM_BT_OK) return st;
     if (p.kernel == KIND_NONE) return GEMM_BT_OK;
     if (!C || (uintptr_t)C % out_size(out_dtype)) return GEMM_BT_ERR_INVALID_VALUE;
@@ -1308,10 +1377,19 @@ static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_
     st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
     if (num_cu != 256) {
-        st = plan_block(M, N, K, out_dtype, align_of(A), align_of(B), num_cu, ws != nullptr, &p);
+        st = plan_block(M, N, K, tall, out_dtype, align_of(A), align_of(B), num_cu, ws != nullptr, allow_rows, &p);
         if (st != GEMM_BT_OK) return st;
     }
     if (p.workspace_bytes > 0 && ((uintptr_t)ws % 16 != 0 || ws_bytes < (size_t)p.workspace_bytes)) return GEMM_BT_ERR_INVALID_VALUE;
+    if (p.split_rows > 0) {
+        const int64_t m1 = p.split_rows;
+        st = launch_block(A, B, C, m1, N, K, out_dtype, epi, blk, tall, ws, ws_bytes, stream, false);
+        if (st != GEMM_BT_OK) return st;
+        BlkArgs rest = blk;
+        rest.a.s += m1 * blk.a.row;
+        return launch_block((const char*)A + m1 * K, B, (char*)C + m1 * N * out_size(out_dtype), M - m1, N, K, out_dtype,
+                            epi_rows(epi, m1, N), rest, tall, ws, ws_bytes, stream, false);
+    }
     const u16* a = (const u16*)A;
     const u16* b = (const u16*)B;
     int Mi = (int)M, Ni = (int)N, Ki = (int)K;
@@ -1557,18 +1635,21 @@ int gemm_bt_epi(const void* A, const void* B, void* C, int64_t M, int64_t N, int
     return launch_inner(A, B, C, 1, M, N, K, 0, 0, 0, in_dtype, epi_plan_type(in_dtype, out_dtype), workspace, workspace_bytes, stream, &e);
 }
 
-int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int out_dtype, size_t* bytes) {
+int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int b_block_rows, int out_dtype, size_t* bytes) {
     if (!bytes) return GEMM_BT_ERR_INVALID_VALUE;
     *bytes = 0;
     gemm_bt_plan_t p;
-    const int st = plan_block(M, N, K, out_dtype, 256, 256, plan_cus(), true, &p);
+    const int st = gemm_bt_plan_block(M, N, K, b_block_rows, out_dtype, 256, 256, &p);
     if (st == GEMM_BT_OK) *bytes = (size_t)p.workspace_bytes;
     return st;
 }
 
-int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, gemm_bt_plan_t* plan) {
+int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int b_block_rows, int out_dtype, int a_align, int b_align,
+                       gemm_bt_plan_t* plan) {
     if (!plan) return GEMM_BT_ERR_INVALID_VALUE;
-    return plan_block(M, N, K, out_dtype, a_align, b_align, plan_cus(), true, plan);
+    std::memset(plan, 0, sizeof(*plan));
+    if (b_block_rows != 1 && b_block_rows != 128) return GEMM_BT_ERR_INVALID_VALUE;
+    return plan_block(M, N, K, b_block_rows == 128, out_dtype, a_align, b_align, plan_cus(), true, true, plan);
 }
 
 int gemm_bt_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, const float* a_scale, int64_t a_row_stride,

@@ -89,17 +89,19 @@ const void* epi_skinny_fn(int in_dtype, bool gated) {
     }
 }
 
-template <int BM, int BN, int S, int WM, int WN, int SCHED, int SK, int BLK>
+template <int BM, int BN, int BK, int S, int WM, int WN, int SCHED, int SK, int BLK>
 static const void* block_fn() {
-    return (const void*)&dma_kernel<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BM, BN, 128, S, WM, WN, 2, SCHED, 0, 32, 0, 0, SK, 0, 1, BLK>;
+    return (const void*)&dma_kernel<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BM, BN, BK, S, WM, WN, 2, SCHED, 0, 32, 0, 0, SK, 0, 1, BLK>;
 }
 template <int BLK>
 static const void* block_fn_of(int tile, bool split) {
-    if (split) return tile == 2 ? block_fn<64, 64, 4, 2, 2, 4, 1, BLK>() : nullptr;
+    if (split) return tile == 4 ? block_fn<64, 64, 256, 4, 2, 2, 4, 1, BLK>() : nullptr;
     switch (tile) {
-        case 0: return block_fn<256, 128, 3, 4, 2, 8, 0, BLK>();
-        case 1: return block_fn<128, 128, 4, 2, 2, 8, 0, BLK>();
-        default: return block_fn<64, 64, 4, 2, 2, 4, 0, BLK>();
+        case 0: return block_fn<256, 128, 128, 3, 4, 2, 8, 0, BLK>();
+        case 1: return block_fn<128, 128, 128, 4, 2, 2, 8, 0, BLK>();
+        case 2: return block_fn<64, 64, 128, 4, 2, 2, 4, 0, BLK>();
+        case 4: return block_fn<64, 64, 256, 4, 2, 2, 4, 0, BLK>();
+        default: return BLK == 1 ? block_fn<256, 256, 128, 2, 2, 4, 6, 0, 1>() : nullptr;
     }
 }
 const void* block_dma_fn(int tile, bool tall, bool split) {

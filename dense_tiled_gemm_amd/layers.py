@@ -698,7 +698,7 @@ def block_linear(x, weight, x_scale, weight_scale, bias=None, activation="none",
         e.preact, e.preact_dtype = z.data_ptr(), BF16
     with _on(device):
         s = _stream(device.index)
-        need = _block_bytes(M, N, K, out_code, device.index)
+        need = _block_bytes(M, N, K, high, out_code, device.index)
         ws, ws_bytes = None, 0
         if need:
             t = workspace_for(device, s, need)

@@ -459,16 +459,17 @@ int gemm_bt_quantize_blocks(const void* x, int64_t ldx, void* q, float* scale, i
  *              aligned (else UNSUPPORTED), as for 8-bit inputs of gemm_bt
  *   out_dtype, epilogue, K == 0 as for gemm_bt_epi
  *   workspace  as for gemm_bt_ws, of gemm_bt_block_workspace_size bytes (NULL: no split along K)
- * For M <= 16 and N more than 16 per compute unit the streaming kernel; else tiles
- * of 256 x 128, 128 x 128 or 64 x 64, these cut along K where they leave half the
- * compute units idle.  gemm_bt_plan_block reports the plan with a workspace (its
- * variant is the index in that list).
+ * For M <= 16 and N more than 16 per compute unit the streaming kernel; else the
+ * tiles with the shortest estimate: 256 x 128 (the plan's variant 0), 128 x 128 (1),
+ * 64 x 64 in steps of 128 (2) or 256 (4) along K, and for B in blocks of 128 x 128 256 x
+ * 256 (3); 64 x 64 ones cut along K where they leave half the compute units idle, and
+ * rows past whole waves of large tiles in a second launch (gemm_bt_plan_block).
  */
 int gemm_bt_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, const float* a_scale,
                   int64_t a_row_stride, int64_t a_block_stride, const float* b_scale, int64_t b_row_stride,
                   int64_t b_block_stride, int b_block_rows, int in_dtype, int out_dtype,
                   const gemm_bt_epilogue_t* epilogue, void* workspace, size_t workspace_bytes, void* stream);
-int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int out_dtype, size_t* bytes);
+int gemm_bt_block_workspace_size(int64_t M, int64_t N, int64_t K, int b_block_rows, int out_dtype, size_t* bytes);
 
 /* Workspace gemm_bt_ws needs for these sizes and types (0 when it runs the
    plain grid), for the current device (256 compute units without one).  At
@@ -533,7 +534,8 @@ int gemm_bt_plan_epi(int64_t M, int64_t N, int64_t K, int in_dtype, int out_dtyp
                      int c_align, gemm_bt_plan_t* plan);
 
 /* The plan of gemm_bt_block given a workspace that is large enough. */
-int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int out_dtype, int a_align, int b_align, gemm_bt_plan_t* plan);
+int gemm_bt_plan_block(int64_t M, int64_t N, int64_t K, int b_block_rows, int out_dtype, int a_align, int b_align,
+                       gemm_bt_plan_t* plan);
 
 /* The plan of gemm_bt_layout (for kernel 5 the variant is 0: A K-outer, 1: B
    K-outer, 2: both, on 128 x 128 tiles; 3, 4, 5 the same on 256 x 256 tiles). */

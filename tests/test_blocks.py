@@ -174,7 +174,7 @@ def check(gpu, M, N, K, high, outd, act, bias=None, res=None, pre=False, seed=0,
     close(y, a, tol, "y")
 
 
-SHAPES = [(1, 1, 16), (1, 72, 4096), (16, 8192, 512), (1, 4104, 4096), (5, 6001, 272), (16, 4099, 8208), (3, 5000, 128), (64, 512, 8192),
+SHAPES = [(1, 1, 16), (520, 4096, 208), (1100, 1500, 400), (4400, 4096, 64), (2100, 4350, 336), (1040, 2000, 144), (1, 72, 4096), (16, 8192, 512), (1, 4104, 4096), (5, 6001, 272), (16, 4099, 8208), (3, 5000, 128), (64, 512, 8192),
           (33, 4096, 4096), (200, 300, 8208), (7, 70, 16384), (129, 1000, 4112), (33, 65, 144), (130, 264, 208), (300, 333, 128),
           (700, 1100, 128), (1000, 2050, 400), (2050, 2050, 64), (2048, 4352, 80), (4100, 4096, 48), (4096, 4097, 32), (1000, 3000, 2064),
           (2048, 4096, 1024), (5000, 3333, 144)]
@@ -193,10 +193,14 @@ def test_block_linear(gpu, high, shape):
 
 def test_shapes_cover_every_kernel():
     seen = set()
-    for M, N, K in SHAPES:
-        p = gb.gemm_bt_plan_block(M, N, K, gb.BF16)
-        seen.add((p.kernel, p.variant if p.kernel == 4 else 0, p.split_tiles > 0))
-    assert seen == {(3, 0, False), (4, 0, False), (4, 1, False), (4, 2, False), (4, 2, True)}, seen
+    for (M, N, K), high in itertools.product(SHAPES, (1, 128)):
+        p = gb.gemm_bt_plan_block(M, N, K, high, gb.BF16)
+        parts = [p] + ([gb.gemm_bt_plan_block(M - p.split_rows, N, K, high, gb.BF16)] if p.split_rows else [])
+        seen |= {(high, q.kernel, q.variant, q.split_tiles > 0, p.split_rows > 0) for q in parts}
+    kinds = {(h, k, v, s) for h, k, v, s, _ in seen}
+    tiles = {(h, 4, v, False) for h in (1, 128) for v in (0, 1, 2, 4)} | {(128, 4, 3, False)}
+    assert kinds == tiles | {(h, 4, 4, True) for h in (1, 128)} | {(h, 3, 0, False) for h in (1, 128)}, kinds
+    assert {h for h, _, _, _, rows in seen if rows} == {1, 128}
 
 
 @pytest.mark.gpu
@@ -308,7 +312,7 @@ def test_large_offsets(gpu):
 def test_streams_and_graphs(gpu):
     """Quantisation and products, a split one among them, on side streams and in replayed graphs."""
     M, N, K = 64, 512, 8192
-    assert gpu.gemm_bt_plan_block(M, N, K, gpu.BF16).split_tiles > 0
+    assert gpu.gemm_bt_plan_block(M, N, K, 128, gpu.BF16).split_tiles > 0
     make = lambda seed: [randn(seed, M, K, dtype=torch.bfloat16).cuda(), randn(seed + 1, N, K, dtype=torch.bfloat16).cuda()]
 
     def both(x, w, stream=None):
@@ -377,13 +381,14 @@ def test_refusals(kw, want):
 def test_workspaces_and_plans():
     lib, n = gb.load(), ctypes.c_size_t()
     f = lib.gemm_bt_block_workspace_size
-    assert f(4, 4, 16, gb.BF16, None) == BAD and f(-1, 4, 16, gb.BF16, ctypes.byref(n)) == BAD and f(4, 4, 8, gb.BF16, ctypes.byref(n)) == UNSUP
-    assert f(4, 4, 16, gb.INT32, ctypes.byref(n)) == UNSUP and n.value == 0
-    assert f(64, 512, 8192, gb.BF16, ctypes.byref(n)) == gb.OK
-    p = gb.gemm_bt_plan_block(64, 512, 8192, gb.BF16)
-    assert n.value == p.workspace_bytes == 16384 + p.grid * 64 * 64 * 4 and p.grid == p.split_tiles * 8
+    assert f(4, 4, 16, 1, gb.BF16, None) == BAD and f(-1, 4, 16, 1, gb.BF16, ctypes.byref(n)) == BAD
+    assert f(4, 4, 8, 1, gb.BF16, ctypes.byref(n)) == UNSUP and f(4, 4, 16, 64, gb.BF16, ctypes.byref(n)) == BAD
+    assert f(4, 4, 16, 1, gb.INT32, ctypes.byref(n)) == UNSUP and n.value == 0
+    assert f(64, 512, 8192, 128, gb.BF16, ctypes.byref(n)) == gb.OK
+    p = gb.gemm_bt_plan_block(64, 512, 8192, 128, gb.BF16)
+    assert n.value == p.workspace_bytes == 16384 + p.grid * 64 * 64 * 4 and p.grid == p.split_tiles * 4
     assert block(M=64, N=512, K=8192, ba=64, ws=16, n=n.value - 1) in (BAD, gb.ERR_NO_DEVICE)  # (checked after the device)
-    assert lib.gemm_bt_plan_block(4, 4, 16, gb.BF16, 16, 16, None) == BAD
+    assert lib.gemm_bt_plan_block(4, 4, 16, 1, gb.BF16, 16, 16, None) == BAD
 
 
 def test_wrappers_check_before_the_library():
