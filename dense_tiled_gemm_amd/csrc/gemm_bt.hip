@@ -1099,8 +1099,8 @@ static SkArgs sk_args(const gemm_bt_plan_t& p, int64_t K, void* ws) {
 // Every K-inner call: argument checks, the plan for the current device and
 // the launch.  `ws` (with `ws_bytes`) enables the stream-K plan; NULL plans
 // the data-parallel grid as gemm_bt does.  `gated`: B has 2 N rows, and the plan is
-// that of 2 N columns (its tiles_n and the streaming kernel's grid then count
-// blocks of half as many columns of C).
+// that of 2 N columns (its tiles_n then counts blocks of half as many columns of
+// C), the streaming kernel in the shape that pick_stream gives.
 static int launch_inner(const void* A, const void* B, void* C, int64_t batch, int64_t M, int64_t N, int64_t K,
                         int64_t stride_a, int64_t stride_b, int64_t stride_c, int in_dtype, int out_dtype, void* ws,
                         size_t ws_bytes, void* stream, const EpiArgs* epi = nullptr, bool gated = false) {
@@ -1204,7 +1204,9 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
         } else {
             const void* fn = nullptr;
             if (epi) {
-                fn = epi_skinny_fn(in_dtype, gated);
+                const int shape = gated ? pick_stream(2 * N, K * isz, num_cu) : 0;
+                fn = gated ? gated_skinny_fn(in_dtype, shape) : epi_skinny_fn(in_dtype);
+                if (gated) p.grid = (2 * N + kStream[shape].rows - 1) / kStream[shape].rows;
             } else if (p.variant >= 1) {
                 int n = 0;
                 fn = skinny_variants(&n)[p.variant - 1].fn[in_index(in_dtype)][out_index(out_dtype)];
@@ -1269,8 +1271,8 @@ static int block_best(int64_t M, int64_t N, int64_t K, bool tall, int num_cu, do
     return best;
 }
 
-// Plan: the streaming kernel for M <= 16 where its workgroups of 8 rows of B are
-// more than two per CU (as for 8-bit rows with an epilogue), else the tile shape
+// Plan: the streaming kernel for M <= 16 and N more than 16 per CU (as for 8-bit rows
+// with an epilogue; `variant` is its shape in kStream), else the tile shape
 // with the shortest estimate (`variant` is its index in kBlockTile).  Where whole
 // waves of it and another plan for the remaining rows, in a second launch, are
 // estimated shorter, the product is split into those (split_rows).  64 x 64
@@ -1298,14 +1300,16 @@ static int plan_block(int64_t M, int64_t N, int64_t K, bool tall, int out_dtype,
     p->vec = 16;
     if (M <= 16 && N > 16 * (int64_t)num_cu) {
         p->kernel = KIND_SKINNY;
+        p->variant = pick_stream(N, K, num_cu);
+        const StreamShape& s = kStream[p->variant];
         p->bm = 16;
-        p->bn = 8;
-        p->bk = 512;
-        p->stages = 3;
+        p->bn = s.rows;
+        p->bk = s.bytes;
+        p->stages = s.stages;
         p->ksplit = 1;
         p->threads = 64;
         p->tiles_m = 1;
-        p->tiles_n = p->grid = (N + 7) / 8;
+        p->tiles_n = p->grid = (N + s.rows - 1) / s.rows;
         return GEMM_BT_OK;
     }
     double whole = 0.0;
@@ -1401,7 +1405,7 @@ static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_
     if (p.kernel == KIND_SKINNY) {
         BlkArgs ba = blk;
         void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &ea, &ba};
-        return launch(block_skinny_fn(tall), dim3((unsigned)p.grid), p.threads, args, stream);
+        return launch(block_skinny_fn(tall, p.variant), dim3((unsigned)p.grid), p.threads, args, stream);
     }
     SkBlkArgs s;
     (SkArgs&)s = sk_args(p, K, ws);

@@ -72,19 +72,40 @@ const void* epi_dma_fn(int variant, int in_dtype, bool split, bool gated) {
     return gated ? fn_of<2>(variant, in_dtype, split) : fn_of<1>(variant, in_dtype, split);
 }
 
-// 512 bytes of K per row and stage
-template <int IN>
-static const void* skinny_of(bool gated) {
-    constexpr int KB = 512 / in_size(IN);
-    return gated ? (const void*)&skinny_gated_kernel<IN, 8, KB, 3, 1> : (const void*)&skinny_epi_kernel<IN, 8, KB, 3, 1>;
+const void* epi_skinny_fn(int in_dtype) {
+    switch (in_dtype) {  // 512 bytes of K per row and stage
+        case GEMM_BT_BF16: return (const void*)&skinny_epi_kernel<GEMM_BT_BF16, 8, 256, 3, 1>;
+        case GEMM_BT_F16: return (const void*)&skinny_epi_kernel<GEMM_BT_F16, 8, 256, 3, 1>;
+        case GEMM_BT_FP8_E4M3: return (const void*)&skinny_epi_kernel<GEMM_BT_FP8_E4M3, 8, 512, 3, 1>;
+        case GEMM_BT_FP8_E5M2: return (const void*)&skinny_epi_kernel<GEMM_BT_FP8_E5M2, 8, 512, 3, 1>;
+        case GEMM_BT_INT8: return (const void*)&skinny_epi_kernel<GEMM_BT_INT8, 8, 512, 3, 1>;
+        default: return nullptr;
+    }
 }
-const void* epi_skinny_fn(int in_dtype, bool gated) {
+
+// f(std::integral_constant<int, i>{}) for the shape kStream[i]
+template <class F>
+static const void* with_stream(int shape, F&& f) {
+    switch (shape) {
+        case 0: return f(std::integral_constant<int, 0>{});
+        case 1: return f(std::integral_constant<int, 1>{});
+        default: return f(std::integral_constant<int, 2>{});
+    }
+}
+template <int IN>
+static const void* gated_of(int shape) {
+    return with_stream(shape, [](auto c) {
+        constexpr StreamShape s = kStream[c()];
+        return (const void*)&skinny_gated_kernel<IN, s.rows, s.bytes / in_size(IN), s.stages, 1>;
+    });
+}
+const void* gated_skinny_fn(int in_dtype, int shape) {
     switch (in_dtype) {
-        case GEMM_BT_BF16: return skinny_of<GEMM_BT_BF16>(gated);
-        case GEMM_BT_F16: return skinny_of<GEMM_BT_F16>(gated);
-        case GEMM_BT_FP8_E4M3: return skinny_of<GEMM_BT_FP8_E4M3>(gated);
-        case GEMM_BT_FP8_E5M2: return skinny_of<GEMM_BT_FP8_E5M2>(gated);
-        case GEMM_BT_INT8: return skinny_of<GEMM_BT_INT8>(gated);
+        case GEMM_BT_BF16: return gated_of<GEMM_BT_BF16>(shape);
+        case GEMM_BT_F16: return gated_of<GEMM_BT_F16>(shape);
+        case GEMM_BT_FP8_E4M3: return gated_of<GEMM_BT_FP8_E4M3>(shape);
+        case GEMM_BT_FP8_E5M2: return gated_of<GEMM_BT_FP8_E5M2>(shape);
+        case GEMM_BT_INT8: return gated_of<GEMM_BT_INT8>(shape);
         default: return nullptr;
     }
 }
@@ -107,8 +128,12 @@ static const void* block_fn_of(int tile, bool split) {
 const void* block_dma_fn(int tile, bool tall, bool split) {
     return tall ? block_fn_of<1>(tile, split) : block_fn_of<2>(tile, split);
 }
-const void* block_skinny_fn(bool tall) {
-    return tall ? (const void*)&skinny_block_kernel<1, 8, 512, 3> : (const void*)&skinny_block_kernel<0, 8, 512, 3>;
+const void* block_skinny_fn(bool tall, int shape) {
+    return with_stream(shape, [&](auto c) {
+        constexpr StreamShape s = kStream[c()];
+        return tall ? (const void*)&skinny_block_kernel<1, s.rows, s.bytes, s.stages>
+                    : (const void*)&skinny_block_kernel<0, s.rows, s.bytes, s.stages>;
+    });
 }
 
 // K == 0: the epilogue of empty sums.

@@ -67,7 +67,7 @@ __device__ __forceinline__ f32x4 skinny_mma(u32x4 b, u32x4 a, f32x4 c) {
 // The kernel's body.  `epi` is the epilogue's arguments (EpiArgs, or SkinnyGated
 // for the gated one), or nothing (SkinnyPlain): then the sums are rounded into C
 // as they are.  Gated: the BN rows of B are BN / 2 of its first N rows and the same
-// of its second N rows, so a lane finds the other product of its outputs 16 lanes
+// of its second N rows, so a lane finds the other product of its outputs 2 BN lanes
 // on.
 struct SkinnyPlain {};
 struct SkinnyGated {
@@ -107,7 +107,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     constexpr int PEND = (STAGES - 2) * LOADS;
     constexpr int OSZ = OUT == GEMM_BT_F32 ? 4 : 2;
     static_assert(RPI >= 1 && ROWB * RPI == 1024, "stage rows must tile 1 KiB loads");
-    static_assert(BN % RPI == 0 && (BN % 16 == 0 || BN < 16), "B rows per workgroup");
+    static_assert(STAGES >= 2 && BN % RPI == 0 && (BN % 16 == 0 || BN < 16), "B rows per workgroup");
     static_assert((A_LOADS + B_LOADS) % W == 0, "loads split evenly over waves");
     static_assert(KBLK % W == 0, "k-blocks split evenly over waves");
     static_assert(CPR >= 16, "swizzle needs 16 chunks per row");
@@ -128,7 +128,7 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr bool GATE = std::is_same_v<Epi, SkinnyGated>;
     constexpr int BNR = GATE ? BN / 2 : BN;  // columns of C per workgroup
-    static_assert(!GATE || (BN == 8 && BNR % RPI == 0), "4 columns, and a load lies in one half of B");
+    static_assert(!GATE || (NBLK == 1 && BNR % 4 == 0 && BNR % RPI == 0), "whole lanes, and a load lies in one half of B");
     const int n0 = blockIdx.x * BNR;
     const int rows_a = min(AR, M), rows_b = min(BNR, N - n0);
     const i32x4 ra = rsrc_words(A, (u32)rows_a * (u32)K * (u32)ESZ);
@@ -235,10 +235,11 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     // of row lane % 16 (the first block of B rows is the only one there is)
     constexpr bool EPI = !std::is_same_v<Epi, SkinnyPlain>;
     static_assert(!EPI || (NBLK == 1 && W == 1), "one wave stores 4 outputs per lane");
-    // (gated: lanes 16 .. 31 hold the second products of lanes 0 .. 15, with terms of their own)
-    const int epi_n = !EPI || r16 >= M || 4 * q >= BN ? 0 : GATE ? min(4, N - n0) : min(4, N - n0 - 4 * q);
+    // (gated: the second half of the lanes that hold results have the second products, with terms of their own)
+    const int up_q = GATE && 4 * q >= BNR ? 1 : 0, col = GATE ? n0 + 4 * q - up_q * BNR : n0 + 4 * q;
+    const int epi_n = !EPI || r16 >= M || 4 * q >= BN ? 0 : min(4, N - col);
     Epi4 terms;
-    if constexpr (GATE) terms = load_epi4(N, r16, n0 + (q == 1 ? N : 0), epi_n, epi.e);
+    if constexpr (GATE) terms = load_epi4(N, r16, col + up_q * N, epi_n, epi.e);
     else if constexpr (BLOCKS) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi.e);
     else if constexpr (EPI) terms = load_epi4(N, r16, n0 + 4 * q, epi_n, epi);
 
@@ -285,6 +286,8 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     int cs = 0, ls = STAGES - 1;
     for (int kt = 0; kt < nk; ++kt) {
         wait_vmcnt<PEND + (BLOCKS ? 2 * (STAGES - 2) : 0)>();
+        // two stages: the one refilled next is the one just read
+        if constexpr (STAGES == 2) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         barrier_no_fence();
         issue(ls, kt + STAGES - 1);
         compute(cs);
@@ -309,14 +312,14 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e] * terms.rs, terms.cs[e], terms.cb[e]);
             if (epi_n > 0 && (md & EPI_PREACT))
-                store4(epi.e.preact, epi_type(md, EPI_PREACT_TYPE), (size_t)(2 * r16 + q) * N + n0, epi_n, v);
+                store4(epi.e.preact, epi_type(md, EPI_PREACT_TYPE), (size_t)(2 * r16 + up_q) * N + col, epi_n, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) up[e] = __shfl(v[e], (lane + 16) & 63);
+            for (int e = 0; e < 4; ++e) up[e] = __shfl(v[e], (lane + 4 * BNR) & 63);
             with_act(md >> EPI_ACT, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(act)::value>(v[e]) * up[e];
             });
-            if (epi_n > 0 && q == 0) store4(C, epi_type(md, EPI_OUT_TYPE), (size_t)r16 * N + n0, epi_n, v);
+            if (epi_n > 0 && up_q == 0) store4(C, epi_type(md, EPI_OUT_TYPE), (size_t)r16 * N + col, epi_n, v);
         } else if constexpr (BLOCKS) {
             if (epi_n > 0) store_epi4(v, terms, C, N, r16, n0 + 4 * q, epi_n, epi.e);
         } else {

@@ -177,7 +177,8 @@ def check(gpu, M, N, K, high, outd, act, bias=None, res=None, pre=False, seed=0,
 SHAPES = [(1, 1, 16), (520, 4096, 208), (1100, 1500, 400), (4400, 4096, 64), (2100, 4350, 336), (1040, 2000, 144), (1, 72, 4096), (16, 8192, 512), (1, 4104, 4096), (5, 6001, 272), (16, 4099, 8208), (3, 5000, 128), (64, 512, 8192),
           (33, 4096, 4096), (200, 300, 8208), (7, 70, 16384), (129, 1000, 4112), (33, 65, 144), (130, 264, 208), (300, 333, 128),
           (700, 1100, 128), (1000, 2050, 400), (2050, 2050, 64), (2048, 4352, 80), (4100, 4096, 48), (4096, 4097, 32), (1000, 3000, 2064),
-          (2048, 4096, 1024), (5000, 3333, 144)]
+          (2048, 4096, 1024), (5000, 3333, 144),
+          (16, 12300, 528), (2, 16390, 2064), (13, 32768, 400), (9, 24580, 4112)]
 
 
 @pytest.mark.gpu
@@ -199,7 +200,7 @@ def test_shapes_cover_every_kernel():
         seen |= {(high, q.kernel, q.variant, q.split_tiles > 0, p.split_rows > 0) for q in parts}
     kinds = {(h, k, v, s) for h, k, v, s, _ in seen}
     tiles = {(h, 4, v, False) for h in (1, 128) for v in (0, 1, 2, 4)} | {(128, 4, 3, False)}
-    assert kinds == tiles | {(h, 4, 4, True) for h in (1, 128)} | {(h, 3, 0, False) for h in (1, 128)}, kinds
+    assert kinds == tiles | {(h, 4, 4, True) for h in (1, 128)} | {(h, 3, v, False) for h in (1, 128) for v in (0, 1, 2)}, kinds
     assert {h for h, _, _, _, rows in seen if rows} == {1, 128}
 
 

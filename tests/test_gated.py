@@ -20,7 +20,7 @@ F8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 CODE = {"bf16": gb.BF16, "f16": gb.F16, "e4m3": gb.FP8_E4M3, "e5m2": gb.FP8_E5M2, "i8": gb.INT8}
 
 # the same tile shapes with 2 N columns
-SHAPES = [(M, (N + 1) // 2, K) for M, N, K in SHAPES16] + [(16, 4097, 2048), (33, 7, 40), (1, 3, 8), (300, 5, 72)]
+SHAPES = [(M, (N + 1) // 2, K) for M, N, K in SHAPES16] + [(16, 4097, 2048), (16, 6150, 1031), (3, 8195, 2056), (7, 16384, 200), (11, 12290, 4096), (33, 7, 40), (1, 3, 8), (300, 5, 72)]
 
 
 def inputs(M, N, K, ind, seed):
@@ -119,7 +119,7 @@ def test_shapes_cover_every_kernel():
 @pytest.mark.parametrize("ind", ["e4m3", "e5m2", "i8"])
 @pytest.mark.parametrize("shape", [(1, 1, 16), (1, 36, 4096), (33, 33, 144), (130, 132, 208), (700, 550, 128), (2050, 1025, 64),
                                    (2048, 2176, 80), (4100, 2048, 48), (16, 4096, 512), (1, 2052, 4096), (5, 3001, 272), (64, 256, 8192),
-                                   (33, 2048, 4096), (7, 35, 16384), (4352, 2048, 64)])
+                                   (33, 2048, 4096), (7, 35, 16384), (4352, 2048, 64), (16, 6150, 1040), (3, 8195, 2064), (7, 16384, 208)])
 def test_gated_eight_bits(gpu, ind, shape):
     n = sum(shape)
     for i in (n, n + 5):
