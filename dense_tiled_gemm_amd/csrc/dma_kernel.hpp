@@ -677,7 +677,7 @@ __global__ __launch_bounds__(64 * WM * WN) void dma_kernel(const u16* __restrict
             mma_step(b, a, c >= 0, [&](int d) { load_one(stage, kt, c * CH + d); },
                      [&](auto rc) { read_one(rst, rst + BM * ROWB, rks, rc, rfb, rfa); }, first);
         };
-        constexpr auto kFirst = std::true_type{};
+        constexpr auto kFirst = std::bool_constant<WHOLE>{};  // (one type where it makes no difference)
         constexpr auto kLater = std::false_type{};
         static_assert(!WHOLE || (KS == 2 && FD == 1), "one substep of a block before the barrier, one after it");
         if constexpr (RING5) {
