@@ -397,7 +397,9 @@ __device__ __forceinline__ void store_tile_epi(const typename AccBlock<MF>::type
 //   Zg = row_scale[i] col_scale[j] sum + bias[j],  Zu the same with j + N,
 //   C[i][j] = act(Zg) Zu,
 // and preact holds rows of 2 N elements, Zg and then Zu.  As store_tile_epi in
-// everything else; both halves meet in LDS, so an output costs one pass.
+// everything else; both halves meet in LDS, so an output costs one pass and half
+// the stores of the product with 2 N columns (4096 x 4096 of C, K = 4096, us: bf16 205
+// against 199 for those 2 N columns alone, E4M3 112 against 119).
 template <bool INT, int FN, int FM, int BM, int BN, int WM, int NT, int LDS_BYTES, int MF>
 __device__ __forceinline__ void store_tile_gated(const typename AccBlock<MF>::type (&acc)[FN][FM], unsigned char* lds, void* C,
                                                  int M, int N, int m0, int n0, int mw, int nw, int wm, int tid, const EpiArgs& e) {
