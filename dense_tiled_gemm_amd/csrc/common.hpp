@@ -150,6 +150,21 @@ struct Mfma<GEMM_BT_INT8> {
     __device__ static inline f32x16 m32x32x64(u32x8 a, u32x8 b, f32x16 c) { return half<1>(a, b, half<0>(a, b, c)); }
 };
 
+// Eight E4M3 values (two dwords, in k order) as f16, exactly.
+__device__ __forceinline__ u32x4 widen_e4m3(u32 lo, u32 hi) {
+    auto two = [](u32 w, auto high) __attribute__((always_inline)) {
+        return __builtin_bit_cast(u32, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, decltype(high)::value));
+    };
+    return u32x4{two(lo, std::false_type{}), two(lo, std::true_type{}), two(hi, std::false_type{}), two(hi, std::true_type{})};
+}
+// The 32x32x64 product of E4M3 operands in f16: 8 of the lane's 32 values at a time,
+// the same ones of A and of B, so the sum over all is the full one.
+__device__ __forceinline__ f32x16 widened_m32x32x64(u32x8 a, u32x8 b, f32x16 c) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) c = Mfma<GEMM_BT_F16>::m32x32x16(widen_e4m3(a[i], a[i + 1]), widen_e4m3(b[i], b[i + 1]), c);
+    return c;
+}
+
 // Bytes per input element, and the per-lane MFMA operand fragment: 8 elements
 // (16 bytes) of 16-bit data, 32 elements (32 bytes) of 8-bit data.
 constexpr int in_size(int in) {

@@ -26,6 +26,16 @@ struct StreamShape {
 constexpr int kStreams = 3;
 constexpr StreamShape kStream[kStreams] = {{8, 512, 3, 4, 1.55}, {16, 256, 3, 6, 1.92}, {16, 512, 2, 4, 2.2}};
 
+// f(std::integral_constant<int, i>{}) for the shape kStream[i]
+template <class F>
+inline const void* with_stream(int shape, F&& f) {
+    switch (shape) {
+        case 0: return f(std::integral_constant<int, 0>{});
+        case 1: return f(std::integral_constant<int, 1>{});
+        default: return f(std::integral_constant<int, 2>{});
+    }
+}
+
 // The shape with the shortest estimate for `rows` rows of `bytes` each.  Workgroups
 // that fill the CUs stream a round of rows at HBM's rate (5.1 TB/s; the first
 // shape, with the fewest rows in flight, 4.1); a round that does not takes 4 us and
@@ -53,7 +63,7 @@ inline int pick_stream(int64_t rows, int64_t bytes, int num_cu) {
 // K == 0: (void* C, int M, int N, EpiArgs), a grid of any size.
 const void* epi_fill_fn(bool gated);
 
-// The 8-bit product with scales per block of 128: tiles of blockTile(i) with B's
+// The 8-bit product with scales per block of 128: tiles of kBlockTile[i] with B's
 // scales per 128 rows (tall) or per row, their split form, and the streaming
 // kernel for M <= 16.
 constexpr int kBlockTiles = 5;
@@ -61,9 +71,10 @@ struct BlockTile {
     int bm, bn, bk, threads, stages;
 };
 constexpr BlockTile kBlockTile[kBlockTiles] = {
-    {256, 128, 128, 512, 3}, {128, 128, 128, 256, 4}, {64, 64, 128, 256, 4}, {256, 256, 128, 512, 2}, {64, 64, 256, 256, 4}};  // (3: tall alone)
-const void* block_dma_fn(int tile, bool tall, bool split);
-const void* block_skinny_fn(bool tall, int shape);
+    {256, 128, 128, 512, 3}, {128, 128, 128, 256, 4}, {64, 64, 128, 256, 4}, {256, 256, 128, 512, 2}, {64, 64, 256, 256, 4}};  // (3: tall and not wide alone)
+// `wide`: for fp32 results (kBlkWide).
+const void* block_dma_fn(int tile, bool tall, bool split, bool wide);
+const void* block_skinny_fn(bool tall, int shape, bool wide);
 
 // The same epilogue for the rows from m1 on, N columns each (of the kept
 // pre-activation, where it is gated).

@@ -1235,20 +1235,30 @@ static int launch_inner(const void* A, const void* B, void* C, int64_t batch, in
 
 // What a wave of a tile shape (one workgroup per CU, of 64 x 64 tiles in steps of
 // 128 two) takes in us: `start` for its prologue and epilogue, `step` for each
-// block of 128 along K with B's scales per 128 rows, `step_rows` with one per row.
-// Measured in whole calls, tall and per row (us, 64 x 64 in steps of 256, 64 x 64, 128
-// x 128, 256 x 128, 256 x 256): 256x4096x4096 13.3 13.7, 15.3 16.6, 25.8 29.4, 29.6
-// 35.5, 54.0; 1024x2048x4096 21.4 23.3, 18.6 20.7, 24.8 29.5, 29.8 35.7, 54.0;
-// 1024x4096x4096 46 48, 39 41, 28 32, 32 38, 54; 1536x4096x4096 -, 54 60, 53 61, 35
-// 41, 55; 2048x4352x4096 -, 77 85, 75 89, 68 81, 59; 4096^3 -, 136 147, 106 123, 80 94,
-// 75; 6144x4096x4096 -, 198 218, 157 182, 119 140, 127; 8192x8192x4096 -, 532 584, 423
-// 485, 312 365, 291.
+// block of 128 along K: B's scales per 128 rows, per row, and both with operands
+// widened for fp32 results.  Measured in whole calls, per 128 rows and per row (us,
+// 64 x 64 in steps of 256, 64 x 64, 128 x 128, 256 x 128, 256 x 256): 256x4096x4096 13.3
+// 13.7, 15.3 16.6, 25.8 29.4, 29.6 35.5, 54.0; 1024x2048x4096 21.4 23.3, 18.6 20.7, 24.8
+// 29.5, 29.8 35.7, 54.0; 1024x4096x4096 46 48, 39 41, 28 32, 32 38, 54;
+// 1536x4096x4096 -, 54 60, 53 61, 35 41, 55; 2048x4352x4096 -, 77 85, 75 89, 68 81, 59;
+// 4096^3 -, 136 147, 106 123, 80 94, 75; 6144x4096x4096 -, 198 218, 157 182, 119 140,
+// 127; 8192x8192x4096 -, 532 584, 423 485, 312 365, 291.  fp32 results: 256x4096x4096
+// 19.8 21.2, 23.0 23.4, 41.6 -, 52.1 -; 1024x4096x4096 70 74, 53 59, 44 -, 53 -; 4096^3 255
+// 277, 187 204, 162 -, 140 -.
+struct BlockMode {
+    bool tall, wide;
+    int index() const { return (tall ? 0 : 1) + (wide ? 2 : 0); }
+};
 struct BlockCost {
-    double start, step, step_rows;
+    double start, step[4];
     int per_cu;
 };
-constexpr BlockCost kBlockCost[kBlockTiles] = {
-    {6.0, 0.96, 1.14, 1}, {4.0, 0.67, 0.78, 1}, {2.0, 0.47, 0.52, 2}, {8.0, 1.94, 1e9, 1}, {2.0, 0.235, 0.25, 1}};
+constexpr double kNone = 1e9;  // no such kernel
+constexpr BlockCost kBlockCost[kBlockTiles] = {{6.0, {0.96, 1.14, 1.90, kNone}, 1},
+                                               {4.0, {0.67, 0.78, 1.09, kNone}, 1},
+                                               {2.0, {0.47, 0.52, 0.69, 0.74}, 2},
+                                               {8.0, {1.94, kNone, kNone, kNone}, 1},
+                                               {2.0, {0.235, 0.25, 0.40, 0.44}, 1}};
 
 static int64_t block_tiles(int tile, int64_t M, int64_t N) {
     const BlockTile& t = kBlockTile[tile];
@@ -1257,17 +1267,17 @@ static int64_t block_tiles(int tile, int64_t M, int64_t N) {
 // A last wave that fills a part f of the CUs takes about 0.7 + 0.3 f of a full one
 // (256 x 128 tiles at K = 4096: 128 tiles 32.4 us, 192 35.1, 256 41.4; 256 x 256 ones:
 // 128 54.4, 160 59.9, 256 74.9): the full chip runs at a lower clock.
-static double block_time(int tile, int64_t M, int64_t N, int64_t K, bool tall, int num_cu) {
+static double block_time(int tile, int64_t M, int64_t N, int64_t K, BlockMode mode, int num_cu) {
     const BlockCost& c = kBlockCost[tile];
     const int64_t n = block_tiles(tile, M, N), wave = (int64_t)num_cu * c.per_cu, rest = n % wave;
     const double waves = (double)(n / wave) + (rest ? 0.7 + 0.3 * (double)rest / (double)wave : 0.0);
-    return waves * (c.start + (double)((K + 127) / 128) * (tall ? c.step : c.step_rows));
+    return waves * (c.start + (double)((K + 127) / 128) * c.step[mode.index()]);
 }
-static int block_best(int64_t M, int64_t N, int64_t K, bool tall, int num_cu, double* time) {
+static int block_best(int64_t M, int64_t N, int64_t K, BlockMode mode, int num_cu, double* time) {
     int best = 0;
     for (int i = 1; i < kBlockTiles; ++i)
-        if (block_time(i, M, N, K, tall, num_cu) < block_time(best, M, N, K, tall, num_cu)) best = i;
-    if (time) *time = block_time(best, M, N, K, tall, num_cu);
+        if (block_time(i, M, N, K, mode, num_cu) < block_time(best, M, N, K, mode, num_cu)) best = i;
+    *time = block_time(best, M, N, K, mode, num_cu);
     return best;
 }
 
@@ -1312,8 +1322,9 @@ static int plan_block(int64_t M, int64_t N, int64_t K, bool tall, int out_dtype,
         p->tiles_n = p->grid = (N + s.rows - 1) / s.rows;
         return GEMM_BT_OK;
     }
+    const BlockMode mode = {tall, out_dtype == GEMM_BT_F32};
     double whole = 0.0;
-    const int use = block_best(M, N, K, tall, num_cu, &whole);
+    const int use = block_best(M, N, K, mode, num_cu, &whole);
     if (allow_rows) {
         int64_t rows = 0;
         double least = whole;
@@ -1322,8 +1333,8 @@ static int plan_block(int64_t M, int64_t N, int64_t K, bool tall, int out_dtype,
             const int64_t m1 = block_tiles(i, M, N) / num_cu * num_cu / tn * kBlockTile[i].bm;
             if (m1 <= 0 || m1 >= M) continue;
             double rest = 0.0;
-            block_best(M - m1, N, K, tall, num_cu, &rest);
-            const double both = block_time(i, m1, N, K, tall, num_cu) + rest + 3.0;  // (a launch)
+            block_best(M - m1, N, K, mode, num_cu, &rest);
+            const double both = block_time(i, m1, N, K, mode, num_cu) + rest + 3.0;  // (a launch)
             if (both < least) {
                 least = both;
                 rows = m1;
@@ -1366,6 +1377,7 @@ static int plan_block(int64_t M, int64_t N, int64_t K, bool tall, int out_dtype,
 static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int out_dtype, const EpiArgs& epi,
                         const BlkArgs& blk, bool tall, void* ws, size_t ws_bytes, void* stream, bool allow_rows = true) {
     gemm_bt_plan_t p;
+    const bool wide = out_dtype == GEMM_BT_F32;
     int st = plan_block(M, N, K, tall, out_dtype, align_of(A), align_of(B), 256, ws != nullptr, allow_rows, &p);
     if (st != GEMM_BT_OK) return st;
     if (p.kernel == KIND_NONE) return GEMM_BT_OK;
@@ -1405,7 +1417,7 @@ static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_
     if (p.kernel == KIND_SKINNY) {
         BlkArgs ba = blk;
         void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &ea, &ba};
-        return launch(block_skinny_fn(tall, p.variant), dim3((unsigned)p.grid), p.threads, args, stream);
+        return launch(block_skinny_fn(tall, p.variant, wide), dim3((unsigned)p.grid), p.threads, args, stream);
     }
     SkBlkArgs s;
     (SkArgs&)s = sk_args(p, K, ws);
@@ -1414,7 +1426,8 @@ static int launch_block(const void* A, const void* B, void* C, int64_t M, int64_
     int tm = (int)p.tiles_m, tn = (int)p.tiles_n, gm = p.group_m, vec_store = 0;
     long long zero = 0;
     void* args[] = {&a, &b, &C, &Mi, &Ni, &Ki, &tm, &tn, &gm, &vec_store, &tm, &zero, &zero, &zero, &s};
-    return launch(block_dma_fn(p.variant, tall, p.split_tiles > 0), dim3((unsigned)p.grid), p.threads, args, stream);
+    const void* fn = block_dma_fn(p.variant, tall, p.split_tiles > 0, wide);
+    return fn ? launch(fn, dim3((unsigned)p.grid), p.threads, args, stream) : GEMM_BT_ERR_UNSUPPORTED;
 }
 
 }  // namespace gbt

@@ -83,15 +83,6 @@ const void* epi_skinny_fn(int in_dtype) {
     }
 }
 
-// f(std::integral_constant<int, i>{}) for the shape kStream[i]
-template <class F>
-static const void* with_stream(int shape, F&& f) {
-    switch (shape) {
-        case 0: return f(std::integral_constant<int, 0>{});
-        case 1: return f(std::integral_constant<int, 1>{});
-        default: return f(std::integral_constant<int, 2>{});
-    }
-}
 template <int IN>
 static const void* gated_of(int shape) {
     return with_stream(shape, [](auto c) {
@@ -108,32 +99,6 @@ const void* gated_skinny_fn(int in_dtype, int shape) {
         case GEMM_BT_INT8: return gated_of<GEMM_BT_INT8>(shape);
         default: return nullptr;
     }
-}
-
-template <int BM, int BN, int BK, int S, int WM, int WN, int SCHED, int SK, int BLK>
-static const void* block_fn() {
-    return (const void*)&dma_kernel<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BM, BN, BK, S, WM, WN, 2, SCHED, 0, 32, 0, 0, SK, 0, 1, BLK>;
-}
-template <int BLK>
-static const void* block_fn_of(int tile, bool split) {
-    if (split) return tile == 4 ? block_fn<64, 64, 256, 4, 2, 2, 4, 1, BLK>() : nullptr;
-    switch (tile) {
-        case 0: return block_fn<256, 128, 128, 3, 4, 2, 8, 0, BLK>();
-        case 1: return block_fn<128, 128, 128, 4, 2, 2, 8, 0, BLK>();
-        case 2: return block_fn<64, 64, 128, 4, 2, 2, 4, 0, BLK>();
-        case 4: return block_fn<64, 64, 256, 4, 2, 2, 4, 0, BLK>();
-        default: return BLK == 1 ? block_fn<256, 256, 128, 2, 2, 4, 6, 0, 1>() : nullptr;
-    }
-}
-const void* block_dma_fn(int tile, bool tall, bool split) {
-    return tall ? block_fn_of<1>(tile, split) : block_fn_of<2>(tile, split);
-}
-const void* block_skinny_fn(bool tall, int shape) {
-    return with_stream(shape, [&](auto c) {
-        constexpr StreamShape s = kStream[c()];
-        return tall ? (const void*)&skinny_block_kernel<1, s.rows, s.bytes, s.stages>
-                    : (const void*)&skinny_block_kernel<0, s.rows, s.bytes, s.stages>;
-    });
 }
 
 // K == 0: the epilogue of empty sums.

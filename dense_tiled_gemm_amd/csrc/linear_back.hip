@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "device.hpp"
+#include "gemm_block.hpp"
 #include "rows.hpp"
 #include "trans_kernel.hpp"
 

@@ -76,16 +76,18 @@ struct SkinnyGated {
 // One scale per block of 128 (see BLK in dma_kernel.hpp): a stage holds whole
 // blocks, and the scales of its rows come with it, 4 bytes per lane.  A block's
 // sums start from zero and are added to the others times both scales.
-template <int TALL>
+template <bool TALL, bool WIDE>
 struct SkinnyBlocks {
     EpiArgs e;
     BlkArgs b;
 };
 template <class T>
-struct is_blocks : std::false_type {};
-template <int TALL>
-struct is_blocks<SkinnyBlocks<TALL>> : std::true_type {
-    static constexpr int tall = TALL;
+struct is_blocks : std::false_type {
+    static constexpr bool wide = false;
+};
+template <bool TALL, bool WIDE>
+struct is_blocks<SkinnyBlocks<TALL, WIDE>> : std::true_type {
+    static constexpr bool tall = TALL, wide = WIDE;  // wide: fp32 results (see kBlkWide)
 };
 template <int IN, int OUT, int BN, int KB, int STAGES, int W, int ROT, class Epi>
 __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
@@ -263,7 +265,12 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
                 const int chb = ((4 * kb + q) ^ (brow & 15)) * 16;
                 const u32x4 fb = *(const u32x4*)(s + brow * ROWB + chb);
                 if constexpr (BLOCKS) {
-                    part = skinny_mma<IN>(fb, fa, part);
+                    if constexpr (is_blocks<Epi>::wide) {
+                        part = Mfma<GEMM_BT_F16>::m16x16x32(widen_e4m3(fb[0], fb[1]), widen_e4m3(fa[0], fa[1]), part);
+                        part = Mfma<GEMM_BT_F16>::m16x16x32(widen_e4m3(fb[2], fb[3]), widen_e4m3(fa[2], fa[3]), part);
+                    } else {
+                        part = skinny_mma<IN>(fb, fa, part);
+                    }
                     if (t % 2 == 1) {  // a block is two k-blocks of 64 bytes
                         const float sa = scales[stage][t / 2 * AR + r16];
                         const f32x4 sb = *(const f32x4*)&scales[stage][64 + t / 2 * BN + 4 * q % BN];
@@ -396,11 +403,11 @@ __global__ __launch_bounds__(64 * W) void skinny_gated_kernel(const u16* __restr
     skinny_body<IN, GEMM_BT_F32, BN, KB, STAGES, W, 0>(A, B, C, M, N, K, 0, SkinnyGated{epi});  // (OUT is not used)
 }
 
-// E4M3 with scales per block, B's per 128 rows (TALL) or per row.
-template <int TALL, int BN, int KB, int STAGES>
+// E4M3 with scales per block, B's per 128 rows (TALL) or per row; WIDE: fp32 results.
+template <bool TALL, bool WIDE, int BN, int KB, int STAGES>
 __global__ __launch_bounds__(64) void skinny_block_kernel(const u16* __restrict__ A, const u16* __restrict__ B, void* __restrict__ C,
                                                          int M, int N, int K, const EpiArgs epi, const BlkArgs blk) {
-    skinny_body<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BN, KB, STAGES, 1, 0>(A, B, C, M, N, K, 0, SkinnyBlocks<TALL>{epi, blk});
+    skinny_body<GEMM_BT_FP8_E4M3, GEMM_BT_F32, BN, KB, STAGES, 1, 0>(A, B, C, M, N, K, 0, SkinnyBlocks<TALL, WIDE>{epi, blk});
 }
 
 }  // namespace gbt

@@ -2,8 +2,9 @@
 
 Where the tolerances come from (u = 2^-24).  A scale is one division; codes are taken from v times 448 / amax, two roundings
 before that of E4M3.  A product's sums of 8-bit floats are known to within eight_bit_tol of the scaled operands (a block's
-scales are one factor of its sums): its K u has one rounding per term, the K / 128 + 4 for the blocks' sums and the scales
-come on top.  Bias, activation and residual as for the other products.
+scales are one factor of its sums), sums for fp32 results, whose operands are widened, to within sum_tol: its K u has one
+rounding per term, the K / 128 + 4 for the blocks' sums and the scales come on top.  Bias, activation and residual as for
+the other products.
 """
 import ctypes
 import itertools
@@ -12,7 +13,7 @@ import pytest
 import torch
 
 import dense_tiled_gemm_amd as gb
-from test_gated import eight_bit_tol
+from test_gated import eight_bit_tol, sum_tol
 from test_layers_gpu import ACTS, DT, act64, close, gen, guarded, options, randn, say, u
 
 BAD, UNSUP = gb.ERR_INVALID_VALUE, gb.ERR_UNSUPPORTED
@@ -141,6 +142,12 @@ def operands(gpu, M, N, K, high, seed):
     return x, w, sx, sw
 
 
+def product_tol(x, w, out):
+    """Of the sums of x and w (scaled, in 64 bits) for results of type out."""
+    tol = (sum_tol if out == torch.float32 else eight_bit_tol)(x, w)
+    return tol + (x.shape[1] / 128 + 4) * u * torch.mm(x.abs(), w.abs().t().contiguous())
+
+
 def strided(t):
     return t.cuda().t().contiguous().t()
 
@@ -159,7 +166,7 @@ def check(gpu, M, N, K, high, outd, act, bias=None, res=None, pre=False, seed=0,
     xd = (x.double() * spread(sx, M, K, 1)).cuda()
     wd = (w.double() * spread(sw, N, K, high)).cuda()
     z = torch.mm(xd, wd.t().contiguous()).cpu()
-    tol = (eight_bit_tol(xd, wd) + (K / 128 + 4) * u * torch.mm(xd.abs(), wd.abs().t().contiguous())).cpu()
+    tol = product_tol(xd, wd, DT[outd]).cpu()
     if b is not None:
         z = z + b.double()
         tol = tol + u * z.abs()
@@ -186,7 +193,7 @@ SHAPES = [(1, 1, 16), (520, 4096, 208), (1100, 1500, 400), (4400, 4096, 64), (21
 @pytest.mark.parametrize("high", [128, 1])
 def test_block_linear(gpu, high, shape):
     n = sum(shape)
-    for i in (n, n + 1, n + 5):
+    for i in (n, n + 1, n + 2):  # one of each type of result
         o = options(i)
         o["bias"] = "bf16" if o["bias"] == "own" else o["bias"]
         check(gpu, *shape, high, seed=n, rowwise=i % 2 == 1, **o)
@@ -194,14 +201,16 @@ def test_block_linear(gpu, high, shape):
 
 def test_shapes_cover_every_kernel():
     seen = set()
-    for (M, N, K), high in itertools.product(SHAPES, (1, 128)):
-        p = gb.gemm_bt_plan_block(M, N, K, high, gb.BF16)
-        parts = [p] + ([gb.gemm_bt_plan_block(M - p.split_rows, N, K, high, gb.BF16)] if p.split_rows else [])
-        seen |= {(high, q.kernel, q.variant, q.split_tiles > 0, p.split_rows > 0) for q in parts}
-    kinds = {(h, k, v, s) for h, k, v, s, _ in seen}
-    tiles = {(h, 4, v, False) for h in (1, 128) for v in (0, 1, 2, 4)} | {(128, 4, 3, False)}
-    assert kinds == tiles | {(h, 4, 4, True) for h in (1, 128)} | {(h, 3, v, False) for h in (1, 128) for v in (0, 1, 2)}, kinds
-    assert {h for h, _, _, _, rows in seen if rows} == {1, 128}
+    for (M, N, K), high, out in itertools.product(SHAPES, (1, 128), (gb.BF16, gb.F32)):
+        p = gb.gemm_bt_plan_block(M, N, K, high, out)
+        parts = [p] + ([gb.gemm_bt_plan_block(M - p.split_rows, N, K, high, out)] if p.split_rows else [])
+        seen |= {(high, out, q.kernel, q.variant, q.split_tiles > 0, p.split_rows > 0) for q in parts}
+    for high, out in itertools.product((1, 128), (gb.BF16, gb.F32)):
+        kinds = {(k, v, s) for h, o, k, v, s, _ in seen if (h, o) == (high, out)}
+        large = {(4, 0, False), (4, 1, False)} if (high, out) != (1, gb.F32) else set()
+        widest = {(4, 3, False)} if (high, out) == (128, gb.BF16) else set()
+        assert kinds == large | widest | {(4, 2, False), (4, 4, False), (4, 4, True)} | {(3, v, False) for v in (0, 1, 2)}, (high, out, kinds)
+    assert {h for h, o, _, _, _, rows in seen if rows} == {1, 128}
 
 
 @pytest.mark.gpu
@@ -238,7 +247,7 @@ def test_scales_of_extreme_size(gpu):
         xd, wd = x.double() * spread(sx, M, K, 1), w.double() * spread(sw, N, K, high)
         xd, wd = torch.nan_to_num(xd), torch.nan_to_num(wd)
         want = xd @ wd.t()
-        tol = eight_bit_tol(xd, wd) + (K / 128 + 4) * u * (xd.abs() @ wd.abs().t())
+        tol = product_tol(xd, wd, torch.float32)
         assert bool(((got.double() - want).abs() <= tol + u * want.abs() + 2.0 ** -126)[~bad].all()), (M, N, high)
 
 
@@ -283,7 +292,7 @@ def test_training_step_in_8_bits(gpu):
             got = gpu.block_linear(qa, b.q, a.scale, b.scale, out_dtype=torch.float32)
             av, bv = value(a, rows, depth, 1), value(b, cols, depth, high)
             want = torch.mm(av, bv.t().contiguous())
-            tol = eight_bit_tol(av, bv) + (depth / 128 + 4) * u * torch.mm(av.abs(), bv.abs().t().contiguous())
+            tol = product_tol(av, bv, torch.float32)
             close(got, want.cpu(), tol.cpu(), (M, N, K, rows, cols))
         # and from the 16-bit values themselves: each code within 2^-4 of its value, or half the smallest step of its block
         q = gpu.quantize_blocks(x)
@@ -306,7 +315,7 @@ def test_large_offsets(gpu):
     wd = w.double().cpu() * spread(sw, N, K, 128)
     for rows in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
         xd = x[rows].double().cpu() * spread(sx[rows], 300, K, 1)
-        close(y[rows], xd @ wd.t(), eight_bit_tol(xd, wd) + 6 * u * (xd @ wd.t()), "y")
+        close(y[rows], xd @ wd.t(), product_tol(xd, wd, y.dtype), "y")
 
 
 @pytest.mark.gpu
