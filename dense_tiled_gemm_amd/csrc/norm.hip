@@ -90,10 +90,10 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[16]) {
 
 // Elements i .. i+7 of a row of d that starts at element `base` of p.  RAGGED
 // (d >= 8, no multiple of 8): the last chunk is loaded from element d - 8 on and
-// moved into place when it is decoded.  WHOLE: every chunk is known to be 8 elements.  A load is then one instruction for
-// every lane, and nothing waits for it before its use, where a branch that put
-// single elements together waits for everything in flight.  Rows of whole
-// chunks have kernels without the moves.
+// moved into place when it is decoded.  WHOLE: every chunk is known to be 8 elements.
+// A load is then one instruction for every lane, and nothing waits for it before its
+// use, where a branch that put single elements together waits for everything in
+// flight.  Rows of whole chunks have kernels without the moves.
 template <bool RAGGED, bool WHOLE = false>
 __device__ __forceinline__ Raw8 load_chunk(const void* p, int t, long long base, int i, int d, bool nt = false) {
     if constexpr (WHOLE) return load_raw8(p, t, (size_t)base + i, 8, nt);
@@ -212,7 +212,7 @@ struct NormArgs {
     float* mean;           // layer norm alone; nullptr: not kept
 };
 
-__device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
+__host__ __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
 
 // The mean of a row of d values whose sum in fp32 is `sum`.  Where that left
 // fp32's range the values are summed once more, 2^-27 of each (d <= 2^26).
@@ -327,8 +327,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             rstd = rstd_of<WAVE>(ss, d, a.eps, part + 4, flip, each);
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
-        const bool codes = is_code_type(a.y_type);
-        const float factor = codes && a.weight && !CENTER ? power_below(rstd) : rstd;
+        const bool codes = !CENTER && is_code_type(a.y_type);
+        const float factor = codes && a.weight ? power_below(rstd) : rstd;
         float amax = 0.0f;
         static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
             constexpr int u = decltype(uc)::value;
@@ -351,8 +351,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
 #pragma unroll
                         for (int e = 0; e < 8; ++e) h[u][e] += b[e];
                     }
+                if constexpr (!CENTER)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[u][e]));
+                    for (int e = 0; e < 8; ++e) amax = MaxBitsOp::join(amax, __builtin_fabsf(h[u][e]));
                 if (!codes) store8(a.y, a.y_type, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), h[u]);
             }
         });
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
                 if (i < d) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) h[u][e] *= s.code;
-                    store_codes(a.y, a.y_type, (size_t)(row * d) + i, CENTER && WHOLE ? 8 : min(8, d - i), h[u]);
+                    store_codes(a.y, a.y_type, (size_t)(row * d) + i, min(8, d - i), h[u]);
                 }
             });
         }
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
                     for (int e = 0; e < 8; ++e) h[e] += b[e];
                 }
         };
-        const bool codes = is_code_type(a.y_type);
+        const bool codes = !CENTER && is_code_type(a.y_type);
         float rstd = 1.0f, code = 1.0f, h[8];
         auto each = [&](auto&& f) __attribute__((always_inline)) {
             for (long long i = t * 8; i < a.d; i += T * 8) {
@@ -444,7 +445,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
             rstd = rstd_of<false>(ss, a.d, a.eps, part + 4, flip, each);
             if (a.rstd && t == 0) a.rstd[row] = rstd;
         }
-        const float factor = codes && a.weight && !CENTER ? power_below(rstd) : rstd;
+        const float factor = codes && a.weight ? power_below(rstd) : rstd;
         if (codes) {
             float amax = 0.0f;
             for (long long i = t * 8; i < a.d; i += T * 8) {
@@ -478,6 +479,272 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
                 store8(a.y, a.y_type, at, n, h);
             }
         }
+        flip ^= 1;
+    }
+}
+
+// ---- layer norm in 8 bits --------------------------------------------------------
+
+// Sums, and largest magnitudes, over a row's threads in fp64, as row_sums has them in
+// fp32.
+struct Sum64Op {
+    __device__ static double join(double a, double b) { return a + b; }
+};
+struct MaxBits64Op {  // MaxBitsOp of values that are not negative
+    __device__ static double join(double a, double b) {
+        return __builtin_bit_cast(double, max(__builtin_bit_cast(uint64_t, a), __builtin_bit_cast(uint64_t, b)));
+    }
+};
+// f of both halves' bits
+template <class F>
+__device__ __forceinline__ double halves(double v, F&& f) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(u32)f((int)(b >> 32)) << 32 | (u32)f((int)(u32)b));
+}
+template <class Op, int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double join_moved(double v) {
+    return Op::join(v, halves(v, [](int w) __attribute__((always_inline)) {
+                        return __builtin_amdgcn_update_dpp(0, w, CTRL, ROWS, 0xF, false);
+                    }));
+}
+template <class Op>
+__device__ __forceinline__ double join16(double v) {
+    return join_moved<Op, 0x118>(join_moved<Op, 0x114>(join_moved<Op, 0x112>(join_moved<Op, 0x111>(v))));
+}
+template <class Op, bool WAVE, int N>
+__device__ __forceinline__ void row_joins(double (&v)[N], double (*part)[16]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = halves(join_moved<Op, 0x143, 0xC>(join_moved<Op, 0x142, 0xA>(join16<Op>(v[i]))),
+                      [](int w) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(w, 63); });
+    if constexpr (!WAVE) {
+        const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[i][threadIdx.x >> 6] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = halves(join16<Op>(lane < waves ? part[i][lane & 15] : 0.0),
+                          [](int w) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(w, 15); });
+    }
+}
+
+// A row's mean and 1 / sqrt(var + eps) from the sums of h - m0 and of their squares
+// (fp64 holds the squares of every fp32 value).
+struct RowStats {
+    double mean, rstd;
+};
+__device__ __forceinline__ RowStats row_stats(const double (&sums)[2], float m0, const NormArgs& a, long long row, bool keep) {
+    const double off = sums[0] / (double)a.d;
+    const double var = sums[1] / (double)a.d - off * off;
+    // (a NaN stays one)
+    const RowStats s = {m0 + off, 1.0 / __builtin_sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps)};
+    if (keep) {
+        if (a.mean) a.mean[row] = (float)s.mean;
+        if (a.rstd) a.rstd[row] = (float)s.rstd;
+    }
+    return s;
+}
+// What a row's values are multiplied by for their codes, from the largest magnitude;
+// the scale as row_scale_of has it.
+__device__ __forceinline__ double row_code(double amax, const NormArgs& a, long long row, bool keep) {
+    const double q = a.y_type == GEMM_BT_FP8_E4M3 ? 448.0 : 127.0, s = amax / q;
+    const bool fine = as_u32((float)amax) < 0x7F800000u, tiny = !(s >= 0x1p-100);
+    if (keep) a.scale[row] = !fine ? as_f32(0x7FC00000u) : tiny ? 0x1p-100f : (float)s;
+    return !fine ? (double)as_f32(0x7FC00000u) : tiny ? 0x1p100 : q / amax;
+}
+// y = (h - mean) rstd w + b of 8 elements.  Past the row's end w and b are 0, and so is
+// y, or the row's mean is not finite and all of it NaN.
+__device__ __forceinline__ void normed8(const float (&h)[8], const RowStats& s, const float (&w)[8], const float (&b)[8], double (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_fma(((double)h[e] - s.mean) * s.rstd, (double)w[e], (double)b[e]);
+}
+__device__ __forceinline__ void store_codes64(const NormArgs& a, size_t i, int n, const double (&y)[8], double code) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)(y[e] * code);
+    store_codes(a.y, a.y_type, i, n, v);
+}
+
+// Layer norm to E4M3 or int8 codes.  A code is a step function of y: each rounding of
+// y in fp32 moves the codes of those values that lie within it of a step's edge by a
+// whole step, 1/16 of an E4M3 value, about one value in 2^21.  With a bias the
+// row's factors do not cancel in y / amax as they do for the other norm, so
+// everything from the centred values to y / scale is kept in fp64 (the vector unit
+// needs as many instructions as in fp32 and the conversions) and rounded to fp32 once, to
+// the code once more.  Bound by the vector unit: 8192 x 8192 bf16 with residual to E4M3
+// 132 us (3.6 TB/s; 150 with y made twice, in fp32 about as long as the other norm's 83),
+// 8192 x 4096 60, 16384 x 1024 29; one row of 4096 11 us, bound by the call.  Rows as in
+// norm_kernel.
+template <int XT, int U, bool WAVE, bool RAGGED>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const NormArgs a, int w_type) {
+    constexpr bool WHOLE = !RAGGED && !WAVE;  // as in norm_kernel
+    // y stays in registers where a workgroup of 1024 threads has enough, else it is made
+    // twice (w and b come from a cache then)
+    constexpr bool HOLD = U == 1 || XT != GEMM_BT_F32;
+    __shared__ float part[4][16];
+    __shared__ double part64[6][16];
+    const int T = WAVE ? 64 : blockDim.x, RB = WAVE ? blockDim.x >> 6 : 1;
+    const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    const int d = a.d;
+    int flip = 0;
+    for (long long row = (long long)blockIdx.x * RB + (WAVE ? threadIdx.x >> 6 : 0); row < a.rows;
+         row += (long long)gridDim.x * RB) {
+        float h[U][8], sum = 0.0f;
+        {
+            Raw8 xr[U], rr[U];
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int i = (u * T + renew(t)) * 8;
+                if (i < d) {
+                    xr[u] = load_chunk<RAGGED, WHOLE>(a.x, XT, row * a.ldx, i, d);
+                    if (a.residual) rr[u] = load_chunk<RAGGED, WHOLE>(a.residual, XT, row * a.ldr, i, d);
+                }
+            });
+            static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int i = (u * T + renew(t)) * 8;
+                if (i < d) {
+                    decode_chunk<RAGGED>(xr[u], XT, i, d, h[u]);
+                    if (a.residual) {
+                        float v[8];
+                        decode_chunk<RAGGED>(rr[u], XT, i, d, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[u][e] += v[e];
+                    }
+                    if (a.h) store8(a.h, XT, (size_t)(row * d) + i, WHOLE ? 8 : min(8, d - i), h[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[u][e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += h[u][e];
+            });
+        }
+        const float m0 = mean_of<WAVE>(row_sum<WAVE>(sum, part + flip), d, part[2 + flip], [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f(h[u][e]);
+        });
+        double sums[2] = {0.0, 0.0};
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            const int n = d - (u * T + renew(t)) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double c = (WHOLE ? 0 : e) < n ? (double)h[u][e] - (double)m0 : 0.0;
+                sums[0] += c;
+                sums[1] = __builtin_fma(c, c, sums[1]);
+            }
+        });
+        row_joins<Sum64Op, WAVE>(sums, part64 + 2 * flip);
+        const RowStats s = row_stats(sums, m0, a, row, t == 0);
+        double y[HOLD ? U : 1][8], amax[1] = {0.0};
+        auto load_y = [&](int i, const float (&h)[8], double (&y)[8]) __attribute__((always_inline)) {
+            float w[8], b[8];
+            decode_chunk<RAGGED>(load_chunk<RAGGED, WHOLE>(a.weight, w_type, 0, i, d), w_type, i, d, w);
+            if (a.bias)
+                decode_chunk<RAGGED>(load_chunk<RAGGED, WHOLE>(a.bias, w_type, 0, i, d), w_type, i, d, b);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+            normed8(h, s, w, b, y);
+        };
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value, v = HOLD ? u : 0;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                load_y(i, h[u], y[v]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax[0] = MaxBits64Op::join(amax[0], __builtin_fabs(y[v][e]));
+            }
+        });
+        row_joins<MaxBits64Op, WAVE>(amax, part64 + 4 + flip);
+        const double code = row_code(amax[0], a, row, t == 0);
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value, v = HOLD ? u : 0;
+            const int i = (u * T + renew(t)) * 8;
+            if (i < d) {
+                if constexpr (!HOLD) load_y(i, h[u], y[v]);
+                store_codes64(a, (size_t)(row * d) + i, WHOLE ? 8 : min(8, d - i), y[v], code);
+            }
+        });
+        flip ^= 1;  // the next row's joins use other words
+    }
+}
+
+// Rows too long for registers: read once per statistic, h written in the last pass.
+template <int XT, int WT>
+__global__ __launch_bounds__(1024) void norm_codes_long_kernel(const NormArgs a) {
+    constexpr int T = 1024;
+    __shared__ float part[4][16];
+    __shared__ double part64[6][16];
+    const int t = threadIdx.x;
+    int flip = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        // f(first element, elements, their h)
+        auto each8 = [&](auto&& f) __attribute__((always_inline)) {
+            for (long long i = renew(t) * 8; i < a.d; i += T * 8) {
+                const int n = min(8, a.d - (int)i);
+                float h[8];
+                decode8(load_raw8(a.x, XT, (size_t)(row * a.ldx) + i, n), XT, h);
+                if (a.residual) {
+                    float v[8];
+                    decode8(load_raw8(a.residual, XT, (size_t)(row * a.ldr) + i, n), XT, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[e] += v[e];
+                }
+                f((int)i, n, h);
+            }
+        };
+        float sum = 0.0f;
+        auto each = [&](auto&& f) __attribute__((always_inline)) {
+            each8([&](int, int, float (&h)[8]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f(h[e]);  // (0 past the row's end)
+            });
+        };
+        each([&](float v) __attribute__((always_inline)) { sum += v; });
+        const float m0 = mean_of<false>(row_sum<false>(sum, part + flip), a.d, part[2 + flip], each);
+        double sums[2] = {0.0, 0.0};
+        each8([&](int, int n, float (&h)[8]) __attribute__((always_inline)) {
+            n = renew(n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double c = e < n ? (double)h[e] - (double)m0 : 0.0;
+                sums[0] += c;
+                sums[1] = __builtin_fma(c, c, sums[1]);
+            }
+        });
+        row_joins<Sum64Op, false>(sums, part64 + 2 * flip);
+        const RowStats s = row_stats(sums, m0, a, row, renew(t) == 0);
+        auto load_y = [&](int i, int n, const float (&h)[8], double (&y)[8]) __attribute__((always_inline)) {
+            float w[8], b[8];
+            decode8(load_raw8(a.weight, WT, (size_t)i, n), WT, w);
+            if (a.bias)
+                decode8(load_raw8(a.bias, WT, (size_t)i, n), WT, b);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+            normed8(h, s, w, b, y);
+        };
+        double amax[1] = {0.0};
+        each8([&](int i, int n, float (&h)[8]) __attribute__((always_inline)) {
+            double y[8];
+            load_y(i, n, h, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax[0] = MaxBits64Op::join(amax[0], __builtin_fabs(y[e]));
+        });
+        row_joins<MaxBits64Op, false>(amax, part64 + 4 + flip);
+        const double code = row_code(amax[0], a, row, renew(t) == 0);
+        each8([&](int i, int n, float (&h)[8]) __attribute__((always_inline)) {
+            double y[8];
+            load_y(i, n, h, y);
+            if (a.h) store8(a.h, XT, (size_t)(row * a.d) + i, n, h);
+            store_codes64(a, (size_t)(row * a.d) + i, renew(n), y, code);
+        });
         flip ^= 1;
     }
 }
@@ -1179,20 +1446,31 @@ struct RowPlan {
 // Whole waves that hold `chunks` groups of 8 elements, U of them per thread.
 static int threads_for(int64_t chunks, int U) { return (int)((chunks + 64 * U - 1) / (64 * U) * 64); }
 
-template <int XT, int WT, bool R, bool C>
-static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
+// fn(chunks per thread, whether a wave holds a row) for rows in registers, else far.
+template <class F>
+static RowPlan rows_plan(int64_t rows, int64_t d, int num_cu, const void* far, F&& fn) {
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
     const int64_t chunks = (d + 7) / 8;
     // Few rows (at most two per CU): one chunk per thread, so that one load's
     // latency is all that is waited for.
     const bool few = rows <= 2 * num_cu;
-    if (chunks <= 64)
-        return few ? RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R, C>, 64, 1}
-                   : RowPlan{(const void*)&norm_kernel<XT, WT, 1, true, R, C>, 256, 4};
-    if (chunks <= 128 && !few) return {(const void*)&norm_kernel<XT, WT, 2, true, R, C>, 256, 4};
-    if (chunks <= 256 || (few && chunks <= 1024))
-        return {(const void*)&norm_kernel<XT, WT, 1, false, R, C>, threads_for(chunks, 1), 1};
-    if (chunks <= 2048) return {(const void*)&norm_kernel<XT, WT, 2, false, R, C>, threads_for(chunks, 2), 1};
-    return {(const void*)&norm_long_kernel<XT, WT, C>, 1024, 1};
+    if (chunks <= 64) return few ? RowPlan{fn(One{}, std::true_type{}), 64, 1} : RowPlan{fn(One{}, std::true_type{}), 256, 4};
+    if (chunks <= 128 && !few) return {fn(Two{}, std::true_type{}), 256, 4};
+    if (chunks <= 256 || (few && chunks <= 1024)) return {fn(One{}, std::false_type{}), threads_for(chunks, 1), 1};
+    if (chunks <= 2048) return {fn(Two{}, std::false_type{}), threads_for(chunks, 2), 1};
+    return {far, 1024, 1};
+}
+template <int XT, int WT, bool R, bool C>
+static RowPlan norm_plan(int64_t rows, int64_t d, int num_cu) {
+    return rows_plan(rows, d, num_cu, (const void*)&norm_long_kernel<XT, WT, C>,
+                     [](auto u, auto wave) { return (const void*)&norm_kernel<XT, WT, u(), wave(), R, C>; });
+}
+// Layer norm in 8 bits: the kernels that hold a row take w's type as an argument.
+template <int XT, int WT, bool R>
+static RowPlan norm_codes_plan(int64_t rows, int64_t d, int num_cu) {
+    return rows_plan(rows, d, num_cu, (const void*)&norm_codes_long_kernel<XT, WT>,
+                     [](auto u, auto wave) { return (const void*)&norm_codes_kernel<XT, u(), wave(), R>; });
 }
 
 template <int XT, int WT, bool R, bool C>
@@ -1233,10 +1511,13 @@ static int launch_norm(NormArgs& a, int x_type, int w_type, void* stream) {
     int num_cu = 0;
     const int st = check_device(&num_cu);
     if (st != GEMM_BT_OK) return st;
-    const RowPlan p = with_types(
-        x_type, w_type, a.d, [&](auto x, auto w, auto r) { return norm_plan<x(), w(), r(), C>(a.rows, a.d, num_cu); });
+    const RowPlan p = with_types(x_type, w_type, a.d, [&](auto x, auto w, auto r) {
+        if constexpr (C)
+            if (is_code_type(a.y_type)) return norm_codes_plan<x(), w(), r()>(a.rows, a.d, num_cu);
+        return norm_plan<x(), w(), r(), C>(a.rows, a.d, num_cu);
+    });
     const int64_t grid = std::min<int64_t>((a.rows + p.rows_per_block - 1) / p.rows_per_block, 1 << 20);
-    void* args[] = {&a};
+    void* args[] = {&a, &w_type};  // (norm_codes_kernel has both)
     return launch(p.fn, dim3((unsigned)grid), p.threads, args, stream);
 }
 

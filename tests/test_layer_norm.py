@@ -402,3 +402,53 @@ def test_wrapper_refusals(gpu):
                         (ValueError, lambda: gpu.add_layer_norm_backward(x, x, w, m, m, dh=x[:1]))):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [3, 64, 511, 1000, 4096, 6001, 16384, 20000])
+def test_codes_are_those_of_64_bits(gpu, d):
+    """The codes of the exact rows, but for values within fp32's rounding of a step's edge: y / scale is rounded once to
+    fp32, 2^-24 of it, and what 64 bits leave out, d 2^-53 and less of the terms of y, is within 2^-36 of them for
+    d < 2^17.  (x and the residual are multiples of 2^-6 below 2^6, so their sum is exact in fp32.)"""
+    for k, (dt, wt, res, bias) in enumerate(itertools.product(DT, ("own", "f32"), (0, 1), (0, 1))):
+        rows, seed = (5, 600)[k % 2], 77 * d + k
+        say("layer norm codes", rows, d, dt, wt, res, bias, "seed", seed)
+        grid = lambda s, std: ((randn(s, rows, d, std=std) * 64).round() / 64).clamp(-63, 63).to(DT[dt])
+        x, r = grid(seed, 2.0), grid(seed + 1, 3.0) if res else None
+        w_dt = DT[dt] if wt == "own" else torch.float32
+        w = (1 + randn(seed + 2, d, std=0.3)).to(w_dt)
+        b = randn(seed + 3, d, std=0.5).to(w_dt) if bias else None
+        for out in ("e4m3", "i8"):
+            got = gpu.add_layer_norm(x.cuda(), w.cuda(), None if b is None else b.cuda(), residual=None if r is None else r.cuda(),
+                                     eps=EPS, out_dtype=EIGHT[out])
+            y = norm64(x, r, w, b)[0][3]
+            terms = y.abs() + (0 if b is None else 2 * b.double().abs())
+            scale = torch.clamp(y.abs().amax(-1) / QMAX[out], min=2.0 ** -100)
+            assert bool(((got.scale.cpu().double() - scale).abs() <= u * scale + 2.0 ** -36 * terms.amax(-1) / QMAX[out]).all())
+            v, t = y / scale[:, None], 2.0 ** -36 * terms / scale[:, None]
+            top = (v.abs() + t) * (1 + 1e-6)
+            half = torch.full_like(v, 0.5) if out == "i8" else torch.exp2(torch.floor(torch.log2(top.clamp_min(2.0 ** -6))) - 4)
+            off = (got.y.float().double().cpu() - v).abs()
+            assert bool((off <= half + 2 * u * v.abs() + 2 * t).all()), (dt, wt, res, bias, out, float((off - half).max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("d", [6, 40, 2048, 6000, 20000])
+def test_codes_of_extremes(gpu, d, dt):
+    """Squares outside fp32's range, centred values outside it, and rows of one value (y is 0, or b)."""
+    big = torch.finfo(DT[dt]).max
+    x = randn(3, 4, d)
+    x[0] = big
+    x[0, ::2] = -big
+    x[1] *= 2.0 ** -20
+    x[2] = big
+    x[2, 0] = -big
+    x[3] = 2.5
+    x = x.to(DT[dt])
+    w, b = torch.ones(d), randn(4, d, std=0.5)
+    for qt, bias in itertools.product(EIGHT, (None, b)):
+        say("layer norm codes of extremes", d, dt, qt, bias is not None)
+        got = gpu.add_layer_norm(x.cuda(), w.cuda(), None if bias is None else b.cuda(), eps=EPS, out_dtype=EIGHT[qt])
+        (_, _, _, y64), (_, _, t_y) = norm64(x, None, w, bias)
+        check_codes(got.y, got.scale, y64, t_y, qt, (d, dt, qt))
