@@ -6,9 +6,9 @@ As in the rest of the binding, every arithmetic step runs in the library's HIP k
 and the stream.  Leading dimensions count as rows: an input of shape (..., d) is (rows, d), and its results have its
 leading dimensions.  The inputs of the norms and of the quantisations may have evenly spaced rows any number of elements
 apart (a slice of a wider tensor's last dimension, say), and the scales of blocks any strides; other layouts, and every
-strided input of the products, are made contiguous first.  Calls are asynchronous on torch's current stream, or on ``stream`` (a handle or torch's object), on
-which their results are then allocated; inputs that another stream still writes have to be waited for by the caller, as
-with torch's own operators.  The calls stand outside torch's autograd: results never require gradients, whatever the
+strided input of the products, are made contiguous first.  Calls are asynchronous on torch's current stream, or on
+``stream`` (a handle or torch's object), on which their results are then allocated; inputs that another stream still
+writes have to be waited for by the caller, as with torch's own operators.  The calls stand outside torch's autograd: results never require gradients, whatever the
 inputs do, and a training step calls the backward functions itself.
 """
 from __future__ import annotations

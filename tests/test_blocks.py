@@ -422,3 +422,18 @@ def test_wrapper_refusals(gpu):
                         (gpu.GemmBtError, lambda: gpu.block_linear(x[:, :120], w[:, :120], z(4, 1), z(2, 1)))):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.gpu
+def test_codes_without_a_value(gpu):
+    """A NaN among the codes reaches its own row or column of the product, for every kind of result."""
+    for (M, N, K, high), dt in itertools.product(((40, 300, 656, 128), (9, 4200, 640, 1), (600, 520, 640, 128)),
+                                                 (torch.bfloat16, torch.float32)):
+        x, w, sx, sw = operands(gpu, M, N, K, high, 19)
+        xb, wb = x.view(torch.uint8).clone(), w.view(torch.uint8).clone()
+        xb[3, 5], xb[M - 1, K - 1], wb[7, 200] = 0x7F, 0xFF, 0x7F
+        got = gpu.block_linear(xb.view(F8).cuda(), wb.view(F8).cuda(), sx.cuda(), sw.cuda(), out_dtype=dt).cpu()
+        bad = torch.zeros(M, N, dtype=torch.bool)
+        bad[3] = bad[M - 1] = True
+        bad[:, 7] = True
+        assert torch.equal(torch.isnan(got), bad), (M, N, high, dt)
