@@ -771,14 +771,31 @@ struct BlockArgs {
     long long tiles_d, tiles;    // 128 x 128 tiles of x: per row of them, and all
 };
 
+// v / scale of a block's values to fp32's rounding, from the largest magnitude: 448 / amax
+// in two parts.  With 16-bit inputs v 448 / amax often lies on the edge between two
+// codes; rounded to one part first, 1 in 400 of their codes fell on the wrong side.
+struct BlockCode {
+    float high, low;
+    __device__ __forceinline__ float of(float v) const {
+        const float p = v * high;
+        return p + __builtin_fmaf(v, low, __builtin_fmaf(v, high, -p));
+    }
+};
+__device__ __forceinline__ BlockCode block_code(float amax, float* scale) {
+    const RowScale s = row_scale_of(amax, 1.0f, GEMM_BT_FP8_E4M3);
+    *scale = s.scale;
+    // (a scale kept at 2^-100 has a reciprocal of one part)
+    return {s.code, s.scale == 0x1p-100f ? 0.0f : __builtin_fmaf(-s.code, amax, 448.0f) * (s.code * (1.0f / 448.0f))};
+}
+
 // V = x, or x transposed (TRANS), in E4M3 with one scale per 1 x 128 block of V, or
 // per 128 x 128 block (TALL): scale = max(amax / 448, 2^-100), code = RNE(v / scale).
-// Bound by HBM: 8192 x 8192 bf16 37.5 us (5.4 TB/s); 1000 x 2000 f16 transposed 5.6,
-// 128 workgroups of one tile each.  A workgroup takes a 128 x 128 tile of x, thread (tr, tc) = (t / 16,
-// t % 16) its rows 8 tr .. 8 tr + 7 and columns 8 tc .. 8 tc + 7: the 16 lanes of a row
-// of x are one row of the vector unit's data moves, a column's rows lie in 8
-// registers, and the 8 x 8 codes of a thread turn in registers for the transposed
-// result, which leaves through LDS as whole 128-byte rows.  Scales lie block by
+// Bound by HBM: 8192 x 8192 bf16 38 us (5.3 TB/s), transposed 44; 1000 x 2000 f16
+// transposed 5.6, 128 workgroups of one tile each.  A workgroup takes a 128 x 128 tile
+// of x, thread (tr, tc) = (t / 16, t % 16) its rows 8 tr .. 8 tr + 7 and columns 8 tc ..
+// 8 tc + 7: the 16 lanes of a row of x are one row of the vector unit's data moves, a
+// column's rows lie in 8 registers, and the 8 x 8 codes of a thread turn in registers
+// for the transposed result, which leaves through LDS as whole 128-byte rows.  Scales lie block by
 // block, those of consecutive rows of V next to each other, as the product's
 // tiles read them.
 template <int XT, bool TALL, bool TRANS>
@@ -802,7 +819,7 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a)
         for (int r = 0; r < 8; ++r) decode8(raw[r], XT, v[r]);
         auto larger = [](float p, float x) __attribute__((always_inline)) { return MaxBitsOp::join(p, __builtin_fabsf(x)); };
         // what each row (TRANS: each column; TALL: every one) of the thread's part is multiplied by
-        float code[8];
+        BlockCode code[8];
         if constexpr (TALL) {
             float top = 0.0f;
 #pragma unroll
@@ -814,12 +831,13 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a)
             if ((t & 63) == 0) part[wave][0] = top;
             __syncthreads();
             top = MaxBitsOp::join(MaxBitsOp::join(part[0][0], part[1][0]), MaxBitsOp::join(part[2][0], part[3][0]));
-            const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
+            float scale;
+            const BlockCode one = block_code(top, &scale);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) code[r] = s.code;
+            for (int r = 0; r < 8; ++r) code[r] = one;
             if (t == 0) {
                 const long long high = (a.rows + 127) / 128;  // row blocks of x
-                a.scale[TRANS ? ti * a.tiles_d + tj : tj * high + ti] = s.scale;
+                a.scale[TRANS ? ti * a.tiles_d + tj : tj * high + ti] = scale;
             }
         } else if constexpr (!TRANS) {
             float scale[8];
@@ -836,26 +854,25 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a)
                 moved(std::integral_constant<int, 0x124>{});
                 moved(std::integral_constant<int, 0x122>{});
                 moved(std::integral_constant<int, 0x121>{});
-                const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
-                code[r] = s.code;
-                scale[r] = s.scale;
+                code[r] = block_code(top, &scale[r]);
             }
             if (tc == 0)
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
                     if (r < rows) a.scale[tj * a.rows + row0 + r] = scale[r];
         } else {
+            float tops[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 float top = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) top = larger(top, v[r][c]);
                 top = MaxBitsOp::join(top, __shfl_xor(top, 16));
-                code[c] = MaxBitsOp::join(top, __shfl_xor(top, 32));
+                tops[c] = MaxBitsOp::join(top, __shfl_xor(top, 32));
             }
             if ((t & 63) < 16) {
-                *(f32x4*)&part[wave][8 * tc] = f32x4{code[0], code[1], code[2], code[3]};
-                *(f32x4*)&part[wave][8 * tc + 4] = f32x4{code[4], code[5], code[6], code[7]};
+                *(f32x4*)&part[wave][8 * tc] = f32x4{tops[0], tops[1], tops[2], tops[3]};
+                *(f32x4*)&part[wave][8 * tc + 4] = f32x4{tops[4], tops[5], tops[6], tops[7]};
             }
             __syncthreads();
 #pragma unroll
@@ -863,15 +880,15 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a)
                 float top = part[0][8 * tc + c];
 #pragma unroll
                 for (int w = 1; w < 4; ++w) top = MaxBitsOp::join(top, part[w][8 * tc + c]);
-                const RowScale s = row_scale_of(top, 1.0f, GEMM_BT_FP8_E4M3);
-                code[c] = s.code;
-                if (tr == 0 && c < cols) a.scale[ti * a.d + col0 + c] = s.scale;
+                float scale;
+                code[c] = block_code(top, &scale);
+                if (tr == 0 && c < cols) a.scale[ti * a.d + col0 + c] = scale;
             }
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[r][c] *= code[TRANS ? c : r];
+            for (int c = 0; c < 8; ++c) v[r][c] = code[TRANS ? c : r].of(v[r][c]);
         if constexpr (!TRANS) {
 #pragma unroll
             for (int r = 0; r < 8; ++r)

@@ -437,3 +437,18 @@ def test_codes_without_a_value(gpu):
         bad[3] = bad[M - 1] = True
         bad[:, 7] = True
         assert torch.equal(torch.isnan(got), bad), (M, N, high, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(1, 128), (5, 100), (130, 300), (300, 1024)])
+def test_codes_are_rounded_once(gpu, rows, d):
+    """16-bit inputs: the codes are those of v / scale exactly.  v 448 / amax is a quotient of two integers, the divisor
+    below 2^11: on the edge between two codes, or further from it than 2^-17 of itself, so fp32 holds it on the right side."""
+    for dt, high, transpose in itertools.product((torch.bfloat16, torch.float16), (1, 128), (False, True)):
+        say("block codes", rows, d, dt, high, transpose)
+        x = randn(rows + d, rows, d, std=3.0).to(dt)
+        v = (x.t() if transpose else x).double()
+        full = spread(block_max(v, high), *v.shape, high)
+        want = (v * 448 / full).float().to(F8)
+        got = gpu.quantize_blocks(x.cuda(), block=(high, 128), transpose=transpose).q.cpu()[:, :v.shape[1]]
+        assert torch.equal(got.float(), want.float()), (rows, d, dt, high, transpose)
