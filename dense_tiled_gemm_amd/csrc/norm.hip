@@ -535,9 +535,9 @@ __device__ __forceinline__ void row_joins(double (&v)[N], double (*part)[16]) {
 struct RowStats {
     double mean, rstd;
 };
-__device__ __forceinline__ RowStats row_stats(const double (&sums)[2], float m0, const NormArgs& a, long long row, bool keep) {
-    const double off = sums[0] / (double)a.d;
-    const double var = sums[1] / (double)a.d - off * off;
+__device__ __forceinline__ RowStats row_stats(const double (&sums)[2], float m0, double per, const NormArgs& a, long long row, bool keep) {
+    const double off = sums[0] * per;  // (per: 1 / d)
+    const double var = sums[1] * per - off * off;
     // (a NaN stays one)
     const RowStats s = {m0 + off, 1.0 / __builtin_sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps)};
     if (keep) {
@@ -549,10 +549,22 @@ __device__ __forceinline__ RowStats row_stats(const double (&sums)[2], float m0,
 // What a row's values are multiplied by for their codes, from the largest magnitude;
 // the scale as row_scale_of has it.
 __device__ __forceinline__ double row_code(double amax, const NormArgs& a, long long row, bool keep) {
-    const double q = a.y_type == GEMM_BT_FP8_E4M3 ? 448.0 : 127.0, s = amax / q;
+    const bool e4m3 = a.y_type == GEMM_BT_FP8_E4M3;
+    const double q = e4m3 ? 448.0 : 127.0, s = amax * (e4m3 ? 1.0 / 448.0 : 1.0 / 127.0);
     const bool fine = as_u32((float)amax) < 0x7F800000u, tiny = !(s >= 0x1p-100);
     if (keep) a.scale[row] = !fine ? as_f32(0x7FC00000u) : tiny ? 0x1p-100f : (float)s;
     return !fine ? (double)as_f32(0x7FC00000u) : tiny ? 0x1p100 : q / amax;
+}
+// The largest magnitude of 8 values, a NaN above all.
+__device__ __forceinline__ double largest8(const double (&y)[8]) {
+    double amax = 0.0;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        amax = __builtin_fmax(amax, __builtin_fabs(y[e]));
+        nan |= y[e] != y[e];
+    }
+    return nan ? __builtin_nan("") : amax;
 }
 // y = (h - mean) rstd w + b of 8 elements.  Past the row's end w and b are 0, and so is
 // y, or the row's mean is not finite and all of it NaN.
@@ -573,10 +585,11 @@ __device__ __forceinline__ void store_codes64(const NormArgs& a, size_t i, int n
 // row's factors do not cancel in y / amax as they do for the other norm, so
 // everything from the centred values to y / scale is kept in fp64 (the vector unit
 // needs as many instructions as in fp32 and the conversions) and rounded to fp32 once, to
-// the code once more.  Bound by the vector unit: 8192 x 8192 bf16 with residual to E4M3
-// 132 us (3.6 TB/s; 150 with y made twice, in fp32 about as long as the other norm's 83),
-// 8192 x 4096 60, 16384 x 1024 29; one row of 4096 11 us, bound by the call.  Rows as in
-// norm_kernel.
+// the code once more.  Bound by that work between a row's loads and its stores, of
+// which the two workgroups that fit a CU cover a part: 8192 x 8192 bf16 with residual to
+// E4M3 128 us (3.7 TB/s; 150 with y made twice; one chunk per thread 185; the other
+// norm, in fp32, 83), 8192 x 4096 59, 16384 x 1024 28; one row of 4096 11 us, bound by
+// the call.  Rows as in norm_kernel.
 template <int XT, int U, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const NormArgs a, int w_type) {
     constexpr bool WHOLE = !RAGGED && !WAVE;  // as in norm_kernel
@@ -588,6 +601,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const Nor
     const int T = WAVE ? 64 : blockDim.x, RB = WAVE ? blockDim.x >> 6 : 1;
     const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int d = a.d;
+    const double per = 1.0 / (double)d;
     int flip = 0;
     for (long long row = (long long)blockIdx.x * RB + (WAVE ? threadIdx.x >> 6 : 0); row < a.rows;
          row += (long long)gridDim.x * RB) {
@@ -640,7 +654,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const Nor
             }
         });
         row_joins<Sum64Op, WAVE>(sums, part64 + 2 * flip);
-        const RowStats s = row_stats(sums, m0, a, row, t == 0);
+        const RowStats s = row_stats(sums, m0, per, a, row, t == 0);
         double y[HOLD ? U : 1][8], amax[1] = {0.0};
         auto load_y = [&](int i, const float (&h)[8], double (&y)[8]) __attribute__((always_inline)) {
             float w[8], b[8];
@@ -657,8 +671,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const Nor
             const int i = (u * T + renew(t)) * 8;
             if (i < d) {
                 load_y(i, h[u], y[v]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax[0] = MaxBits64Op::join(amax[0], __builtin_fabs(y[v][e]));
+                amax[0] = MaxBits64Op::join(amax[0], largest8(y[v]));
             }
         });
         row_joins<MaxBits64Op, WAVE>(amax, part64 + 4 + flip);
@@ -682,6 +695,7 @@ __global__ __launch_bounds__(1024) void norm_codes_long_kernel(const NormArgs a)
     __shared__ float part[4][16];
     __shared__ double part64[6][16];
     const int t = threadIdx.x;
+    const double per = 1.0 / (double)a.d;
     int flip = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         // f(first element, elements, their h)
@@ -719,7 +733,7 @@ __global__ __launch_bounds__(1024) void norm_codes_long_kernel(const NormArgs a)
             }
         });
         row_joins<Sum64Op, false>(sums, part64 + 2 * flip);
-        const RowStats s = row_stats(sums, m0, a, row, renew(t) == 0);
+        const RowStats s = row_stats(sums, m0, per, a, row, renew(t) == 0);
         auto load_y = [&](int i, int n, const float (&h)[8], double (&y)[8]) __attribute__((always_inline)) {
             float w[8], b[8];
             decode8(load_raw8(a.weight, WT, (size_t)i, n), WT, w);
@@ -734,8 +748,7 @@ __global__ __launch_bounds__(1024) void norm_codes_long_kernel(const NormArgs a)
         each8([&](int i, int n, float (&h)[8]) __attribute__((always_inline)) {
             double y[8];
             load_y(i, n, h, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax[0] = MaxBits64Op::join(amax[0], __builtin_fabs(y[e]));
+            amax[0] = MaxBits64Op::join(amax[0], largest8(y));
         });
         row_joins<MaxBits64Op, false>(amax, part64 + 4 + flip);
         const double code = row_code(amax[0], a, row, renew(t) == 0);
