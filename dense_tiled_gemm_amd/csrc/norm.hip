@@ -572,10 +572,18 @@ __device__ __forceinline__ void normed8(const float (&h)[8], const RowStats& s, 
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __builtin_fma(((double)h[e] - s.mean) * s.rstd, (double)w[e], (double)b[e]);
 }
+// v in fp32, cut toward zero, its last bit set where that left anything out: what is then
+// rounded to fewer bits comes out as if it had been rounded once (v is 0 or far above
+// fp32's smallest normal, or its code 0 either way).
+__device__ __forceinline__ float to_odd(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const u32 low = (u32)b, left = (low & 0x1FFFFFFFu) + 0x1FFFFFFFu;
+    return (float)__builtin_bit_cast(double, (b >> 32) << 32 | ((low | left) & 0xE0000000u));
+}
 __device__ __forceinline__ void store_codes64(const NormArgs& a, size_t i, int n, const double (&y)[8], double code) {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)(y[e] * code);
+    for (int e = 0; e < 8; ++e) v[e] = to_odd(y[e] * code);
     store_codes(a.y, a.y_type, i, n, v);
 }
 
@@ -584,11 +592,11 @@ __device__ __forceinline__ void store_codes64(const NormArgs& a, size_t i, int n
 // whole step, 1/16 of an E4M3 value, about one value in 2^21.  With a bias the
 // row's factors do not cancel in y / amax as they do for the other norm, so
 // everything from the centred values to y / scale is kept in fp64 (the vector unit
-// needs as many instructions as in fp32 and the conversions) and rounded to fp32 once, to
-// the code once more.  Bound by that work between a row's loads and its stores, of
+// needs as many instructions as in fp32 and the conversions) and the codes are those of
+// one rounding.  Bound by that work between a row's loads and its stores, of
 // which the two workgroups that fit a CU cover a part: 8192 x 8192 bf16 with residual to
-// E4M3 128 us (3.7 TB/s; 150 with y made twice; one chunk per thread 185; the other
-// norm, in fp32, 83), 8192 x 4096 59, 16384 x 1024 28; one row of 4096 11 us, bound by
+// E4M3 131 us (3.6 TB/s; 150 with y made twice; one chunk per thread 185; the other
+// norm, in fp32, 83), 8192 x 4096 60, 16384 x 1024 29; one row of 4096 11 us, bound by
 // the call.  Rows as in norm_kernel.
 template <int XT, int U, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const NormArgs a, int w_type) {
@@ -784,14 +792,21 @@ struct BlockArgs {
     long long tiles_d, tiles;    // 128 x 128 tiles of x: per row of them, and all
 };
 
-// v / scale of a block's values to fp32's rounding, from the largest magnitude: 448 / amax
-// in two parts.  With 16-bit inputs v 448 / amax often lies on the edge between two
-// codes; rounded to one part first, 1 in 400 of their codes fell on the wrong side.
+// v / scale of a block's values, from the largest magnitude: 448 / amax in two parts.
+// With 16-bit inputs v 448 / amax often lies on the edge between two codes, else well
+// off it; with 448 / amax in one part 1 in 400 of their codes fell on the wrong side.  Of
+// fp32 inputs it may lie anywhere: ODD sets the last bit of a rounded value, so that the
+// code comes out as if it had been rounded once.
 struct BlockCode {
     float high, low;
+    template <bool ODD>
     __device__ __forceinline__ float of(float v) const {
-        const float p = v * high;
-        return p + __builtin_fmaf(v, low, __builtin_fmaf(v, high, -p));
+#pragma clang fp contract(off)  // p is the rounded product in f and in what is left
+        const float p = v * high, q = __builtin_fmaf(v, low, __builtin_fmaf(v, high, -p)), f = p + q;
+        if constexpr (!ODD) return f;
+        const float left = q - (f - p);
+        const u32 b = as_u32(f);  // (toward what is left: up in magnitude where the signs agree)
+        return as_f32(left == 0.0f || (b & 1) ? b : b + (u32)(((int)(as_u32(left) ^ b) >> 31) | 1));
     }
 };
 __device__ __forceinline__ BlockCode block_code(float amax, float* scale) {
@@ -901,7 +916,7 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const BlockArgs a)
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[r][c] = code[TRANS ? c : r].of(v[r][c]);
+            for (int c = 0; c < 8; ++c) v[r][c] = code[TRANS ? c : r].template of<XT == GEMM_BT_F32>(v[r][c]);
         if constexpr (!TRANS) {
 #pragma unroll
             for (int r = 0; r < 8; ++r)

@@ -452,3 +452,25 @@ def test_codes_are_rounded_once(gpu, rows, d):
         want = (v * 448 / full).float().to(F8)
         got = gpu.quantize_blocks(x.cuda(), block=(high, 128), transpose=transpose).q.cpu()[:, :v.shape[1]]
         assert torch.equal(got.float(), want.float()), (rows, d, dt, high, transpose)
+
+
+def codes64(v):
+    """v in E4M3, to nearest even, and how far v is from the edge between two codes, in steps."""
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
+    t = v / step
+    return torch.round(t) * step, (t - t.floor() - 0.5).abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(130, 300), (1000, 4096)])
+def test_codes_of_fp32_are_rounded_once(gpu, rows, d):
+    """fp32 inputs: the codes are those of v 448 / amax unless it lies within 2^-40 of a code's edge.  What is left out of
+    448 / amax and of the product in two parts is below 2^-45 of it; a rounding to fp32 before would change 1 in 3e6."""
+    for high, transpose in itertools.product((1, 128), (False, True)):
+        say("block codes fp32", rows, d, high, transpose)
+        x = randn(rows + d, rows, d, std=3.0)
+        v = (x.t() if transpose else x).double()
+        full = spread(block_max(v, high), *v.shape, high)
+        want, edge = codes64(v * 448 / full)
+        got = gpu.quantize_blocks(x.cuda(), block=(high, 128), transpose=transpose).q.cpu()[:, :v.shape[1]].float().double()
+        assert bool(((got == want) | (edge < 2.0 ** -36)).all()), (rows, d, high, transpose, int((got != want).sum()))

@@ -452,3 +452,22 @@ def test_codes_of_extremes(gpu, d, dt):
         got = gpu.add_layer_norm(x.cuda(), w.cuda(), None if bias is None else b.cuda(), eps=EPS, out_dtype=EIGHT[qt])
         (_, _, _, y64), (_, _, t_y) = norm64(x, None, w, bias)
         check_codes(got.y, got.scale, y64, t_y, qt, (d, dt, qt))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [1000, 4096, 20000])
+def test_codes_are_rounded_once(gpu, d):
+    """Four million values: the codes are those of y / scale unless it lies within 64 bits' errors of a step's edge: d 2^-53
+    of the terms of y, which are below 4 times the row's largest value, and so below 2^-36 448 in units of the scale.  A
+    rounding to fp32 before the codes would change 1 in 3e6 of them, one of y as many again."""
+    rows = 4_000_000 // d
+    say("layer norm codes, once", rows, d)
+    x, w, b = randn(d, rows, d, std=2.0), 1 + randn(d + 1, d, std=0.3), randn(d + 2, d, std=0.5)
+    y = norm64(x, None, w, b)[0][3]
+    v = y * QMAX["e4m3"] / y.abs().amax(-1, keepdim=True)
+    got = gpu.add_layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=EPS, out_dtype=EIGHT["e4m3"]).y.float().double().cpu()
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
+    t = v / step
+    edge = (t - t.floor() - 0.5).abs()
+    bad = (got != torch.round(t) * step) & (edge * step > 2.0 ** -36 * 448)
+    assert not bool(bad.any()), (d, int(bad.sum()))
