@@ -184,7 +184,8 @@ __device__ __forceinline__ float rstd_of(float ss, int d, float eps, float (*par
         float amax = 0.0f;
         each([&](float v) __attribute__((always_inline)) { amax = MaxBitsOp::join(amax, __builtin_fabsf(v)); });
         amax = row_join<MaxBitsOp, WAVE>(amax, part[flip]);
-        if (amax > 0.0f && amax < __builtin_inff()) {
+        if (amax == 0.0f) return 1.0f / __builtin_sqrtf(eps);  // (of layer norm, whose ss may hold what its mean left out)
+        if (amax < __builtin_inff()) {
             const float s = as_f32((254u - min(as_u32(amax) >> 23, 253u)) << 23);
             float sq = 0.0f;
             each([&](float v) __attribute__((always_inline)) { sq = __builtin_fmaf(v * s, v * s, sq); });
@@ -312,7 +313,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
             row_sums<WAVE, 2>(sums, part + flip, 12);
             const float off = sums[0] / (float)d;
             if (a.mean && t == 0) a.mean[row] = m0 + off;
-            ss = __builtin_fmaxf(__builtin_fmaf(-off * off, (float)d, sums[1]), 0.0f);
+            // squares outside fp32's range stay infinite, for rstd_of, which takes those of h - m0 - off; a NaN stays one
+            ss = sums[1] < __builtin_inff() ? __builtin_fmaxf(__builtin_fmaf(-off * off, (float)d, sums[1]), 0.0f)
+                                            : sums[1] + (off - off);
             static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
                 constexpr int u = decltype(uc)::value;
                 const int n = d - (u * T + renew(t)) * 8;
