@@ -215,8 +215,9 @@ struct NormArgs {
 
 __host__ __device__ inline bool is_code_type(int t) { return t == GEMM_BT_FP8_E4M3 || t == GEMM_BT_INT8; }
 
-// The mean of a row of d values whose sum in fp32 is `sum`.  Where that left
-// fp32's range the values are summed once more, 2^-27 of each (d <= 2^26).
+// The mean of a row of d values whose sum in fp32 is `sum`.  Where that, or a part of
+// it on the way, left fp32's range the values are summed once more, 2^-27 of each
+// (d <= 2^26).  NaN where a value is infinite.
 template <bool WAVE, class Each>
 __device__ __forceinline__ float mean_of(float sum, int d, float* part, Each&& each) {
     float mean = sum / (float)d;
@@ -224,6 +225,7 @@ __device__ __forceinline__ float mean_of(float sum, int d, float* part, Each&& e
         float s = 0.0f;
         each([&](float v) __attribute__((always_inline)) { s = __builtin_fmaf(v, 0x1p-27f, s); });
         mean = row_join<SumOp, WAVE>(s, part) / (float)d * 0x1p27f;
+        mean += mean - mean;
     }
     return mean;
 }
@@ -311,7 +313,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs 
                 }
             });
             row_sums<WAVE, 2>(sums, part + flip, 12);
-            const float off = sums[0] / (float)d;
+            const float off = mean_of<WAVE>(sums[0], d, part[10 + flip], each);
             if (a.mean && t == 0) a.mean[row] = m0 + off;
             // squares outside fp32's range stay infinite, for rstd_of, which takes those of h - m0 - off; a NaN stays one
             ss = sums[1] < __builtin_inff() ? __builtin_fmaxf(__builtin_fmaf(-off * off, (float)d, sums[1]), 0.0f)
@@ -438,7 +440,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
             m0 = mean_of<false>(row_join<SumOp, false>(sum, part[8 + flip]), a.d, part[10 + flip], each);
             sum = 0.0f;
             each([&](float v) __attribute__((always_inline)) { sum += v; });
-            off = row_join<SumOp, false>(sum, part[12 + flip]) / (float)a.d;
+            off = mean_of<false>(row_join<SumOp, false>(sum, part[12 + flip]), a.d, part[10 + flip], each);
             if (a.mean && t == 0) a.mean[row] = m0 + off;
         }
         if (a.weight) {

@@ -73,3 +73,38 @@ def test_nearly_equal_large_entries(gpu, d, dt):
         x[::2] = (big * 2.0 ** power)[::2]
         say("layer norm, nearly equal large entries", rows, d, dt, "2 **", power, "seed", seed)
         check(gpu, x.to(DT[dt]), None, seed, (d, dt, power))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_sums_outside_the_range(gpu, d, dt):
+    """Runs of large entries of one sign: what a thread, a wave or a workgroup sums on the way is infinite, or infinities of
+    both signs meet, in the first mean's sum or in that of what it leaves."""
+    size = (1 + 0.1 * randn(d, 6, d).abs()).clamp(max=1.4) * 2.0 ** 125
+    sign = torch.ones(6, d)
+    sign[0, d // 2:] = -1          # halves
+    sign[1, d // 4:] = -1 / 3      # a quarter against the rest
+    sign[2, :] = -1                # one sign alone
+    sign[3] = 1 - 2 * (torch.arange(d) // 8 % 2)    # a thread's entries of one sign
+    sign[4] = 1 - 2 * (torch.arange(d) // 512 % 2)  # a wave's
+    sign[5, d // 2:] = 2.0 ** -60
+    for rows in (6, 600):
+        x = (size * sign).repeat(rows // 6, 1).to(DT[dt])
+        for r in (None, (randn(d + 1, rows, d) * 2.0 ** 120).to(DT[dt])):
+            say("layer norm, sums outside the range", rows, d, dt, r is not None)
+            check(gpu, x, r, d, (d, dt, rows))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [40, 2048, 4096, 20000])
+def test_centred_values_outside_the_range(gpu, d):
+    """A finite row whose h - mean is infinite somewhere has no value: y, mean and rstd are NaN, and no other row's."""
+    big = torch.finfo(torch.float32).max
+    x = randn(d, 4, d)
+    x[1], x[1, 3] = big, -big
+    x[2], x[2, d - 1] = -big, big
+    got = gpu.add_layer_norm(x.cuda(), torch.ones(d, device="cuda"), eps=EPS, save_stats=True)
+    bad = torch.tensor([False, True, True, False])
+    for t in (got.y.cpu(), got.mean.cpu()[:, None], got.rstd.cpu()[:, None]):
+        assert torch.equal(torch.isnan(t), bad[:, None].expand_as(t)), d
