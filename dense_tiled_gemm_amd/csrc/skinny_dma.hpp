@@ -293,8 +293,9 @@ __device__ __forceinline__ void skinny_body(const u16* __restrict__ A, const u16
     int cs = 0, ls = STAGES - 1;
     for (int kt = 0; kt < nk; ++kt) {
         wait_vmcnt<PEND + (BLOCKS ? 2 * (STAGES - 2) : 0)>();
-        // two stages: the one refilled next is the one just read
-        if constexpr (STAGES == 2) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        // the stage refilled next is the one that the step before this one read, whatever their number: its reads have
+        // returned (each is used in its own step, so this waits for nothing, but no order of instructions is relied on)
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         barrier_no_fence();
         issue(ls, kt + STAGES - 1);
         compute(cs);
