@@ -648,9 +648,9 @@ def _block_scale(t, rows, blocks, what):
         raise ValueError("%s must be a float32 tensor of %d rows of %d blocks, got %s %s" % (what, rows, blocks, t.dtype, tuple(t.shape)))
     if t.dim() != 2:  # (leading dimensions as one: a view where they are evenly spaced)
         t = t.reshape(rows, blocks)
-    row, block = t.stride()
-    if row >= 1 << 20 or block >= 1 << 26:
-        t = t.t().contiguous().t()
+    row, block = (0 if n <= 1 else s for n, s in zip(t.shape, t.stride()))  # (of one entry a stride is never taken)
+    if row >= 1 << 20 or block >= 1 << 26:  # the kernels' limits: consecutive rows next to each other, or consecutive blocks
+        t = t.t().contiguous().t() if rows < 1 << 26 else t.contiguous()
         row, block = t.stride()
     return t, row, block
 
