@@ -243,10 +243,10 @@ __device__ __forceinline__ float mean_of(float sum, int d, float* part, Each&& e
 // the mean of h - m0, which is what the rounding of m0 left out, comes with the
 // squares of h - m0, d off^2 above those of h - m0 - off.  So the centred values do
 // not depend on how well the first sum came out, and rows of nearly equal entries
-// keep what distinguishes them.  Bound by HBM: 8192 x 8192 bf16 with residual 98 us
-// (5.5 TB/s), 8192 x 4096 49, 16384 x 1024 24.  Two joins over the row's threads where
+// keep what distinguishes them.  Bound by HBM: 8192 x 8192 bf16 with residual 96 us
+// (5.6 TB/s), 8192 x 4096 49, 16384 x 1024 23.  Two joins over the row's threads where
 // the other norm has one: with shuffles and three barriers they cost 113 us, with
-// two 108, with moves in the vector unit (row_sums) 98.
+// two 108, with moves in the vector unit (row_sums) 96.
 template <int XT, int WT, int U, bool WAVE, bool RAGGED, bool CENTER = false>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(const NormArgs a) {
     constexpr bool WHOLE = !RAGGED && !WAVE;  // every chunk is 8 elements of the row (rows below 8 have a wave each)
@@ -600,9 +600,10 @@ __device__ __forceinline__ void store_codes64(const NormArgs& a, size_t i, int n
 // needs as many instructions as in fp32 and the conversions) and the codes are those of
 // one rounding.  Bound by that work between a row's loads and its stores, of
 // which the two workgroups that fit a CU cover a part: 8192 x 8192 bf16 with residual to
-// E4M3 131 us (3.6 TB/s; 150 with y made twice; one chunk per thread 185; the other
-// norm, in fp32, 83), 8192 x 4096 60, 16384 x 1024 29; one row of 4096 11 us, bound by
-// the call.  Rows as in norm_kernel.
+// E4M3 129 us (3.6 TB/s; 150 with y made twice; one chunk per thread 185; the other
+// norm, in fp32, 83), 8192 x 4096 61, 16384 x 1024 29; one row of 4096 11 to 14 us, bound by
+// the call.  Rows that end inside a chunk cost most: 8191 x 4097 128 us (to 16 bits 68), x,
+// the residual, w and b each moved into place.  Rows as in norm_kernel.
 template <int XT, int U, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_codes_kernel(const NormArgs a, int w_type) {
     constexpr bool WHOLE = !RAGGED && !WAVE;  // as in norm_kernel
@@ -979,8 +980,9 @@ struct NormBackArgs {
 // workgroup leaves one row of partial sums.  AHEAD: the next row is fetched
 // while this one is worked on, and the weight stays in registers; without it
 // (rows that fill the registers) both are read when they are needed.
-// CENTER: layer norm (8192 x 4096 bf16 with dh and db 50 us in all, 5.4 TB/s; joins by
-// shuffles 53).  xhat = (h - mean) rstd, dx = rstd (g - mean(g) - xhat mean(g
+// CENTER: layer norm (8192 x 4096 bf16 with dh and db 57 us in all: this kernel 49, 5.4
+// TB/s, the fold of dw and db 7; with a dh that stays in the caches 50, by shuffles
+// 53).  xhat = (h - mean) rstd, dx = rstd (g - mean(g) - xhat mean(g
 // xhat)) + dh, and db = sum over rows of dy, summed and left like dw.
 template <int XT, int WT, int U, bool WAVE, bool AHEAD, int MOST, bool RAGGED, bool CENTER = false>
 __global__ __launch_bounds__(MOST) void norm_back_kernel(const NormBackArgs a) {

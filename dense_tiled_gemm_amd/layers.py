@@ -8,8 +8,8 @@ leading dimensions.  The inputs of the norms and of the quantisations may have e
 apart (a slice of a wider tensor's last dimension, say), and the scales of blocks any strides; other layouts, and every
 strided input of the products, are made contiguous first.  Calls are asynchronous on torch's current stream, or on
 ``stream`` (a handle or torch's object), on which their results are then allocated; inputs that another stream still
-writes have to be waited for by the caller, as with torch's own operators.  The calls stand outside torch's autograd: results never require gradients, whatever the
-inputs do, and a training step calls the backward functions itself.
+writes have to be waited for by the caller, as with torch's own operators.  The calls stand outside torch's autograd:
+results never require gradients, whatever the inputs do, and a training step calls the backward functions itself.
 """
 from __future__ import annotations
 
@@ -661,7 +661,10 @@ def block_linear(x, weight, x_scale, weight_scale, bias=None, activation="none",
 
     x (..., K) and weight (N, K): float8_e4m3fn, K % 16 == 0; x_scale (..., ceil(K / 128)), one per 1 x 128 block of x;
     weight_scale (ceil(N / 128), ceil(K / 128)), one per 128 x 128 block, or (N, ceil(K / 128)), one per 1 x 128 block, as
-    quantize_blocks makes them; matrices that it transposed go in with the zeros it filled their rows with.  bias, activation, residual, ``out_dtype``, ``save_preact`` (z in bfloat16) and ``out`` as for linear.
+    quantize_blocks makes them.  Matrices that it transposed go in with the zeros it filled their rows with; the other operand,
+    where it was not transposed, is then filled with zeros up to the same K by the caller (dy for an input's gradient, where
+    the weight has a number of rows that is not a multiple of 16).  bias, activation, residual, ``out_dtype``,
+    ``save_preact`` (z in bfloat16) and ``out`` as for linear.
     """
     if stream is not None:
         return _on_stream(stream, x, lambda: block_linear(x, weight, x_scale, weight_scale, bias, activation, residual, out_dtype,

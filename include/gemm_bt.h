@@ -331,7 +331,10 @@ int gemm_bt_rms_norm_backward_workspace(int64_t rows, int64_t d, size_t* bytes);
  * As gemm_bt_rms_norm in everything else: types, strides, 8-bit y with one
  * scale per row, what may be what.  The squares are those of h - mean (never
  * mean(h^2) - mean^2), and the mean's own rounding is taken out of h - mean.
- * A row with an infinity or a NaN, or whose h - mean leaves fp32's range, is NaN.
+ * Rows whose sums or squares leave fp32's range are summed once more, scaled.
+ * A row with an infinity or a NaN has y, mean and rstd NaN, and so has one whose
+ * h - mean leaves fp32's range (not in 8 bits: there it is held in 64 bits, and
+ * the row has its values).
  *   bias   d elements of w_dtype, or NULL
  *   mean   rows fp32, or NULL: receives mean for the backward pass
  * A row of no elements has mean 0.
@@ -345,7 +348,9 @@ int gemm_bt_layer_norm(const void* x, int64_t ldx, const void* residual, int64_t
  *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dh
  *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy
  * As gemm_bt_rms_norm_backward in everything else.
- *   mean, rstd  as gemm_bt_layer_norm left them
+ *   mean, rstd  as gemm_bt_layer_norm left them.  mean is rounded to fp32, which
+ *               xhat does not make up for: it shows where a row's entries differ
+ *               by little more than that
  *   dbias       d elements of w_dtype, or NULL: not wanted
  *   workspace   at least gemm_bt_layer_norm_backward_workspace bytes
  */
@@ -435,8 +440,9 @@ int gemm_bt_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int activa
  * x d) or, with transpose = 1, x transposed (d x rows); a block is 1 x 128 entries of
  * V (block_rows 1) or 128 x 128 (block_rows 128), the last ones of a row or column
  * shorter.  With amax a block's largest |v|, scale = max(amax / 448, 2^-100) and q
- * holds v / scale rounded to nearest even; a block with an infinity or a NaN gets
- * the scale NaN (its codes then hold no value).
+ * holds v / scale rounded to nearest even (v 448 / amax, not v over the scale as it
+ * is rounded to fp32: they differ where v lies half-way between two codes); a block
+ * with an infinity or a NaN gets the scale NaN (its codes then hold no value).
  *   x      as for gemm_bt_quantize_rows
  *   q      q_dtype GEMM_BT_FP8_E4M3 (else UNSUPPORTED): V row-major, dense; with
  *          transpose the rows are rows rounded up to a multiple of 16 long, the
@@ -455,10 +461,11 @@ int gemm_bt_quantize_blocks(const void* x, int64_t ldx, void* q, float* scale, i
  * row j) or of 128 x 128 (128: that of row j / 128).  A scale lies at
  * row * row_stride + b * block_stride floats: strides (1, R) as gemm_bt_quantize_blocks
  * leaves them (the fastest), or others (0 .. 2^20 - 1 and 0 .. 2^26 - 1, else UNSUPPORTED).
- * A block's sum and everything after it is held in fp32; sa * sb is rounded to fp32
- * first where B has blocks of 128 x 128, so it must not leave fp32's range.  For results of
- * 16 bits the matrix units' instructions for 8-bit floats multiply, which cut each product to
- * a multiple of 2^-13 of the largest of its group of 8 consecutive k; for GEMM_BT_F32
+ * A block's sum and everything after it is held in fp32; before the sum over blocks
+ * either sa * sb (tiles, where B has blocks of 128 x 128) or a block's sum times sa (else)
+ * is rounded to fp32, so neither must leave fp32's range.  For results of 16 bits the
+ * matrix units' instructions for 8-bit floats multiply, which cut each product to a
+ * multiple of 2^-13 of the largest of its group of 8 consecutive k; for GEMM_BT_F32
  * the codes are widened to 16 bits (exactly) and every sum is a sum of fp32 roundings, at
  * about half the rate.
  *   in_dtype   GEMM_BT_FP8_E4M3 (else UNSUPPORTED); K % 16 == 0, A and B 16-byte
